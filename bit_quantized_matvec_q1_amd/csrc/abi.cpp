@@ -111,6 +111,12 @@ lb_status check_product(const char *fn, int fmt, const void *W, int64_t N, int64
 
 } // namespace
 
+namespace lb {
+lb_status abi_fail(lb_status st, const char *fn, const char *what) { return fail(st, fn, what); }
+lb_status abi_hip(const char *fn, hipError_t e) { return e == hipSuccess ? LB_OK : hip_fail(fn, e); }
+lb_status abi_check_device(const char *fn) { return check_device(fn); }
+} // namespace lb
+
 extern "C" {
 
 const char *lowbit_status_str(lb_status st)

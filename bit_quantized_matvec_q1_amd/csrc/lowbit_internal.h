@@ -79,6 +79,11 @@ template <int L> inline __device__ float group_sum_f(float v)
     return v;
 }
 
+// --- the ABI layer's errors and device check (abi.cpp), for its other translation units
+lb_status abi_fail(lb_status st, const char *fn, const char *what);
+lb_status abi_hip(const char *fn, hipError_t e); // LB_OK for hipSuccess
+lb_status abi_check_device(const char *fn);
+
 // --- launchers (each validates nothing: the ABI layer has done it) ------------------------------
 
 hipError_t launch_quantize_q8_0(const float *x, int64_t M, int64_t K, int8_t *xq, uint16_t *xs, hipStream_t s);

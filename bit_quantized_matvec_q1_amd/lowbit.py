@@ -14,6 +14,7 @@ import torch
 
 Q1_0, Q2_0_G64, TERNARY_PLANAR, Q8_0, TERNARY_B3 = 1, 2, 3, 4, 5
 ACT_Q8_0, ACT_I8_ROW, ACT_F32_Q8_0 = 1, 2, 3
+F32, BF16, F16 = 0, 1, 2
 LB_OK, LB_EINVAL, LB_ESHAPE, LB_EALIGN, LB_EUNSUPPORTED, LB_EDEVICE, LB_ENOMEM = range(7)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblowbit.so")
@@ -44,6 +45,15 @@ SIGNATURES = {
     "lowbit_batch_launches": (ctypes.c_int32, [_P]),
     "lowbit_batch_destroy": (None, [_P]),
     "lowbit_matvec_batched_static": (_I, [_P, ctypes.c_int32, _P]),
+    "lowbit_kv_cache_bytes": (_I64, [_I64, _I64, _I64, _I64]),
+    "lowbit_kv_plan": (_I, [_P, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P]),
+    "lowbit_kv_release": (_I, [_P, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _P, _P]),
+    "lowbit_kv_append": (_I, [_I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P]),
+    "lowbit_kv_read": (_I, [_I, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P]),
+    "lowbit_kv_attention_workspace": (_I64, [_I64] * 8),
+    "lowbit_kv_attention": (_I, [_I, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _F, _I64,
+                                 _P, _I64, _P, _I64, _P]),
+    "lowbit_logits_process": (_I, [_I, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P]),
     "lowbit_read_probe": (_I, [_P, _I64, _P, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
@@ -225,6 +235,209 @@ def dense_head_matvec_i8(W, row_scale, N, K, x, y, stream=None):
 def lowbit_read_probe(buf, nbytes, sink, stream=None):
     pb, ps = _args((buf, "buf", nbytes), (sink, "sink", 65536, (torch.int32, torch.uint32)))
     _check(lib.lowbit_read_probe(pb, nbytes, ps, _stream(stream, buf)), "lowbit_read_probe")
+
+
+# ---- serving: block tables, the 4-bit cache, attention over it, logits ----------------------------
+
+_DTYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+_I32 = (torch.int32,)
+
+
+def _serve(fn, stream, tensors, call):
+    """call(stream) on the tensors' device, which all of them have to share, whatever the current device is."""
+    on = [t for t in tensors if isinstance(t, torch.Tensor)]
+    for t in on:
+        if not t.is_cuda:
+            raise ValueError(f"device tensor required, got one on {t.device}")
+        if t.device != on[0].device:
+            raise ValueError(f"tensors on {on[0].device} and {t.device}: one device required")
+    if not on or on[0].device.index == torch.cuda.current_device():
+        _check(call(_stream(stream, *on)), fn)
+        return
+    with torch.cuda.device(on[0].device):
+        _check(call(_stream(stream, *on)), fn)
+
+
+def _row_arg(t, name, dtype, T, heads, D, stride):
+    """Rows [T][heads][D]: (address, token stride).  A tensor may be a part of wider rows (any token stride, the
+    row itself dense); an address takes `stride`, dense rows by default."""
+    width = max(int(heads), 0) * max(int(D), 0)
+    if t is None or isinstance(t, int):
+        return t, width if stride is None else int(stride)
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a torch tensor, an int address or None is required")
+    if dtype in _DTYPES and t.dtype != _DTYPES[dtype]:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {_DTYPES[dtype]}")
+    if T <= 0:
+        return t.data_ptr(), width if stride is None else int(stride)
+    if t.dim() == 2 and t.shape[1] == width:
+        dense = t.stride(1) == 1 or width == 1
+    elif t.dim() == 3 and tuple(t.shape[1:]) == (heads, D):
+        dense = (t.stride(2) == 1 or D == 1) and (t.stride(1) == D or heads == 1)
+    else:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {heads}, {D}] or [T, {width}]")
+    if t.shape[0] < T:
+        raise ValueError(f"{name}: needs at least {T} rows, has {t.shape[0]}")
+    step = t.stride(0) if T > 1 else max(t.stride(0), width)
+    if not dense or step < width:
+        raise ValueError(f"{name}: a row's elements have to be dense, and rows apart")
+    if stride is not None and int(stride) != step:
+        raise ValueError(f"{name}: stride {stride} given, the tensor's is {step}")
+    return t.data_ptr(), step
+
+
+def _flat(*specs):
+    """Addresses of dense arguments (t, name, count[, dtypes]) after the checks of sizes, types and layout (the
+    device is checked for all of a call's tensors together)."""
+    out = []
+    for t, name, count, *types in specs:
+        _check_arg(t, name, count, *types)
+        if isinstance(t, torch.Tensor) and not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous tensor required (the C ABI takes dense row-major buffers)")
+        out.append(t.data_ptr() if isinstance(t, torch.Tensor) else t)
+    return out
+
+
+def _size(*v):
+    """The sizes' product for the extents checks, 0 if one is not positive (the library refuses negative ones)."""
+    n = 1
+    for x in v:
+        n *= max(int(x), 0)
+    return n
+
+
+def lowbit_kv_cache_bytes(pages: int, kv_heads: int, page_tokens: int, head_dim: int) -> int:
+    return lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim)
+
+
+def lowbit_kv_plan(new_lens, B, page_tokens, kv_lens, kv_lens_out, block_table, table_stride, free_pages, free_count,
+                   free_count_out, cu_q, cu_pages, slots, positions, max_tokens, status, free_capacity=None, stream=None):
+    """free_capacity: entries of free_pages (the tensor's size by default)."""
+    if free_capacity is None:
+        if not isinstance(free_pages, torch.Tensor):
+            raise ValueError("free_capacity: needed where free_pages is no tensor")
+        free_capacity = free_pages.numel()
+    b, n = _size(B), _size(max_tokens)
+    p = _flat((new_lens, "new_lens", b, _I32), (kv_lens, "kv_lens", b, _I32), (kv_lens_out, "kv_lens_out", b, _I32),
+              (block_table, "block_table", _size(B, table_stride), _I32), (free_pages, "free_pages", _size(free_capacity), _I32),
+              (free_count, "free_count", min(b, 1), _I32), (free_count_out, "free_count_out", min(b, 1), _I32),
+              (cu_q, "cu_q", b and b + 1, _I32), (cu_pages, "cu_pages", b and b + 1, _I32), (slots, "slots", b and n, (torch.int64,)),
+              (positions, "positions", b and n, _I32), (status, "status", b and 3, _I32))
+    ts = (new_lens, kv_lens, kv_lens_out, block_table, free_pages, free_count, free_count_out, cu_q, cu_pages, slots, positions, status)
+    _serve("lowbit_kv_plan", stream, ts, lambda s: lib.lowbit_kv_plan(
+        p[0], B, page_tokens, p[1], p[2], p[3], table_stride, p[4], free_capacity, p[5], p[6], p[7], p[8], p[9], p[10], max_tokens,
+        p[11], s))
+
+
+def lowbit_kv_release(done, B, page_tokens, kv_lens, block_table, table_stride, free_pages, free_count, status, free_capacity=None,
+                      stream=None):
+    if free_capacity is None:
+        if not isinstance(free_pages, torch.Tensor):
+            raise ValueError("free_capacity: needed where free_pages is no tensor")
+        free_capacity = free_pages.numel()
+    b = _size(B)
+    p = _flat((done, "done", b, _I32), (kv_lens, "kv_lens", b, _I32), (block_table, "block_table", _size(B, table_stride), _I32),
+              (free_pages, "free_pages", _size(free_capacity), _I32), (free_count, "free_count", min(b, 1), _I32),
+              (status, "status", b and 2, _I32))
+    _serve("lowbit_kv_release", stream, (done, kv_lens, block_table, free_pages, free_count, status), lambda s: lib.lowbit_kv_release(
+        p[0], B, page_tokens, p[1], p[2], table_stride, p[3], free_capacity, p[4], p[5], s))
+
+
+def lowbit_kv_append(dtype, k, v, T, kv_heads, head_dim, slots, cache, pages, page_tokens, k_stride=None, v_stride=None, stream=None):
+    """k, v: [T][kv_heads][head_dim] tensors (any token stride), or addresses with k_stride, v_stride."""
+    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
+    (pk, sk), (pv, sv) = (_row_arg(t, n, dtype, T, kv_heads, head_dim, st) for t, n, st in ((k, "k", k_stride), (v, "v", v_stride)))
+    ps, pc = _flat((slots, "slots", _size(T), (torch.int64,)), (cache, "cache", nb if T > 0 else 0))
+    _serve("lowbit_kv_append", stream, (k, v, slots, cache), lambda s: lib.lowbit_kv_append(
+        dtype, pk, sk, pv, sv, T, kv_heads, head_dim, ps, pc, pages, page_tokens, s))
+
+
+def lowbit_kv_read(dtype, cache, pages, page_tokens, T, kv_heads, head_dim, slots, k, v, k_stride=None, v_stride=None, stream=None):
+    """The rows of `slots` as the cache holds them, into k and v ([T][kv_heads][head_dim], any token stride)."""
+    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
+    (pk, sk), (pv, sv) = (_row_arg(t, n, dtype, T, kv_heads, head_dim, st) for t, n, st in ((k, "k", k_stride), (v, "v", v_stride)))
+    ps, pc = _flat((slots, "slots", _size(T), (torch.int64,)), (cache, "cache", nb if T > 0 else 0))
+    _serve("lowbit_kv_read", stream, (k, v, slots, cache), lambda s: lib.lowbit_kv_read(
+        dtype, pc, pages, page_tokens, T, kv_heads, head_dim, ps, pk, sk, pv, sv, s))
+
+
+def lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window=0) -> int:
+    return lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
+
+
+def lowbit_kv_attention(dtype, q, T, B, q_heads, kv_heads, head_dim, cu_q, kv_lens, block_table, table_stride, cache, pages,
+                        page_tokens, max_q, max_kv, scale, out, window=0, workspace=None, q_stride=None, out_stride=None, stream=None):
+    """q, out: [T][q_heads][head_dim] tensors (any token stride), or addresses with q_stride, out_stride.
+    workspace: a tensor of at least lowbit_kv_attention_workspace(...) bytes; by default one is taken from torch's
+    allocator for the stream the call runs on."""
+    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
+    some = T > 0 and B > 0
+    (pq, sq), (po, so) = (_row_arg(t, n, dtype, T, q_heads, head_dim, st) for t, n, st in ((q, "q", q_stride), (out, "out", out_stride)))
+    pcu, pl, pt, pc = _flat((cu_q, "cu_q", _size(B) + 1 if some else 0, _I32), (kv_lens, "kv_lens", _size(B) if some else 0, _I32),
+                            (block_table, "block_table", _size(B, table_stride) if some else 0, _I32),
+                            (cache, "cache", nb if some else 0))
+    need = lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
+
+    def call(s):
+        ws = workspace
+        if ws is None and need > 0:
+            at = out if isinstance(out, torch.Tensor) else None
+            dev = at.device if at is not None else torch.device("cuda", torch.cuda.current_device())
+            if s == torch.cuda.current_stream(dev).cuda_stream:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:  # of the other stream's own, so that nothing else gets it while that stream still works on it
+                with torch.cuda.stream(torch.cuda.ExternalStream(s or 0, device=dev)):
+                    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        have = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else max(need, 0)
+        (pw,) = _flat((ws, "workspace", max(need, 0)))
+        return lib.lowbit_kv_attention(dtype, pq, sq, T, B, q_heads, kv_heads, head_dim, pcu, pl, pt, table_stride, pc, pages,
+                                       page_tokens, max_q, max_kv, float(scale), window, po, so, pw, have, s)
+
+    _serve("lowbit_kv_attention", stream, (q, out, cu_q, kv_lens, block_table, cache, workspace), call)
+
+
+def _matrix(t, name, rows, width, types):
+    """A [rows][>= width] matrix with dense rows: (address, row stride in elements).  width None: any."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype not in types:
+        raise ValueError(f"{name}: a tensor of one of {[str(d) for d in types]} is required")
+    if t.dim() != 2 or t.shape[0] < rows or (width is not None and t.shape[1] < width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs at least [{rows}, {width if width is not None else 'any'}]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: dense rows required")
+    step = t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
+    if rows > 1 and step < t.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr(), step
+
+
+def lowbit_logits_process(dtype, logits, B, V, out, tokens=None, prompt_lens=None, total_lens=None, repetition=None, presence=None,
+                          frequency=None, bias_tokens=None, bias_values=None, bias_lens=None, mask=None, stream=None):
+    """logits, out [B][>= V] (out may be logits); tokens, bias_tokens, bias_values int32/int32/fp32 matrices with a
+    row a request; mask: int32 or uint32 words [B][>= ceil(V / 32)]; the rest vectors of B (include/lowbit.h)."""
+    b = _size(B)
+    types = (_DTYPES[dtype],) if dtype in _DTYPES else tuple(_DTYPES.values())
+    pin, sin = _matrix(logits, "logits", b, _size(V), types)
+    po, so = _matrix(out, "out", b, _size(V), types)
+    pt, st = _matrix(tokens, "tokens", b, None, _I32)
+    pm, sm = _matrix(mask, "mask", b, (_size(V) + 31) // 32, (torch.int32, torch.uint32))
+    f32 = (torch.float32,)
+    pp, ptl, pr, pps, pf, pbl = _flat((prompt_lens, "prompt_lens", b, _I32), (total_lens, "total_lens", b, _I32),
+                                      (repetition, "repetition", b, f32), (presence, "presence", b, f32),
+                                      (frequency, "frequency", b, f32), (bias_lens, "bias_lens", b, _I32))
+    pbt, sbt = _matrix(bias_tokens, "bias_tokens", b, None, _I32)
+    pbv, sbv = _matrix(bias_values, "bias_values", b, None, f32)
+    if bias_tokens is not None:
+        if bias_values is None or bias_values.shape[1] != bias_tokens.shape[1] or sbv != sbt:
+            raise ValueError("bias_values: the shape and row stride of bias_tokens are required")
+        if sbt != bias_tokens.shape[1]:
+            raise ValueError("bias_tokens: contiguous tensor required")
+    if tokens is not None and st != tokens.shape[1]:
+        raise ValueError("tokens: contiguous tensor required")
+    ts = (logits, out, tokens, prompt_lens, total_lens, repetition, presence, frequency, bias_tokens, bias_values, bias_lens, mask)
+    _serve("lowbit_logits_process", stream, ts, lambda s: lib.lowbit_logits_process(
+        dtype, pin, sin, B, V, pt, st, pp, ptl, pr, pps, pf, pbt, pbv, sbt, pbl, pm, sm, po, so, s))
 
 
 class Batch:

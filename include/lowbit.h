@@ -249,6 +249,117 @@ void lowbit_batch_destroy(lb_batch *b);
 lb_status lowbit_matvec_batched_static(const lb_matvec_desc *list, int32_t n, hipStream_t s);
 
 /*
+ * ---- Serving: the steps of a token between and after the products --------------------------------------
+ *
+ * A batch of B requests holds its keys and values in one paged cache a layer, 4 bits a value.  A step brings
+ * new_lens[b] new tokens of request b: lowbit_kv_plan gives them pages and slots, lowbit_kv_append quantises
+ * their keys and values into the slots, lowbit_kv_attention lets their queries attend to all of the request, and
+ * after the head lowbit_logits_process prepares the logits for sampling.  (The KV cache is the state that the
+ * bankml build history's 0.3.9 entry quantises with q8_0; the sampler's penalties, biases and grammars are those
+ * of the bankml technical report, section IV.4.)
+ *
+ * The cache of a layer (lowbit_kv_cache_bytes): `pages` pages of page_tokens tokens P (a power of two, 16 to
+ * 1024), a record of P * head_dim * 9 / 8 bytes per page and kv head, [pages][kv_heads][record].  32 consecutive
+ * values of a head share a binary16 scale d = fp16_rne(amax / 6) (the fp32 quotient, at most 65504), and a code
+ * is the E2M1 number (sign, then 0 .5 1 1.5 2 3 4 6) nearest to x / d, ties to the even code; all codes are 0
+ * where d = 0, and a block with a value that is not finite reads back as NaN.  With nb = head_dim / 32:
+ *   K codes  [P][4][nb][4 bytes]     byte (g, b, i): elements 32b + 8g + 2i (lower code) and 32b + 8g + 2i + 1
+ *   V codes  [P/4][16][4][nb bytes]  quad of tokens, c, token of the quad, byte i: elements 32i + c, 32i + 16 + c
+ *   K scales [P/4][nb][4] binary16   quad of tokens, block, token of the quad; then the V scales alike
+ * head_dim is 64, 128 or 256.  A slot is page * P + token of the page, in 64 bits.
+ *
+ * Rows (queries, keys, values, outputs) are [T][heads][head_dim] of type `dtype` with a stride between tokens in
+ * elements (so that they may be parts of wider rows); pointer and stride are multiples of 16 bytes.  What these
+ * entry points read on the device (lengths, tables, slots, token numbers) is checked by the kernels: no value of
+ * them leads outside the buffers that the sizes describe.
+ */
+typedef enum { LB_F32 = 0, LB_BF16 = 1, LB_F16 = 2 } lb_dtype;
+
+/* Bytes of one layer's cache; -1 for a bad shape. */
+int64_t lowbit_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_tokens, int64_t head_dim);
+
+/*
+ * The pages and slots of a step, from the requests' lengths.  Request b holds kv_lens[b] tokens in the pages
+ * block_table[b][0 ..] ([B][table_stride]) and brings new_lens[b] >= 0.  Its ceil((len + new) / P) - ceil(len / P)
+ * new pages come off the top of the free list: in order of requests and blocks, the i-th new page of the step is
+ * free_pages[free_count - 1 - i].  All device int32 (slots int64); written:
+ *   block_table        the entries of the new pages (no others)
+ *   kv_lens_out [B], free_count_out [1]   lengths and free pages after the step; may be kv_lens, free_count
+ *   cu_q [B+1], cu_pages [B+1]            running sums of the new tokens and of the new pages
+ *   slots, positions [max_tokens]         of new token i of request b, at cu_q[b] + i: its slot and its place in
+ *                                         the request (from 0); behind the last token, slot -1 and position 0
+ *   status [3]         0, or a sum of 1: too few free pages, 2: over max_tokens tokens, 4: a negative length, or
+ *                      one beyond its table or 2^31 - 1, 8: a free count below 0 or above free_capacity;
+ *                      then the pages and the tokens that the step asked for.
+ * All or nothing: where status[0] is not 0, no table entry, length or count changes, the sums are 0 and all slots
+ * -1, so that the step's other calls do nothing.  One launch up to 2048 requests and max_tokens 8192, else two.
+ */
+lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens, const int32_t *kv_lens, int32_t *kv_lens_out,
+                         int32_t *block_table, int64_t table_stride, const int32_t *free_pages, int64_t free_capacity,
+                         const int32_t *free_count, int32_t *free_count_out, int32_t *cu_q, int32_t *cu_pages, int64_t *slots,
+                         int32_t *positions, int64_t max_tokens, int32_t *status, hipStream_t s);
+
+/*
+ * The pages of the requests with done[b] != 0 go back on top of the free list (in order of requests and blocks),
+ * and their lengths become 0.  status [2]: 0, or a sum of 4: a length beyond its table, 8: the list would pass
+ * free_capacity, or its count is below 0 (then no length and no count changes); and the pages given back.
+ */
+lb_status lowbit_kv_release(const int32_t *done, int64_t B, int64_t page_tokens, int32_t *kv_lens, const int32_t *block_table,
+                            int64_t table_stride, int32_t *free_pages, int64_t free_capacity, int32_t *free_count, int32_t *status,
+                            hipStream_t s);
+
+/*
+ * Quantises T rows of keys and values into the slots of a layer's cache.  A row whose slot is negative or past
+ * the cache is left out.  Two rows with the same slot leave a mixture of both there.
+ */
+lb_status lowbit_kv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t T, int64_t kv_heads,
+                           int64_t head_dim, const int64_t *slots, void *cache, int64_t pages, int64_t page_tokens, hipStream_t s);
+
+/* The rows of T slots as the cache holds them (code times scale, rounded to dtype); zeros for a slot outside. */
+lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t page_tokens, int64_t T, int64_t kv_heads, int64_t head_dim,
+                         const int64_t *slots, void *k, int64_t k_stride, void *v, int64_t v_stride, hipStream_t s);
+
+/*
+ * Causal attention of a step's new tokens.  Request b's queries are rows cu_q[b] .. cu_q[b+1] - 1 of q and out
+ * (at most max_q of them, T rows in all), the last tokens of its kv_lens[b] <= max_kv tokens (new ones included,
+ * already appended), found through block_table[b].  Query i of n, at position pos = kv_lens[b] - n + i, sees the
+ * keys j with j <= pos, and with window > 0 only those with j > pos - window:
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max),  head h reading kv head h / (q_heads / kv_heads).
+ * A query that sees no key (kv_lens[b] < n) gives zeros; rows behind the last request are left as they were.  A
+ * page number outside the cache, among those that a query sees, makes the query's result NaN, as does a request
+ * longer than max_kv or than its table.  A request of more than max_q tokens may leave rows unwritten.
+ * fp32 rows are computed to fp32's accuracy (2^-20), bf16 and fp16 rows to binary16's.
+ * workspace: lowbit_kv_attention_workspace(...) bytes, 16-byte aligned, for the joining of long requests' parts
+ * (0 bytes, NULL, where none are split); calls that may run at the same time need one each.
+ */
+int64_t lowbit_kv_attention_workspace(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
+                                      int64_t max_kv, int64_t window);
+lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
+                              int64_t head_dim, const int32_t *cu_q, const int32_t *kv_lens, const int32_t *block_table,
+                              int64_t table_stride, const void *cache, int64_t pages, int64_t page_tokens, int64_t max_q,
+                              int64_t max_kv, float scale, int64_t window, void *out, int64_t out_stride, void *workspace,
+                              int64_t workspace_bytes, hipStream_t s);
+
+/*
+ * Logits before sampling: logits [B][V] of type `dtype`, row stride in_stride elements; out alike (it may be
+ * logits itself, with the same stride, but not overlap it otherwise).  In fp32, for every token t of row b, in
+ * this order, rounded to dtype once at the end:
+ *   penalties  t anywhere in the history tokens[b][0 .. total_lens[b]): l = l > 0 ? l / repetition[b] : l * repetition[b];
+ *              t count times in its output part, from prompt_lens[b] on, count > 0: l -= frequency[b] * count, then
+ *              l -= presence[b]
+ *   biases     l += the sum of the values of t's entries in bias_tokens[b][0 .. bias_lens[b]), added in list order
+ *   mask       l = -inf where bit t % 32 of mask[b][t / 32] is 0
+ * tokens, repetition, presence, frequency, bias_tokens and mask may be NULL (left out), prompt_lens too (all of the
+ * history is output).  Lengths are cut to the strides; token numbers outside 0 .. V-1 are passed over.  At most
+ * 16384 biases a row.  Results do not depend on the order in which anything runs.
+ */
+lb_status lowbit_logits_process(int dtype, const void *logits, int64_t in_stride, int64_t B, int64_t V, const int32_t *tokens,
+                                int64_t tok_stride, const int32_t *prompt_lens, const int32_t *total_lens, const float *repetition,
+                                const float *presence, const float *frequency, const int32_t *bias_tokens, const float *bias_values,
+                                int64_t bias_stride, const int32_t *bias_lens, const uint32_t *mask, int64_t mask_stride, void *out,
+                                int64_t out_stride, hipStream_t s);
+
+/*
  * Measurement helper, not a product: a streaming read of `nbytes` (a multiple of 16, 16-byte aligned) of
  * device memory by 16-byte non-temporal loads, the access pattern of the decode kernels' weight stream,
  * so its rate bounds theirs (tritium "Architecture", section 3: the roofline is measured with a

@@ -1,0 +1,231 @@
+"""Attention over the 4-bit cache against the 64-bit reference, with the reference's own bound of a 32-bit kernel's
+error, element by element."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_matvec_q1_amd.lowbit as L
+import serve_ref as R
+from gpu_util import dev, host, say
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": (L.F32, torch.float32), "bf16": (L.BF16, torch.bfloat16), "f16": (L.F16, torch.float16)}
+
+
+class Case:
+    def __init__(self, seed, kind, D, P, hq, hk, lens, news, window=0, v_scale=1.0, q_scale=1.0, extra=2, pad=0):
+        rng = np.random.default_rng(seed)
+        self.__dict__.update(kind=kind, D=D, P=P, hq=hq, hk=hk, lens=lens, news=news, window=window, B=len(lens), T=sum(news) + extra)
+        need = [-(-max(n, 0) // P) for n in lens]
+        self.pages, self.stride = sum(need) + 2, max(need + [1]) + 1
+        order = rng.permutation(self.pages)
+        self.table = np.full((self.B, self.stride), -1, np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.cache = R.random_cache(rng, self.pages, hk, P, D)
+        half = self.cache[:, :, P * D + P * D // 16:]
+        half[:] = (half.view(np.float16).astype(np.float64) * v_scale).astype(np.float16).view(np.uint8)
+        self.q = (torch.from_numpy(rng.standard_normal((self.T, hq, D))) * q_scale).to(TYPES[kind][1])
+        self.cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        self.scale = 1 / math.sqrt(D)
+        self.max_q, self.max_kv, self.pad = max(news + [0]), max(lens + [0]), pad
+
+    def gpu(self, **o):
+        a = dict(table=self.table, lens=np.array(self.lens, np.int32), cu=self.cu, max_q=self.max_q, max_kv=self.max_kv, workspace=None)
+        a.update(o)
+        wide = torch.full((self.T, self.hq * self.D + self.pad), 7.0, dtype=TYPES[self.kind][1], device="cuda")
+        out = wide[:, :self.hq * self.D]
+        q = torch.zeros(self.T, self.hq * self.D + self.pad, dtype=TYPES[self.kind][1], device="cuda")
+        q[:, :self.hq * self.D] = self.q.reshape(self.T, -1).cuda()
+        L.lowbit_kv_attention(TYPES[self.kind][0], q[:, :self.hq * self.D], self.T, self.B, self.hq, self.hk, self.D, dev(a["cu"]), dev(a["lens"]),
+                              dev(a["table"]), self.stride, dev(self.cache), self.pages, self.P, a["max_q"], a["max_kv"], self.scale, out,
+                              window=self.window, workspace=a["workspace"])
+        torch.cuda.synchronize()
+        assert (wide[:, self.hq * self.D:] == 7).all()
+        return out.double().cpu().numpy().reshape(self.T, self.hq, self.D)
+
+    def want(self):
+        return R.attention(self.cache, self.P, self.D, self.q.double().numpy(), self.cu, self.lens, self.table, self.hk, self.scale, self.window, self.kind)
+
+    def check(self, what, **o):
+        say("case " + what)
+        got, (ref, tol) = self.gpu(**o), self.want()
+        rows = self.cu[-1]
+        assert (got[rows:] == 7).all(), "rows behind the last request were written"
+        err = np.abs(got[:rows] - ref[:rows])
+        assert np.isfinite(got[:rows]).all()
+        worst = float((err / np.maximum(tol[:rows], 1e-300)).max()) if rows else 0.0
+        say(f"  worst error {err.max() if rows else 0:.3g}, of the bound {worst:.3g}")
+        assert worst <= 1.0
+        return got
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("D,hq,hk", [(128, 8, 2), (128, 5, 5), (64, 7, 1), (256, 16, 1), (64, 40, 2), (256, 6, 2)])
+def test_single_tokens(kind, D, hq, hk):
+    # one token to several chunks, one short of a page's end, at it and past it; requests of none
+    lens = [1, 2, 15, 16, 17, 31, 33, 130, 300, 1, 64, 0]
+    Case(D + hq, kind, D, 16, hq, hk, lens, [1] * 9 + [0] + [1] * 2, pad=64).check(f"single {kind} D={D} {hq}/{hk}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("D,P,hq,hk,window", [(128, 16, 4, 2, 0), (128, 64, 3, 1, 0), (64, 32, 8, 1, 0), (256, 16, 2, 1, 0), (128, 32, 4, 1, 5),
+                                              (64, 16, 2, 2, 33), (256, 128, 5, 1, 100)])
+def test_several_tokens(kind, D, P, hq, hk, window):
+    lens, news = [7, 40, 170, 3, 65, 90], [7, 33, 2, 0, 65, 1]
+    Case(P + hq, kind, D, P, hq, hk, lens, news, window).check(f"several {kind} D={D} P={P} {hq}/{hk} window={window}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_long_contexts_are_split_and_joined(kind):
+    c = Case(9, kind, 128, 32, 4, 1, [3000, 130, 1], [1, 1, 1])
+    assert L.lowbit_kv_attention_workspace(c.T, c.B, 4, 1, 128, 1, 3000) > 0
+    c.check(f"split {kind}")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_long_prompt(kind):
+    Case(10, kind, 64, 16, 2, 1, [400], [400], extra=0).check(f"prompt {kind}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("window", [1, 16, 1000])
+def test_windows(kind, window):
+    c = Case(11 + window, kind, 64, 16, 4, 2, [900, 20, 17], [1, 3, 17], window)
+    # pages before every query's window may be gone
+    for b in range(c.B):
+        first = max(0, c.lens[b] - c.news[b] + 1 - window)
+        c.table[b, :first // 16] = -1
+    c.check(f"window {window} {kind}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_rows_that_see_nothing_are_zero(kind):
+    # more new tokens than the request holds: the first queries lie before the first key
+    c = Case(12, kind, 128, 16, 4, 2, [3, 0, 20], [5, 4, 30])
+    got = c.check(f"empty rows {kind}")
+    assert (got[:2] == 0).all() and (got[5:9] == 0).all() and (got[9:19] == 0).all()
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("v_scale,q_scale", [(1e-4, 1.0), (2000.0, 1.0), (1.0, 1e-6), (1.0, 30.0), (1e-3, 12.0)])
+def test_ranges(kind, v_scale, q_scale):
+    Case(13, kind, 128, 16, 4, 1, [50, 300], [2, 1], v_scale=v_scale, q_scale=q_scale).check(f"ranges {kind} v {v_scale} q {q_scale}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_values_of_mixed_ranges(kind):
+    # a few tokens' values are thousands of times the others', some are all zero
+    c = Case(14, kind, 64, 16, 4, 1, [200], [1])
+    d = c.cache[:, :, 16 * 64 + 64:].view(np.float16)
+    d[0] *= np.float16(3000)
+    d[1] = 0
+    d[2] *= np.float16(1e-3)
+    c.check(f"mixed values {kind}")
+
+
+def test_masked_places_may_hold_anything():
+    # NaN scales behind every request's end, and in the new tokens that earlier queries must not see
+    c = Case(15, "f32", 128, 16, 4, 2, [37, 20], [3, 20])
+    ref, tol = c.want()
+    nan = np.float16(np.nan).view(np.uint16)
+    for b in range(2):
+        for j in range(c.lens[b] - 1, int(-(-c.lens[b] // 16) * 16)):  # the last token too
+            rec = c.cache[c.table[b, j // 16]]
+            for s in R.places(16, 128, j % 16)[4:]:
+                rec[:, s], rec[:, s + 1] = nan & 255, nan >> 8
+    say("case masked NaN")
+    got = c.gpu()
+    for b in range(2):
+        a, z = c.cu[b], c.cu[b + 1]
+        assert (np.abs(got[a:z - 1] - ref[a:z - 1]) <= tol[a:z - 1]).all()
+        assert np.isnan(got[z - 1]).all()  # the only query that sees it
+
+
+def test_queries_that_are_not_finite():
+    c = Case(16, "bf16", 64, 16, 4, 1, [40, 40], [1, 1])
+    ref, tol = c.want()
+    c.q[0, 1, 3] = math.nan
+    c.q[0, 2, 5] = math.inf
+    say("case NaN and infinite queries")
+    got = c.gpu()
+    assert np.isnan(got[0, 1]).all() and not np.isfinite(got[0, 2]).any()
+    for at in ((0, 0), (0, 3), (1, 0), (1, 1), (1, 2), (1, 3)):
+        assert (np.abs(got[at] - ref[at]) <= tol[at]).all()
+
+
+def test_bad_pages_lengths_and_offsets_stay_inside():
+    c = Case(17, "f16", 128, 16, 4, 2, [100, 100, 40, 100], [1, 1, 1, 1])
+    ref, tol = c.want()
+    table, lens = c.table.copy(), np.array(c.lens, np.int32)
+    table[0, 2] = c.pages  # seen: NaN
+    table[1, 2] = -5
+    lens[3] = 10**9  # longer than max_kv
+    say("case bad pages and lengths")
+    got = c.gpu(table=table, lens=lens)
+    assert np.isnan(got[[0, 1, 3]]).all() and (np.abs(got[2] - ref[2]) <= tol[2]).all()
+    lens[:] = -3
+    assert (c.gpu(lens=lens)[:4] == 0).all()
+    say("case bad offsets")
+    c.gpu(cu=np.array([0, 2**30, 1, -4, 3], np.int32))
+    c.gpu(cu=np.array([5, 4, 3, 2, 1], np.int32))
+    c.gpu(cu=np.array([-1, 1, 2, 3, 4], np.int32))
+    c = Case(18, "f16", 128, 16, 4, 1, [40, 40], [20, 20])
+    c.gpu(cu=np.array([7, 2**30, -3], np.int32))
+    c.gpu(max_q=1)  # fewer than there are: rows may stay unwritten, nothing else
+
+
+def test_cache_past_32_bits():
+    """The pages of a request that lie beyond 4 GiB."""
+    say("case attention past 4 GiB")
+    c = Case(19, "f32", 128, 16, 4, 4, [70], [1], extra=0)
+    ref, tol = c.want()
+    pages = (5 << 30) // (4 * R.record_bytes(16, 128))
+    big = torch.zeros(pages, 4, R.record_bytes(16, 128), dtype=torch.uint8, device="cuda")
+    big[pages - c.pages:] = dev(c.cache)
+    table = dev(np.where(c.table >= 0, c.table + (pages - c.pages), -1).astype(np.int32))
+    out = torch.empty(1, 4, 128, device="cuda")
+    L.lowbit_kv_attention(L.F32, c.q.cuda(), 1, 1, 4, 4, 128, dev(c.cu), dev(np.array(c.lens, np.int32)), table, c.stride, big, pages, 16, 1, 70,
+                          c.scale, out)
+    assert (np.abs(host(out).astype(np.float64) - ref) <= tol).all()
+
+
+def test_other_streams_graphs_and_workspaces():
+    """A captured call replayed with other contents, between eager calls on another stream, each with its own
+    workspace."""
+    say("case streams and graphs")
+    c = Case(20, "f16", 128, 16, 4, 1, [1500, 700], [1, 1], extra=0)
+    ref, tol = c.want()
+    args = [dev(x) for x in (c.cu, np.array(c.lens, np.int32), c.table, c.cache)]
+    q, out = c.q.cuda(), torch.empty_like(c.q, device="cuda")
+    need = L.lowbit_kv_attention_workspace(c.T, 2, 4, 1, 128, 1, 1500)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def call(q, out, **o):
+        L.lowbit_kv_attention(L.F16, q, c.T, 2, 4, 1, 128, args[0], args[1], args[2], c.stride, args[3], c.pages, 16, 1, 1500, c.scale, out, **o)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(q, out, workspace=ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(q, out, workspace=ws)
+    q2 = torch.flip(q, [0])
+    for turn in range(4):
+        out.zero_()
+        graph.replay()
+        eager = torch.empty_like(out)
+        call(q2, eager, stream=side)  # its own workspace, on a stream of its own
+        torch.cuda.synchronize()
+        assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+        again = torch.empty_like(out)
+        call(q2, again)
+        torch.cuda.synchronize()
+        assert torch.equal(again, eager)

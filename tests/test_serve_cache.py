@@ -1,0 +1,196 @@
+"""Rows into the 4-bit cache and back, and the step's page plan, against the 64-bit reference."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_matvec_q1_amd.lowbit as L
+import serve_ref as R
+from gpu_util import dev, host, say
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": (L.F32, torch.float32), "bf16": (L.BF16, torch.bfloat16), "f16": (L.F16, torch.float16)}
+
+
+def rows(rng, T, H, D, kind):
+    x = rng.standard_normal((T, H, D)) * np.exp(rng.uniform(-3, 3, (T, H, 1)))
+    return torch.from_numpy(x).to(TYPES[kind][1])
+
+
+def as64(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("D,P,H,T", [(64, 16, 1, 1), (64, 32, 3, 19), (128, 16, 5, 33), (128, 64, 2, 130), (256, 16, 2, 21), (256, 1024, 1, 7)])
+def test_append_writes_the_records(kind, D, P, H, T):
+    say(f"case append {kind} D={D} P={P} H={H} T={T}")
+    rng = np.random.default_rng(T + D)
+    pages = -(-T // P) + 2
+    slots = rng.permutation(pages * P)[:T].astype(np.int64)
+    slots[T // 2] = [-1, pages * P, slots[T // 2], 2**40][T % 4]  # left out, or not
+    k, v = rows(rng, T, H, D, kind), rows(rng, T, H, D, kind)
+    want = rng.integers(0, 256, (pages, H, R.record_bytes(P, D)), dtype=np.uint8)
+    cache = dev(want)
+    k64, v64 = as64(k), as64(v)
+    for t, s in enumerate(slots):
+        if 0 <= s < pages * P:
+            for h in range(H):
+                R.store(want, P, D, int(s), h, k64[t, h], v64[t, h])
+    # parts of wider rows: queries before, something behind
+    wide = torch.zeros(T, 2 * H * D + 64, dtype=TYPES[kind][1])
+    wide[:, 32:32 + H * D] = k.reshape(T, -1)
+    wide[:, 32 + H * D:32 + 2 * H * D] = v.reshape(T, -1)
+    wide = wide.cuda()
+    L.lowbit_kv_append(TYPES[kind][0], wide[:, 32:32 + H * D], wide[:, 32 + H * D:32 + 2 * H * D].view(T, H, D), T, H, D, dev(slots), cache, pages, P)
+    got = host(cache)
+    assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
+
+    back = torch.full((T + 1, 2, H * D), 7.0, dtype=TYPES[kind][1], device="cuda")
+    L.lowbit_kv_read(TYPES[kind][0], cache, pages, P, T, H, D, dev(slots), back[:, 0], back[:, 1])
+    got = as64(back)
+    for t, s in enumerate(slots):
+        for h in range(H):
+            kk, vv = R.load(want, P, D, int(s), h)[:2] if 0 <= s < pages * P else (np.zeros(D), np.zeros(D))
+            for i, x in enumerate((kk, vv)):
+                assert np.array_equal(got[t, i, h * D:(h + 1) * D], as64(torch.from_numpy(x).to(TYPES[kind][1])))
+    assert (got[T] == 7).all()  # behind the last row
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_append_ends_of_the_range_and_ties(kind):
+    say(f"case append ends {kind}")
+    D, P = 128, 16
+    big = {"f32": 3e38, "bf16": 3e38, "f16": 65504.0}[kind]
+    x = np.zeros((8, 1, D))
+    x[0, 0, :32] = np.tile([6, 0.25, -0.75, 1.25, -1.75, 2.5, 3.5, -5], 4)  # every border between two codes
+    x[0, 0, 32:64] = np.tile([-6 * 2**-10, 2**-12, 2**-8, 0.0], 8)
+    x[1, 0, 5] = np.nan
+    x[2, 0, 40] = np.inf
+    x[3, 0, 100] = -np.inf
+    x[4] = big
+    x[5] = 6e-8 if kind == "f16" else 1e-12  # the scale rounds to 0
+    x[6] = 2.0**-22  # a scale in binary16's lowest range
+    x[7] = np.random.default_rng(3).standard_normal(D)
+    t = torch.from_numpy(x).to(TYPES[kind][1])
+    want = np.zeros((1, 1, R.record_bytes(P, D)), np.uint8)
+    for i in range(8):
+        R.store(want, P, D, i, 0, as64(t)[i, 0], as64(t)[i, 0])
+    cache = torch.zeros(want.size, dtype=torch.uint8, device="cuda")
+    L.lowbit_kv_append(TYPES[kind][0], t.cuda(), t.cuda(), 8, 1, D, torch.arange(8, device="cuda"), cache, 1, P)
+    assert np.array_equal(host(cache), want.reshape(-1))
+    out = torch.empty(8, 1, D, device="cuda")
+    L.lowbit_kv_read(L.F32, cache, 1, P, 8, 1, D, torch.arange(8, device="cuda"), out, torch.empty_like(out))
+    o = host(out)[:, 0]
+    assert np.isnan(o[1, :32]).all() and (o[1, 32:] == 0).all() and np.isnan(o[2, 32:64]).all() and np.isnan(o[3, 96:]).all()
+
+
+def test_slots_past_32_bits():
+    """A cache of over 4 GiB: the last page's records, and nothing else, are written."""
+    say("case append past 4 GiB")
+    D, P, H = 128, 16, 4
+    pages = (5 << 30) // (H * R.record_bytes(P, D))
+    cache = torch.zeros(L.lowbit_kv_cache_bytes(pages, H, P, D), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(5)
+    k, v = rows(rng, 2, H, D, "f32"), rows(rng, 2, H, D, "f32")
+    slots = np.array([pages * P - 1, 3], np.int64)
+    L.lowbit_kv_append(L.F32, k.cuda(), v.cuda(), 2, H, D, dev(slots), cache, pages, P)
+    got = cache.view(pages, H, -1)
+    for t, s in enumerate(slots):
+        want = np.zeros((1, H, R.record_bytes(P, D)), np.uint8)
+        for h in range(H):
+            R.store(want, P, D, int(s) % P, h, as64(k)[t, h], as64(v)[t, h])
+        assert np.array_equal(host(got[int(s) // P]), want[0])
+    assert int(cache.count_nonzero()) == int(got[0].count_nonzero()) + int(got[pages - 1].count_nonzero())
+
+
+# ---- the step's pages and slots ------------------------------------------------------------------
+
+def gpu_plan(new, P, lens, table, free, count, max_tokens, capacity=None, alias=False):
+    i32 = lambda a: torch.tensor(np.array(a), dtype=torch.int32, device="cuda")  # noqa: E731
+    B, stride = len(lens), len(table[0])
+    d = dict(new=i32(new), lens=i32(lens), table=i32(table).reshape(B, stride), free=i32(free), count=i32([count]))
+    o = dict(cu=i32([-7] * (B + 1)), pages=i32([-7] * (B + 1)), slots=torch.full((max_tokens,), -7, device="cuda"),
+             positions=i32([-7] * max_tokens), status=i32([-7] * 3), table=d["table"])
+    o["lens"], o["count"] = (d["lens"], d["count"]) if alias else (i32([-7] * B), i32([-7]))
+    L.lowbit_kv_plan(d["new"], B, P, d["lens"], o["lens"], d["table"], stride, d["free"], d["count"], o["count"], o["cu"], o["pages"], o["slots"],
+                     o["positions"], max_tokens, o["status"], free_capacity=capacity)
+    return {k: host(v).tolist() for k, v in o.items()}
+
+
+def plan_case(rng, B, P, most, new):
+    lens = rng.integers(0, most + 1, B).tolist()
+    news = rng.integers(0, new + 1, B).tolist()
+    stride = -(-(most + new) // P)
+    used = [-(-n // P) for n in lens]
+    order = rng.permutation(B * stride + 3)
+    table, at = [], 0
+    for n in used:
+        table.append(order[at:at + n].tolist() + [-1] * (stride - n))
+        at += n
+    return news, lens, table, order[at:].tolist()
+
+
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("B,P,most,new", [(1, 16, 0, 1), (1, 1024, 5, 3), (7, 16, 100, 1), (64, 32, 300, 40), (1030, 16, 40, 2), (2048, 16, 20, 1),
+                                          (2049, 16, 20, 3), (20, 64, 1000, 3000)])
+def test_plan(B, P, most, new, alias):
+    say(f"case plan B={B} P={P} held<={most} new<={new} alias={alias}")
+    news, lens, table, free = plan_case(np.random.default_rng(B + P), B, P, most, new)
+    want = R.plan(news, P, lens, table, free, len(free), sum(news) + 3, len(free))
+    got = gpu_plan(news, P, lens, table, free, len(free), sum(news) + 3, alias=alias)
+    assert got == want
+
+
+@pytest.mark.parametrize("big", [False, True])  # one launch, and two
+def test_plan_refuses_as_a_whole(big):
+    say(f"case plan refusals big={big}")
+    B, P = (3000 if big else 9), 16
+    news, lens, table, free = plan_case(np.random.default_rng(1), B, P, 50, 30)
+    n, m = len(free), sum(news)
+    need = R.plan(news, P, lens, table, free, n, m, n)["status"][1]
+    assert gpu_plan(news, P, lens, table, free, need, m)["status"] == [0, need, m]  # exactly enough
+    for kw, bit in ((dict(count=need - 1), 1), (dict(max_tokens=m - 1), 2), (dict(count=-1), 9), (dict(count=n + 1, capacity=n), 8)):
+        a = dict(count=n, max_tokens=m, capacity=n)
+        a.update(kw)
+        for alias in (False, True):
+            want = R.plan(news, P, lens, table, free, a["count"], a["max_tokens"], a["capacity"])
+            got = gpu_plan(news, P, lens, table, free, a["count"], a["max_tokens"], a["capacity"], alias)
+            assert got == want and got["status"][0] == bit and got["lens"] == lens and got["count"] == [a["count"]]
+    for at, what in ((0, dict(new=-1)), (B - 1, dict(len=-5)), (B // 2, dict(new=10**6)), (B // 2, dict(len=2**31 - 1, new=1))):
+        x, y = list(news), list(lens)
+        x[at], y[at] = what.get("new", x[at]), what.get("len", y[at])
+        got = gpu_plan(x, P, y, table, free, n, m)
+        assert got["status"][0] & 4 and got["table"] == table and got["lens"] == y and got["cu"] == [0] * (B + 1) and got["slots"] == [-1] * m
+
+
+def test_plan_without_new_tokens():
+    got = gpu_plan([0, 0], 16, [3, 0], [[5], [-1]], [], 0, 0, capacity=0)
+    assert got["status"] == [0, 0, 0] and got["cu"] == [0, 0, 0] and got["lens"] == [3, 0]
+
+
+@pytest.mark.parametrize("B", [1, 5, 300])
+def test_release_gives_pages_back(B):
+    say(f"case release B={B}")
+    rng = np.random.default_rng(B)
+    _, lens, table, free = plan_case(rng, B, 16, 200, 0)
+    done = rng.integers(0, 2, B) * 3
+    done[0] = 1
+    count = len(free)
+    want = free + [p for b in range(B) if done[b] for p in table[b][:-(-lens[b] // 16)]]
+    i32 = lambda a: torch.tensor(np.array(a), dtype=torch.int32, device="cuda")  # noqa: E731
+    pages = i32(free + [-7] * (len(want) - count))
+    dl, dc, st = i32(lens), i32([count]), i32([-7, -7])
+    args = (i32(done), B, 16, dl, i32(table).reshape(B, -1), len(table[0]))
+    if len(want) > count:  # one too few: nothing changes
+        L.lowbit_kv_release(*args, pages, dc, st, free_capacity=len(want) - 1)
+        assert host(st).tolist() == [8, len(want) - count] and host(dl).tolist() == lens and host(dc).tolist() == [count]
+        assert host(pages).tolist()[:count] == free
+    L.lowbit_kv_release(*args, pages, dc, st)
+    assert host(st).tolist() == [0, len(want) - count] and host(pages).tolist() == want and host(dc).tolist() == [len(want)]
+    assert host(dl).tolist() == [0 if done[b] else lens[b] for b in range(B)]
+    L.lowbit_kv_release(*args, pages, dc, st)  # again: they hold nothing
+    assert host(st).tolist() == [0, 0] and host(dc).tolist() == [len(want)]
+    bad = i32([10**6] + [0] * (B - 1))
+    L.lowbit_kv_release(i32([1] * B), B, 16, bad, args[4], args[5], pages, dc, st)
+    assert host(st)[0] & 4 and host(bad)[0] == 10**6 and host(dc).tolist() == [len(want)]
