@@ -35,6 +35,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int ATT_ROWS = 16;  // query rows a tile
 constexpr int ATT_STEP = 32;  // tokens a step
 constexpr int ATT_WAVES = 4;
+constexpr int ATT_FILL = 1024;
 constexpr float REF_BELOW = 7.0f, REF_MOST = 15.0f; // of a row's reference, log2
 
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -65,22 +66,33 @@ __device__ __forceinline__ f16x2 codes2(uint32_t w, int b)
 template <int N> struct Words {
     uint32_t w[N];
 };
-template <int N> __device__ __forceinline__ Words<N> load_words(const uint8_t *p)
+// ONCE: nothing else reads the bytes, and they need not stay in the caches.
+template <int N, bool ONCE> __device__ __forceinline__ Words<N> load_words(const uint8_t *p)
 {
     Words<N> r;
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            const u32x4 t = *reinterpret_cast<const u32x4 *>(p + 4 * i);
+            const u32x4 *at = reinterpret_cast<const u32x4 *>(p + 4 * i);
+            const u32x4 t = ONCE ? __builtin_nontemporal_load(at) : *at;
             r.w[i] = t.x, r.w[i + 1] = t.y, r.w[i + 2] = t.z, r.w[i + 3] = t.w;
         }
     } else {
-        const u32x2 t = *reinterpret_cast<const u32x2 *>(p);
+        const u32x2 *at = reinterpret_cast<const u32x2 *>(p);
+        const u32x2 t = ONCE ? __builtin_nontemporal_load(at) : *at;
         r.w[0] = t.x, r.w[1] = t.y;
     }
     return r;
 }
 __device__ __forceinline__ float half_of(uint32_t w, int hi) { return half_bits_to_float((uint16_t)(hi ? w >> 16 : w)); }
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// An upper bound, by less than 2, of the log2 of a binary16 magnitude's bits.
+__device__ __forceinline__ float log2_above(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
 
 // Column c of four consecutive tokens (nb bytes each, byte b holding elements 32 b + c and 32 b + 16 + c) as
 // pairs of tokens: byte b of word [pair][half][b / 4] has element 32 b + 16 half + c of tokens 2 pair, 2 pair + 1.
@@ -107,16 +119,34 @@ template <int D> __device__ __forceinline__ Pairs<D> pair_tokens(const Words<D /
     return r;
 }
 
+// Two ways of placing query rows on the 16 columns of S^T:
+//   wide    16 rows; a lane scales four tokens' sums of every block, and needs all of their scales.
+//   packed  16 / nb rows, each once a block: column b * rows + r has row r's block b and zeros elsewhere, so one
+//           chain of products leaves every block's sums in its own column.  A lane multiplies them by its one
+//           block's scales, the nb columns of a row are added across the lanes, and the weights are multiplied by
+//           one block's value scales too; of O the rows (b, r) count in block b's columns.  Per step and lane 8
+//           scores' scalings instead of 8 nb, and 8 of the weights' instead of 8 nb, with a quarter of the scale
+//           registers.  For one token of up to 16 / nb heads a kv head (4 at head size 128) the rows fill the
+//           columns, which are empty otherwise.
+template <int D, bool PACK> struct Shape {
+    static constexpr int ROWS = PACK ? 16 / (D / 32) : ATT_ROWS;
+    static constexpr int SW = PACK ? 2 : D / 16; // words of scales a lane holds of four tokens
+    static __device__ __forceinline__ int word(int b, int i) { return (PACK ? 0 : 2 * b) + i / 2; }
+    // the column with row r's reference and sum for element d
+    static __device__ __forceinline__ int column(int r, int d) { return PACK ? d / 32 * ROWS + r : r; }
+};
+
 // One step's share of the cache in a lane: 16 tokens (sub 0) and 16 more (sub 1).
-template <int D> struct Step {
-    Words<D / 32> k[2];     // quarter g of every block of key c
-    Words<D / 32> v[2];     // column c of the quad g's four tokens
-    Words<D / 16> ks[2];    // [block][token of the quad g], binary16
-    Words<D / 16> vs[2];
+template <int D, bool PACK> struct Step {
+    Words<D / 32> k[2]; // quarter g of every block of key c
+    Words<D / 32> v[2]; // column c of the quad g's four tokens
+    Words<Shape<D, PACK>::SW> ks[2], vs[2]; // [block][token of the quad g], binary16; packed: the lane's block
 };
 
 struct Geo { // of a launch
     int G, nsplit, chunk, shift;
+    int tile, rows; // rows of a tile, and of those the ones that a request may fill
+    bool pack;
     bool by_request; // a request has at most one tile: the tile's slot is the request
     int64_t slots;
 };
@@ -177,58 +207,107 @@ __device__ __forceinline__ float groups_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// A query row's elements 32 b + 8 g + j as binary16, times 2^-e with the row's magnitude below 2^e; returns 2^e.
-template <int DT, int D, bool SPLIT> __device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, int g, f16x8 (&hi)[D / 32], f16x8 (&lo)[SPLIT ? D / 32 : 1])
+// The exponent e that takes a row whose largest magnitude is am below 2^e.
+__device__ __forceinline__ int row_exponent(float am)
 {
-    using R = RowType<DT>;
-    float x[D / 32][8];
-    float am = 0.0f;
-#pragma unroll
-    for (int b = 0; b < D / 32; b++) {
-        const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(q + 32 * b + 8 * g);
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            x[b][j] = R::get(v.v[j]);
-            am = fmaxf(am, fabsf(x[b][j]));
-        }
-    }
-    am = groups_max(am);
     int e = 0;
     if (am > 0.0f && am < INFINITY) { // not finite: the row stays as it is, and its result is not finite either
         (void)frexpf(am, &e);
         e = min(e, 127);
     }
+    return e;
+}
+template <bool SPLIT> __device__ __forceinline__ void query_halves(const float (&x)[8], int e, bool negate, f16x8 &hi, f16x8 &lo)
+{
 #pragma unroll
-    for (int b = 0; b < D / 32; b++)
+    for (int j = 0; j < 8; j++) {
+        const float y = ldexpf(negate ? -x[j] : x[j], -e);
+        const _Float16 h = (_Float16)y;
+        hi[j] = h;
+        if constexpr (SPLIT)
+            lo[j] = (_Float16)(y - (float)h); // the rest: 22 bits in all
+    }
+}
+template <int DT> __device__ __forceinline__ float load_eight(const typename RowType<DT>::T *q, float (&x)[8])
+{
+    const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(q);
+    float am = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float y = ldexpf(x[b][j], -e);
-            const _Float16 h = (_Float16)y;
-            hi[b][j] = h;
+    for (int j = 0; j < 8; j++) {
+        x[j] = RowType<DT>::get(v.v[j]);
+        am = fmaxf(am, fabsf(x[j]));
+    }
+    return am;
+}
+// A lane's column of queries, elements 32 b + 8 g + j, as binary16 times 2^-e; returns 2^e.
+template <int DT, int D, bool PACK, bool SPLIT>
+__device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, int c, int g, bool negate, f16x8 (&hi)[D / 32], f16x8 (&lo)[SPLIT ? D / 32 : 1])
+{
+    constexpr int NB = D / 32;
+    if constexpr (PACK) {
+        constexpr int ROWS = Shape<D, true>::ROWS;
+        float x[8];
+        float am = groups_max(load_eight<DT>(q + 32 * (c / ROWS) + 8 * g, x));
+#pragma unroll
+        for (int d = ROWS; d < 16; d *= 2)
+            am = fmaxf(am, __shfl_xor(am, d));
+        const int e = row_exponent(am);
+        f16x8 h, l;
+        query_halves<SPLIT>(x, e, negate, h, l);
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            hi[b] = b == c / ROWS ? h : f16x8{};
             if constexpr (SPLIT)
-                lo[b][j] = (_Float16)(y - (float)h); // the rest: 22 bits in all
+                lo[b] = b == c / ROWS ? l : f16x8{};
         }
-    return ldexpf(1.0f, e);
+        return ldexpf(1.0f, e);
+    } else {
+        float x[NB][8], am = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+            am = fmaxf(am, load_eight<DT>(q + 32 * b + 8 * g, x[b]));
+        const int e = row_exponent(groups_max(am));
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+            query_halves<SPLIT>(x[b], e, negate, hi[b], lo[SPLIT ? b : 0]);
+        return ldexpf(1.0f, e);
+    }
 }
 
-template <int D> struct Partial { // of a tile and chunk, in the workspace
-    float acc[ATT_ROWS][D];
-    float ref[ATT_ROWS], sum[ATT_ROWS];
+// sum over the lanes of a 16-lane row that are a multiple of N apart
+template <int N> __device__ __forceinline__ float sum_columns(float v)
+{
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false)); // row_ror:8
+    if (N <= 4)
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false)); // row_ror:4
+    if (N <= 2)
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xF, 0xF, false)); // row_ror:2
+    return v;
+}
+
+template <int D, bool PACK> struct Partial { // of a tile and chunk, in the workspace
+    float acc[Shape<D, PACK>::ROWS][D];
+    float ref[16], sum[16]; // by column
 };
 
-template <int DT, int D> __global__ __launch_bounds__(64 * ATT_WAVES, 2) void attn_kernel(AttnArgs a, Geo geo)
+// waves a SIMD that the registers have to leave room for
+template <int DT, int D, bool PACK> constexpr int attn_waves()
+{
+    return PACK ? (D == 256 ? 2 : DT == LB_F32 ? 3 : 4) : D == 256 ? 1 : D == 128 ? (DT == LB_F32 ? 2 : 3) : 4;
+}
+
+template <int DT, int D, bool PACK>
+__global__ __launch_bounds__(64 * ATT_WAVES, (attn_waves<DT, D, PACK>())) void attn_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
+    using S = Shape<D, PACK>;
     constexpr bool SPLIT = DT == LB_F32;
-    constexpr int NB = D / 32, NC = D / 16;
+    constexpr int NB = D / 32, NC = D / 16, ROWS = S::ROWS;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int64_t id = blockIdx.x;
-    const int split = (int)(id % geo.nsplit);
-    const int64_t sh = id / geo.nsplit;
-    const int head = (int)(sh % a.kv_heads);
-    const int64_t slot = sh / a.kv_heads;
-    const Tile t = tile_of(a, geo, slot, ATT_ROWS);
+    const uint32_t sh = blockIdx.x / (uint32_t)geo.nsplit, slot = sh / (uint32_t)a.kv_heads;
+    const int split = (int)(blockIdx.x - sh * geo.nsplit), head = (int)(sh - slot * (uint32_t)a.kv_heads);
+    const Tile t = tile_of(a, geo, slot, ROWS);
     if (t.row0 >= t.rows)
         return;
     const int start = t.lo + split * geo.chunk;
@@ -238,13 +317,13 @@ template <int DT, int D> __global__ __launch_bounds__(64 * ATT_WAVES, 2) void at
     const int P = 1 << geo.shift;
 
     // this lane's query row; the rows past the last repeat it, and are not stored
-    const int row = min(t.row0 + c, t.rows - 1);
+    const int row = min(t.row0 + c % ROWS, t.rows - 1);
     const int tok = row / geo.G, hq = head * geo.G + row % geo.G;
     const int pos = t.pos0 + tok;                                              // last token it sees
     const int from = a.window > 0 ? (int)max((int64_t)0, pos - a.window + 1) : 0; // and the first
     f16x8 qh[NB], ql[SPLIT ? NB : 1];
     const typename R::T *qp = static_cast<const typename R::T *>(a.q) + (int64_t)(a.cu_q[t.b] + tok) * a.q_stride + (int64_t)hq * D;
-    const float qscale = load_query<DT, D, SPLIT>(qp, g, qh, ql) * (a.scale * 1.44269504088896341f); // scores in powers of two
+    const float qscale = load_query<DT, D, PACK, SPLIT>(qp, c, g, a.scale < 0.0f, qh, ql) * (fabsf(a.scale) * 1.44269504088896341f); // scores in powers of two
 
     f32x4 acc[NC];
 #pragma unroll
@@ -255,83 +334,143 @@ template <int DT, int D> __global__ __launch_bounds__(64 * ATT_WAVES, 2) void at
     const int32_t *table = a.block_table + (int64_t)t.b * a.table_stride;
     const int64_t rec = kv_record_bytes(P, D);
     // positions that every row of the tile sees: no comparisons there
-    const int all_to = t.pos0 + t.row0 / geo.G, all_from = a.window > 0 ? (int)max((int64_t)0, t.pos0 + (int64_t)(min(t.rows - 1, t.row0 + ATT_ROWS - 1) / geo.G) - a.window + 1) : 0;
+    const int all_to = t.pos0 + t.row0 / geo.G, all_from = a.window > 0 ? (int)max((int64_t)0, t.pos0 + (int64_t)(min(t.rows - 1, t.row0 + ROWS - 1) / geo.G) - a.window + 1) : 0;
+    const int own = PACK ? c / ROWS : 0; // the first block whose scales this lane holds
 
-    auto load = [&](int t0, Step<D> &s, int (&bad)[2]) {
+    // the pages of a step's two halves; past the end the first's again (its tokens are masked)
+    auto pages_of = [&](int t0, int (&page)[2]) {
+        const int t1 = t0 < end ? t0 : end - 1;
+        page[0] = __builtin_amdgcn_readfirstlane(table[t1 >> geo.shift]);
+        page[1] = __builtin_amdgcn_readfirstlane(table[(t1 + 16 < end ? t1 + 16 : t1) >> geo.shift]);
+    };
+    auto record = [&](int page) {
+        return a.cache + ((int64_t)((uint32_t)page < (uint32_t)a.pages ? page : 0) * a.kv_heads + head) * rec;
+    };
+    // a half past the end lies in the page that pages_of gave for it, whatever it holds there
+    Step<D, PACK> s;
+    auto load_keys = [&](int t0, const int (&page)[2]) {
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-            // past the end the step's first page is read again; its tokens are masked
-            const int at = t0 + 16 * u < end ? t0 + 16 * u : t0;
-            int page = __builtin_amdgcn_readfirstlane(table[at >> geo.shift]);
-            bad[u] = (uint32_t)page >= (uint32_t)a.pages;
-            page = bad[u] ? 0 : page;
-            const uint8_t *r = a.cache + ((int64_t)page * a.kv_heads + head) * rec;
-            const int o = at & (P - 1);
-            s.k[u] = load_words<NB>(r + kv_k_byte(D, o + c, g, 0));
-            s.ks[u] = load_words<NB * 2>(r + kv_scale_byte(P, D, 0, o + 4 * g, 0));
-            s.v[u] = load_words<NB>(r + kv_v_byte(P, D, o + 4 * g, c));
-            s.vs[u] = load_words<NB * 2>(r + kv_scale_byte(P, D, 1, o + 4 * g, 0));
+            const uint8_t *r = record(page[u]);
+            const int o = (t0 + 16 * u) & (P - 1);
+            s.k[u] = load_words<NB, PACK>(r + kv_k_byte(D, o + c, g, 0));
+            s.ks[u] = load_words<S::SW, PACK>(r + kv_scale_byte(P, D, 0, o + 4 * g, own));
+        }
+    };
+    auto load_values = [&](int t0, const int (&page)[2]) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const uint8_t *r = record(page[u]);
+            const int o = (t0 + 16 * u) & (P - 1);
+            s.v[u] = load_words<NB, PACK>(r + kv_v_byte(P, D, o + 4 * g, c));
+            s.vs[u] = load_words<S::SW, PACK>(r + kv_scale_byte(P, D, 1, o + 4 * g, own));
         }
     };
 
-    for (int t0 = start + wave * ATT_STEP; t0 < end; t0 += ATT_WAVES * ATT_STEP) {
-        Step<D> s;
-        int bad[2];
-        load(t0, s, bad);
-        float sc[2][4], key[2][4];
+    // The next step's keys are loaded once this step's are used up, its values likewise, each into the same
+    // registers, and its pages were looked up a step earlier.  Loads past the end give some page of the request's,
+    // and are not used.
+    constexpr int NEXT = ATT_WAVES * ATT_STEP;
+    int page[3][2];
+    const int t_first = start + wave * ATT_STEP;
+    if (t_first < end) {
+        pages_of(t_first, page[0]);
+        pages_of(t_first + NEXT, page[1]);
+        load_keys(t_first, page[0]);
+        load_values(t_first, page[0]);
+    }
+    for (int t0 = t_first; t0 < end; t0 += NEXT) {
+        pages_of(t0 + 2 * NEXT, page[2]);
+        const int (&pg)[2] = page[0];
+        float sc[2][4];
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-            f32x4 x[NB];
+            f32x4 x[PACK ? 1 : NB];
 #pragma unroll
             for (int b = 0; b < NB; b++) {
                 const f16x8 k = codes8(s.k[u].w[b]);
-                x[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[b], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+                f32x4 &to = x[PACK ? 0 : b];
+                to = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[b], PACK && b ? to : f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
                 if constexpr (SPLIT)
-                    x[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[b], x[b], 0, 0, 0);
+                    to = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[b], to, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 float v = 0.0f;
-                uint32_t m = 0;
 #pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    v = fmaf(half_of(s.ks[u].w[2 * b + i / 2], i & 1), x[b][i], v);
-                    const uint32_t w = s.vs[u].w[2 * b + i / 2];
-                    m = max(m, (i & 1 ? w >> 16 : w) & 0x7fffu);
-                }
-                sc[u][i] = bad[u] ? NAN : v * qscale;
-                // the exponent of the largest value scale: an upper bound of its log2
-                key[u][i] = sc[u][i] + (float)((int)(m >> 10) - 14);
+                for (int b = 0; b < (PACK ? 1 : NB); b++)
+                    v = fmaf(half_of(s.ks[u].w[S::word(b, i)], i & 1), x[b][i], v);
+                if constexpr (PACK)
+                    v = sum_columns<ROWS>(v);
+                asm volatile("" : "+v"(v)); // computed here, not where it is used
+                sc[u][i] = v;
             }
         }
-        const bool whole = t0 + ATT_STEP <= end && t0 + ATT_STEP - 1 <= all_to && t0 >= all_from;
-        bool see[2][4];
-        bool past = false;
+        // the loads must not move above the last use of the registers they fill: the copies that this costs would
+        // wait for them at the step's end
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys(t0 + NEXT, page[1]);
+        Words<S::SW> vs[2] = {s.vs[0], s.vs[1]};
+        float most = -INFINITY;
+        uint32_t wide = 0; // the lane's largest value scales, two to a word
+        const bool inside = (uint32_t)pg[0] < (uint32_t)a.pages && (uint32_t)pg[1] < (uint32_t)a.pages;
+        if (!(inside && t0 + ATT_STEP <= end && t0 + ATT_STEP - 1 <= all_to && t0 >= all_from)) {
+            // At an edge: what a row does not see gets the score -inf, and no value scale, as that may be NaN.  What
+            // it sees of a page that is none is NaN.
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+            for (int u = 0; u < 2; u++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int j = t0 + 16 * u + 4 * g + i;
-                see[u][i] = whole || (j <= pos && j >= from && j < end);
-                past = past || (see[u][i] && key[u][i] > ref + REF_MOST);
-            }
-        if (__ballot(past)) {
+                for (int h = 0; h < 2; h++) {
+                    const bool none = (uint32_t)pg[u] >= (uint32_t)a.pages;
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (int i = 2 * h; i < 2 * h + 2; i++) {
+                        const int j = t0 + 16 * u + 4 * g + i;
+                        const bool see = j <= pos && j >= from && j < end;
+                        sc[u][i] = see ? (none ? NAN : sc[u][i]) : -INFINITY;
+                        keep |= see ? 0xffffu << (16 * (i & 1)) : 0u;
+                    }
+#pragma unroll
+                    for (int w = h; w < S::SW; w += 2)
+                        vs[u].w[w] &= keep;
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                most = fmaxf(most, sc[u][i]);
+#pragma unroll
+            for (int i = 0; i < S::SW; i++)
+                wide = max_u16x2(wide, vs[u].w[i]); // a sign, which no scale has, would only raise it
+        }
+        // no token of the lane passes the reference if its largest score with its largest value scale does not
+        const float bound = fmaf(most, qscale, log2_above(max(wide >> 16, wide & 0xffffu)));
+        if (__ballot(bound > ref + REF_MOST)) {
             float m = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    m = see[u][i] ? fmaxf(m, key[u][i]) : m;
-            const float now = fmaxf(ref, groups_max(m) - REF_BELOW);
-            const float f = now > -INFINITY ? exp2_raw(ref - now) : 1.0f; // a row with nothing yet has sums of 0
-            ref = now;
-            sum *= f;
+                for (int i = 0; i < 4; i++) {
+                    uint32_t w = 0;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float fr = __shfl(f, 4 * g + i); // the accumulators' rows
+                    for (int k = i / 2; k < S::SW; k += 2)
+                        w = max(w, (i & 1 ? vs[u].w[k] >> 16 : vs[u].w[k]) & 0x7fffu);
+                    m = fmaxf(m, fmaf(sc[u][i], qscale, log2_above(w)));
+                }
+            const bool past = m > ref + REF_MOST;
+            if (__ballot(past)) {
+                const float now = fmaxf(ref, groups_max(m) - REF_BELOW);
+                const float f = now > -INFINITY ? exp2_raw(ref - now) : 1.0f; // a row with nothing yet has sums of 0
+                ref = now;
+                sum *= f;
 #pragma unroll
-                for (int n = 0; n < NC; n++)
-                    acc[n][i] *= fr;
+                for (int i = 0; i < 4; i++) {
+                    const float fr = __shfl(f, 4 * g + i); // the accumulators' rows
+#pragma unroll
+                    for (int n = 0; n < NC; n++)
+                        acc[n][i] *= fr;
+                }
             }
         }
         const float against = ref > -INFINITY ? ref : 0.0f;
@@ -340,109 +479,148 @@ template <int DT, int D> __global__ __launch_bounds__(64 * ATT_WAVES, 2) void at
         for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                p[u][i] = see[u][i] ? exp2_raw(sc[u][i] - against) : 0.0f;
+                p[u][i] = exp2_raw(fmaf(sc[u][i], qscale, -against));
                 sum += p[u][i];
             }
         const Pairs<D> vp[2] = {pair_tokens<D>(s.v[0]), pair_tokens<D>(s.v[1])};
+        constexpr int PB = PACK ? 1 : NB;
+        f16x8 ph[PB], pl[SPLIT ? PB : 1]; // [first half's tokens, second's]
 #pragma unroll
-        for (int b = 0; b < NB; b++) {
-            f16x8 ph, pl;
+        for (int b = 0; b < PB; b++)
 #pragma unroll
             for (int u = 0; u < 2; u++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    // a token that is not seen may hold any scale, NaN too
-                    const float w = see[u][i] ? p[u][i] * half_of(s.vs[u].w[2 * b + i / 2], i & 1) : 0.0f;
+                    const float w = fmaf(half_of(vs[u].w[S::word(b, i)], i & 1), p[u][i], 0.0f);
                     const _Float16 h = (_Float16)w;
-                    ph[4 * u + i] = h;
+                    ph[b][4 * u + i] = h;
                     if constexpr (SPLIT)
-                        pl[4 * u + i] = (_Float16)(w - (float)h);
+                        pl[b][4 * u + i] = (_Float16)(w - (float)h);
                 }
+        __builtin_amdgcn_sched_barrier(0);
+        load_values(t0 + NEXT, page[1]);
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                f16x8 v;
+                u32x4 w;
 #pragma unroll
                 for (int u = 0; u < 2; u++)
 #pragma unroll
-                    for (int pair = 0; pair < 2; pair++) {
-                        const f16x2 h = codes2(vp[u].w[pair][half][b / 4], b);
-                        v[4 * u + 2 * pair] = h.x;
-                        v[4 * u + 2 * pair + 1] = h.y;
-                    }
-                acc[2 * b + half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, v, acc[2 * b + half], 0, 0, 0);
+                    for (int pair = 0; pair < 2; pair++)
+                        w[2 * u + pair] = __builtin_bit_cast(uint32_t, codes2(vp[u].w[pair][half][b / 4], b));
+                const f16x8 v = __builtin_bit_cast(f16x8, w);
+                acc[2 * b + half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[PACK ? 0 : b], v, acc[2 * b + half], 0, 0, 0);
                 if constexpr (SPLIT)
-                    acc[2 * b + half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, v, acc[2 * b + half], 0, 0, 0);
+                    acc[2 * b + half] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl[PACK ? 0 : b], v, acc[2 * b + half], 0, 0, 0);
             }
         }
+        page[0][0] = page[1][0], page[0][1] = page[1][1];
+        page[1][0] = page[2][0], page[1][1] = page[2][1];
     }
 
     // the four waves' results together
-    __shared__ float s_acc[ATT_WAVES][ATT_ROWS][D];
-    __shared__ float s_ref[ATT_WAVES][ATT_ROWS], s_sum[ATT_WAVES][ATT_ROWS];
+    __shared__ float s_acc[ATT_WAVES][ROWS][D];
+    __shared__ float s_ref[ATT_WAVES][16], s_sum[ATT_WAVES][16];
     sum = groups_sum(sum);
     if (g == 0)
         s_ref[wave][c] = ref, s_sum[wave][c] = sum;
 #pragma unroll
     for (int n = 0; n < NC; n++)
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            s_acc[wave][4 * g + i][16 * n + c] = acc[n][i];
+        for (int i = 0; i < 4; i++) {
+            const int col = 4 * g + i; // the accumulators' rows are the columns of S^T
+            if (!PACK || col / ROWS == n / 2)
+                s_acc[wave][col % ROWS][16 * n + c] = acc[n][i];
+        }
     __syncthreads();
     const bool only = t.hi - t.lo <= geo.chunk; // nothing to join with
-    Partial<D> *part = static_cast<Partial<D> *>(a.workspace) + (sh * geo.nsplit + split);
-    for (int e = threadIdx.x; e < ATT_ROWS * D; e += 64 * ATT_WAVES) {
-        const int r = e / D, d = e % D;
-        float m = s_ref[0][r];
+    Partial<D, PACK> *part = static_cast<Partial<D, PACK> *>(a.workspace) + ((int64_t)sh * geo.nsplit + split);
+    const int real = min(ROWS, t.rows - t.row0); // rows
+    for (int e = threadIdx.x; e < real * D; e += 64 * ATT_WAVES) {
+        const int r = e / D, d = e % D, col = S::column(r, d);
+        float m = s_ref[0][col];
 #pragma unroll
         for (int w = 1; w < ATT_WAVES; w++)
-            m = fmaxf(m, s_ref[w][r]);
+            m = fmaxf(m, s_ref[w][col]);
         float o = 0.0f, l = 0.0f;
 #pragma unroll
         for (int w = 0; w < ATT_WAVES; w++) {
-            const float f = s_ref[w][r] > -INFINITY ? exp2_raw(s_ref[w][r] - m) : s_sum[w][r]; // 0, or NaN where a score was
+            const float f = s_ref[w][col] > -INFINITY ? exp2_raw(s_ref[w][col] - m) : s_sum[w][col]; // 0, or NaN where a score was
             o = fmaf(f, s_acc[w][r][d], o);
-            l = fmaf(f, s_sum[w][r], l);
+            l = fmaf(f, s_sum[w][col], l);
         }
         if (only) {
             const int rr = t.row0 + r;
-            if (rr < t.rows) {
-                typename R::T *op = static_cast<typename R::T *>(a.out) + (int64_t)(a.cu_q[t.b] + rr / geo.G) * a.out_stride + (int64_t)(head * geo.G + rr % geo.G) * D;
-                op[d] = R::put(t.over ? NAN : l == 0.0f ? 0.0f : o / l);
-            }
+            typename R::T *op = static_cast<typename R::T *>(a.out) + (int64_t)(a.cu_q[t.b] + rr / geo.G) * a.out_stride + (int64_t)(head * geo.G + rr % geo.G) * D;
+            op[d] = R::put(t.over ? NAN : l == 0.0f ? 0.0f : o / l);
         } else {
             part->acc[r][d] = o;
-            if (d == 0)
-                part->ref[r] = m, part->sum[r] = l;
+            if (!PACK ? d == 0 : d % 32 == 0)
+                part->ref[col] = m, part->sum[col] = l;
         }
     }
 }
 
-// Joins the chunks of a tile: D threads a row.
-template <int DT, int D> __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Geo geo)
+// Joins the chunks of one row: the 256 threads take D/4 groups of four columns and 1024/D shares of the chunks,
+// whose loads do not wait for each other; the shares are added in LDS.
+template <int DT, int D, bool PACK> __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
-    constexpr int RPW = 256 / D; // rows a workgroup
-    const int64_t id = blockIdx.x;
-    const int64_t sh = id / (ATT_ROWS / RPW);
-    const int r = (int)(id % (ATT_ROWS / RPW)) * RPW + threadIdx.x / D, d = threadIdx.x % D;
-    const int head = (int)(sh % a.kv_heads);
-    const Tile t = tile_of(a, geo, sh / a.kv_heads, ATT_ROWS);
+    using S = Shape<D, PACK>;
+    constexpr int COLS = D / 4, SHARES = 256 / COLS;
+    __shared__ float s_ref[SHARES][COLS], s_l[SHARES][COLS];
+    __shared__ f32x4 s_o[SHARES][COLS];
+    const uint32_t sh = blockIdx.x / (uint32_t)geo.rows, slot = sh / (uint32_t)a.kv_heads;
+    const int r = (int)(blockIdx.x - sh * geo.rows), head = (int)(sh - slot * (uint32_t)a.kv_heads);
+    const Tile t = tile_of(a, geo, slot, S::ROWS);
     const int rr = t.row0 + r;
-    if (rr >= t.rows || t.hi - t.lo <= geo.chunk)
+    if (rr >= t.rows || t.over || t.hi - t.lo <= geo.chunk)
         return;
     const int n = min((t.hi - t.lo + geo.chunk - 1) / geo.chunk, geo.nsplit);
-    const Partial<D> *part = static_cast<const Partial<D> *>(a.workspace) + sh * geo.nsplit;
+    const Partial<D, PACK> *part = static_cast<const Partial<D, PACK> *>(a.workspace) + (int64_t)sh * geo.nsplit;
+    const int group = threadIdx.x % COLS, share = threadIdx.x / COLS, col = S::column(r, 4 * group);
+    // a share's reference first: its sums then need no rescaling
     float m = -INFINITY;
-    for (int i = 0; i < n; i++)
-        m = fmaxf(m, part[i].ref[r]);
-    float o = 0.0f, l = 0.0f;
-    for (int i = 0; i < n; i++) {
-        const float f = part[i].ref[r] > -INFINITY ? exp2_raw(part[i].ref[r] - m) : part[i].sum[r];
-        o = fmaf(f, part[i].acc[r][d], o);
-        l = fmaf(f, part[i].sum[r], l);
+#pragma unroll 4
+    for (int i = share; i < n; i += SHARES)
+        m = fmaxf(m, part[i].ref[col]);
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = share; i < n; i += SHARES) {
+        const float ref = part[i].ref[col], sum = part[i].sum[col];
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(&part[i].acc[r][4 * group]);
+        const float f = ref > -INFINITY ? exp2_raw(ref - m) : sum; // 0, or NaN where a score was
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            o[k] = fmaf(f, x[k], o[k]);
+        l = fmaf(f, sum, l);
     }
+    s_o[share][group] = o;
+    s_ref[share][group] = m;
+    s_l[share][group] = l;
+    __syncthreads();
+    if (threadIdx.x >= COLS)
+        return;
+    for (int i = 0; i < SHARES; i++)
+        m = fmaxf(m, s_ref[i][group]);
+    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    l = 0.0f;
+    for (int i = 0; i < SHARES; i++) {
+        const f32x4 x = s_o[i][group];
+        const float f = s_ref[i][group] > -INFINITY ? exp2_raw(s_ref[i][group] - m) : s_l[i][group];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            o[k] = fmaf(f, x[k], o[k]);
+        l = fmaf(f, s_l[i][group], l);
+    }
+    RowVec<DT, 4> v;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        v.v[k] = R::put(l == 0.0f ? 0.0f : o[k] / l);
     typename R::T *op = static_cast<typename R::T *>(a.out) + (int64_t)(a.cu_q[t.b] + rr / geo.G) * a.out_stride + (int64_t)(head * geo.G + rr % geo.G) * D;
-    op[d] = R::put(l == 0.0f ? 0.0f : o / l);
+    *reinterpret_cast<RowVec<DT, 4> *>(op + 4 * group) = v;
 }
 
 static Geo geometry(const AttnArgs &a)
@@ -452,17 +630,22 @@ static Geo geometry(const AttnArgs &a)
     g.shift = 0;
     while (((int64_t)1 << g.shift) < a.page_tokens)
         g.shift++;
-    g.by_request = a.max_q * g.G <= ATT_ROWS;
-    g.slots = g.by_request ? a.B : a.T * g.G / ATT_ROWS + a.B;
-    // tokens a tile may see, and the longest chunk that still gives the chip 2048 workgroups (8 a CU)
-    int64_t span = a.max_kv;
+    const int64_t most = (a.max_q > 0 ? a.max_q : 1) * g.G; // rows of a request
+    g.pack = most <= 16 / (a.head_dim / 32);
+    g.tile = g.pack ? (int)(16 / (a.head_dim / 32)) : ATT_ROWS;
+    g.by_request = most <= g.tile;
+    g.rows = (int)(g.by_request ? most : g.tile);
+    g.slots = g.by_request ? a.B : a.T * g.G / g.tile + a.B;
+    int64_t span = a.max_kv; // tokens a tile may see
     if (a.window > 0)
         span = span < a.window + ATT_ROWS + ATT_STEP ? span : a.window + ATT_ROWS + ATT_STEP;
-    int64_t chunk = 2048;
-    while (g.slots * a.kv_heads * ((span + chunk - 1) / chunk) > 65536 && chunk < span)
-        chunk *= 2;
-    while (chunk > 128 && g.slots * a.kv_heads * ((span + chunk - 1) / chunk) < 2048)
-        chunk /= 2;
+    const int64_t tiles = g.slots * a.kv_heads;
+    // Chunks long enough for one round of ATT_FILL workgroups, so that each one's start (about 3 us, a chunk of
+    // 2048 tokens takes 40) is paid once; but not over 2048 tokens, as lengths may differ, unless there are several
+    // rounds of tiles anyhow.
+    constexpr int64_t UNIT = ATT_WAVES * ATT_STEP;
+    int64_t chunk = (span * tiles / ATT_FILL + UNIT - 1) / UNIT * UNIT;
+    chunk = chunk < UNIT ? UNIT : chunk > 2048 && tiles < 4 * ATT_FILL ? 2048 : chunk;
     g.chunk = (int)chunk;
     g.nsplit = (int)(span > 0 ? (span + chunk - 1) / chunk : 1);
     return g;
@@ -471,40 +654,37 @@ static Geo geometry(const AttnArgs &a)
 int64_t kv_attention_workspace(const AttnArgs &a)
 {
     const Geo g = geometry(a);
-    if (g.nsplit == 1)
-        return 0;
-    const int64_t one = ATT_ROWS * (a.head_dim + 2) * 4;
-    return g.slots * a.kv_heads * g.nsplit * one;
+    return g.nsplit == 1 ? 0 : g.slots * a.kv_heads * g.nsplit * (g.tile * a.head_dim + 32) * 4;
 }
 
 int64_t kv_attention_workgroups(const AttnArgs &a)
 {
     const Geo g = geometry(a);
-    return g.slots * a.kv_heads * g.nsplit;
+    return g.slots * a.kv_heads * (g.nsplit > g.rows ? g.nsplit : g.rows);
 }
 
-template <int DT, int D> static hipError_t run(const AttnArgs &a, hipStream_t s)
+template <int DT, int D, bool PACK> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
 {
-    static_assert(sizeof(Partial<D>) == ATT_ROWS * (D + 2) * 4, "the workspace's size");
-    const Geo g = geometry(a);
+    static_assert(sizeof(Partial<D, PACK>) == (Shape<D, PACK>::ROWS * D + 32) * 4, "the workspace's size");
     const int64_t tiles = g.slots * a.kv_heads;
-    hipLaunchKernelGGL((attn_kernel<DT, D>), dim3((unsigned)(tiles * g.nsplit)), dim3(64 * ATT_WAVES), 0, s, a, g);
+    hipLaunchKernelGGL((attn_kernel<DT, D, PACK>), dim3((unsigned)(tiles * g.nsplit)), dim3(64 * ATT_WAVES), 0, s, a, g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || g.nsplit == 1)
         return e;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3((unsigned)(tiles * (ATT_ROWS * D / 256))), dim3(256), 0, s, a, g);
+    hipLaunchKernelGGL((attn_join_kernel<DT, D, PACK>), dim3((unsigned)(tiles * g.rows)), dim3(256), 0, s, a, g);
     return hipGetLastError();
 }
 
 template <int DT> static hipError_t run_d(const AttnArgs &a, hipStream_t s)
 {
+    const Geo g = geometry(a);
     switch (a.head_dim) {
     case 64:
-        return run<DT, 64>(a, s);
+        return g.pack ? run<DT, 64, true>(a, g, s) : run<DT, 64, false>(a, g, s);
     case 128:
-        return run<DT, 128>(a, s);
+        return g.pack ? run<DT, 128, true>(a, g, s) : run<DT, 128, false>(a, g, s);
     case 256:
-        return run<DT, 256>(a, s);
+        return g.pack ? run<DT, 256, true>(a, g, s) : run<DT, 256, false>(a, g, s);
     }
     return hipErrorInvalidValue;
 }
