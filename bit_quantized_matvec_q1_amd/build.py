@@ -15,7 +15,7 @@ OUT = os.path.join(HERE, "liblowbit.so")
 BUILD = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["abi.cpp", "quantize.hip", "matvec.hip", "q8.hip", "b3.hip", "popcount.hip", "head.hip", "gemm.hip", "probe.hip",
-           "abi_serve.cpp", "kvplan.hip", "kvcache.hip", "kvattn.hip", "logits.hip"]
+           "abi_serve.cpp", "kvplan.hip", "kvcache.hip", "kvattn.hip", "kvattn_prompt.hip", "logits.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

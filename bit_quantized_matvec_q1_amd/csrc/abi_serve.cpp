@@ -25,6 +25,8 @@ lb_status check_cache(const char *fn, int64_t pages, int64_t heads, int64_t P, i
         return lb::abi_fail(LB_ESHAPE, fn, "kv_heads must be from 1 to 65536");
     if (pages < 0 || pages > kMax)
         return lb::abi_fail(LB_ESHAPE, fn, "negative number of pages, or over 2^31-1");
+    if (heads * lb::kv_record_bytes(P, D) >= (int64_t)1 << 32)
+        return lb::abi_fail(LB_ESHAPE, fn, "a page of 4 GiB or more");
     return LB_OK;
 }
 

@@ -22,102 +22,11 @@
 //
 // Decode is bound by HBM and by the vector unit (unpacking, softmax), so the tokens of one (request, kv head)
 // are cut into chunks, one workgroup each, and the chunks' results joined by a second launch.
-#include "serve_internal.h"
+#include <type_traits>
+
+#include "kvattn_internal.h"
 
 namespace lb {
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int ATT_ROWS = 16;  // query rows a tile
-constexpr int ATT_STEP = 32;  // tokens a step
-constexpr int ATT_WAVES = 4;
-constexpr int ATT_FILL = 1024;
-constexpr float REF_BELOW = 7.0f, REF_MOST = 15.0f; // of a row's reference, log2
-
-__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Four bytes of codes -> eight binary16 numbers, exact.
-__device__ __forceinline__ f16x8 codes8(uint32_t w)
-{
-    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-}
-
-// Byte b's two codes.
-__device__ __forceinline__ f16x2 codes2(uint32_t w, int b)
-{
-    switch (b & 3) {
-    case 0:
-        return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
-    case 1:
-        return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-    case 2:
-        return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
-    default:
-        return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-    }
-}
-
-template <int N> struct Words {
-    uint32_t w[N];
-};
-// ONCE: nothing else reads the bytes, and they need not stay in the caches.
-template <int N, bool ONCE> __device__ __forceinline__ Words<N> load_words(const uint8_t *p)
-{
-    Words<N> r;
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const u32x4 *at = reinterpret_cast<const u32x4 *>(p + 4 * i);
-            const u32x4 t = ONCE ? __builtin_nontemporal_load(at) : *at;
-            r.w[i] = t.x, r.w[i + 1] = t.y, r.w[i + 2] = t.z, r.w[i + 3] = t.w;
-        }
-    } else {
-        const u32x2 *at = reinterpret_cast<const u32x2 *>(p);
-        const u32x2 t = ONCE ? __builtin_nontemporal_load(at) : *at;
-        r.w[0] = t.x, r.w[1] = t.y;
-    }
-    return r;
-}
-__device__ __forceinline__ float half_of(uint32_t w, int hi) { return half_bits_to_float((uint16_t)(hi ? w >> 16 : w)); }
-
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
-}
-// An upper bound, by less than 2, of the log2 of a binary16 magnitude's bits.
-__device__ __forceinline__ float log2_above(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
-
-// Column c of four consecutive tokens (nb bytes each, byte b holding elements 32 b + c and 32 b + 16 + c) as
-// pairs of tokens: byte b of word [pair][half][b / 4] has element 32 b + 16 half + c of tokens 2 pair, 2 pair + 1.
-template <int D> struct Pairs {
-    static constexpr int W = D > 128 ? 2 : 1;
-    uint32_t w[2][2][W];
-};
-template <int D> __device__ __forceinline__ Pairs<D> pair_tokens(const Words<D / 32> &v)
-{
-    Pairs<D> r;
-    constexpr uint32_t LO = 0x0f0f0f0fu, HI = 0xf0f0f0f0u;
-#pragma unroll
-    for (int p = 0; p < 2; p++)
-#pragma unroll
-        for (int i = 0; i < Pairs<D>::W; i++) {
-            uint32_t x, y; // the two tokens' bytes
-            if constexpr (D == 64)
-                x = v.w[p], y = v.w[p] >> 16; // both in one word
-            else
-                x = v.w[2 * p * Pairs<D>::W + i], y = v.w[(2 * p + 1) * Pairs<D>::W + i];
-            r.w[p][0][i] = (x & LO) | ((y << 4) & HI);
-            r.w[p][1][i] = ((x >> 4) & LO) | (y & HI);
-        }
-    return r;
-}
 
 // Two ways of placing query rows on the 16 columns of S^T:
 //   wide    16 rows; a lane scales four tokens' sums of every block, and needs all of their scales.
@@ -143,102 +52,6 @@ template <int D, bool PACK> struct Step {
     Words<Shape<D, PACK>::SW> ks[2], vs[2]; // [block][token of the quad g], binary16; packed: the lane's block
 };
 
-struct Geo { // of a launch
-    int G, nsplit, chunk, shift;
-    int tile, rows; // rows of a tile, and of those the ones that a request may fill
-    bool pack;
-    bool by_request; // a request has at most one tile: the tile's slot is the request
-    int64_t slots;
-};
-
-struct Tile {
-    int b, row0, rows, n, pos0;  // request, first row, the request's rows, its new tokens, first token's position
-    int lo, hi;                  // tokens any row of the tile sees
-    bool over;                   // the request is longer than max_kv: its rows become NaN
-};
-
-// The tile of a slot.  Slots are handed out so that request b's begin at floor(cu[b] * G / 16) + b, which leaves
-// it at least ceil(n_b * G / 16) of them: no sum over the requests' tiles is needed.
-__device__ __forceinline__ Tile tile_of(const AttnArgs &a, const Geo &g, int64_t slot, int rows_per_tile)
-{
-    Tile t;
-    int tile = 0;
-    if (g.by_request) {
-        t.b = (int)slot;
-    } else {
-        int lo = 0, hi = (int)a.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((int64_t)a.cu_q[mid] * g.G / rows_per_tile + mid <= slot)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        t.b = lo;
-        tile = (int)(slot - ((int64_t)a.cu_q[lo] * g.G / rows_per_tile + lo));
-    }
-    const int q0 = a.cu_q[t.b], q1 = a.cu_q[t.b + 1];
-    t.n = max(0, min(q1, (int)a.T) - q0);
-    if (q0 < 0 || tile < 0) // no offsets of a step
-        t.n = 0;
-    t.rows = (int)min((int64_t)t.n * g.G, (int64_t)INT32_MAX);
-    t.row0 = tile * rows_per_tile;
-    const int len = max(a.kv_lens[t.b], 0);
-    t.over = len > a.max_kv || len > a.table_stride << g.shift;
-    t.pos0 = len - t.n;
-    t.lo = t.hi = 0;
-    if (t.row0 < t.rows && !t.over) {
-        const int first = t.pos0 + t.row0 / g.G, last = t.pos0 + min(t.rows - 1, t.row0 + rows_per_tile - 1) / g.G;
-        t.hi = max(0, last + 1);
-        t.lo = a.window > 0 ? (int)max((int64_t)0, first - a.window + 1) & ~(ATT_STEP - 1) : 0;
-    }
-    return t;
-}
-
-// sum and maximum over the four lane groups that hold one row's tokens
-__device__ __forceinline__ float groups_max(float v)
-{
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
-}
-__device__ __forceinline__ float groups_sum(float v)
-{
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
-}
-
-// The exponent e that takes a row whose largest magnitude is am below 2^e.
-__device__ __forceinline__ int row_exponent(float am)
-{
-    int e = 0;
-    if (am > 0.0f && am < INFINITY) { // not finite: the row stays as it is, and its result is not finite either
-        (void)frexpf(am, &e);
-        e = min(e, 127);
-    }
-    return e;
-}
-template <bool SPLIT> __device__ __forceinline__ void query_halves(const float (&x)[8], int e, bool negate, f16x8 &hi, f16x8 &lo)
-{
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float y = ldexpf(negate ? -x[j] : x[j], -e);
-        const _Float16 h = (_Float16)y;
-        hi[j] = h;
-        if constexpr (SPLIT)
-            lo[j] = (_Float16)(y - (float)h); // the rest: 22 bits in all
-    }
-}
-template <int DT> __device__ __forceinline__ float load_eight(const typename RowType<DT>::T *q, float (&x)[8])
-{
-    const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(q);
-    float am = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        x[j] = RowType<DT>::get(v.v[j]);
-        am = fmaxf(am, fabsf(x[j]));
-    }
-    return am;
-}
 // A lane's column of queries, elements 32 b + 8 g + j, as binary16 times 2^-e; returns 2^e.
 template <int DT, int D, bool PACK, bool SPLIT>
 __device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, int c, int g, bool negate, f16x8 (&hi)[D / 32], f16x8 (&lo)[SPLIT ? D / 32 : 1])
@@ -285,10 +98,7 @@ template <int N> __device__ __forceinline__ float sum_columns(float v)
     return v;
 }
 
-template <int D, bool PACK> struct Partial { // of a tile and chunk, in the workspace
-    float acc[Shape<D, PACK>::ROWS][D];
-    float ref[16], sum[16]; // by column
-};
+template <int D, bool PACK> using Partial = PartialOf<D, Shape<D, PACK>::ROWS, 16>; // of a tile and chunk, in the workspace
 
 // waves a SIMD that the registers have to leave room for
 template <int DT, int D, bool PACK> constexpr int attn_waves()
@@ -562,33 +372,40 @@ __global__ __launch_bounds__(64 * ATT_WAVES, (attn_waves<DT, D, PACK>())) void a
     }
 }
 
-// Joins the chunks of one row: the 256 threads take D/4 groups of four columns and 1024/D shares of the chunks,
-// whose loads do not wait for each other; the shares are added in LDS.
-template <int DT, int D, bool PACK> __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Geo geo)
+// Joins the chunks of rows: the 256 threads are D/4 groups of four columns times 1024/D shares.  With many chunks a
+// workgroup takes one row, each share its own of the chunks, whose loads do not wait for each other, and the shares
+// are added in LDS; with at most as many chunks as shares, each share takes a row of its own.
+// TILE: rows of a prompt's tile; 0 for the tiles of attn_kernel.
+template <int DT, int D, bool PACK, int TILE> __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
     using S = Shape<D, PACK>;
+    using Part = std::conditional_t<TILE != 0, PartialOf<D, TILE, TILE>, Partial<D, PACK>>;
     constexpr int COLS = D / 4, SHARES = 256 / COLS;
     __shared__ float s_ref[SHARES][COLS], s_l[SHARES][COLS];
     __shared__ f32x4 s_o[SHARES][COLS];
-    const uint32_t sh = blockIdx.x / (uint32_t)geo.rows, slot = sh / (uint32_t)a.kv_heads;
-    const int r = (int)(blockIdx.x - sh * geo.rows), head = (int)(sh - slot * (uint32_t)a.kv_heads);
-    const Tile t = tile_of(a, geo, slot, S::ROWS);
+    const bool apart = geo.nsplit > SHARES; // a row's chunks over the shares
+    const int groups = apart ? geo.rows : (geo.rows + SHARES - 1) / SHARES;
+    const uint32_t sh = blockIdx.x / (uint32_t)groups, slot = sh / (uint32_t)a.kv_heads;
+    const int group = threadIdx.x % COLS, share = threadIdx.x / COLS;
+    const int r0 = (int)(blockIdx.x - sh * groups), r = apart ? r0 : r0 * SHARES + share;
+    const int head = (int)(sh - slot * (uint32_t)a.kv_heads);
+    const Tile t = tile_of(a, geo, slot, geo.tile);
     const int rr = t.row0 + r;
-    if (rr >= t.rows || t.over || t.hi - t.lo <= geo.chunk)
+    if (rr >= t.rows || r >= geo.rows || t.over || t.hi - t.lo <= geo.chunk) // all of the workgroup, if its shares are added
         return;
     const int n = min((t.hi - t.lo + geo.chunk - 1) / geo.chunk, geo.nsplit);
-    const Partial<D, PACK> *part = static_cast<const Partial<D, PACK> *>(a.workspace) + (int64_t)sh * geo.nsplit;
-    const int group = threadIdx.x % COLS, share = threadIdx.x / COLS, col = S::column(r, 4 * group);
-    // a share's reference first: its sums then need no rescaling
+    const Part *part = static_cast<const Part *>(a.workspace) + (int64_t)sh * geo.nsplit;
+    const int first = apart ? share : 0, step = apart ? SHARES : 1, col = S::column(r, 4 * group);
+    // the reference first: the sums then need no rescaling
     float m = -INFINITY;
 #pragma unroll 4
-    for (int i = share; i < n; i += SHARES)
+    for (int i = first; i < n; i += step)
         m = fmaxf(m, part[i].ref[col]);
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
 #pragma unroll 4
-    for (int i = share; i < n; i += SHARES) {
+    for (int i = first; i < n; i += step) {
         const float ref = part[i].ref[col], sum = part[i].sum[col];
         const f32x4 x = *reinterpret_cast<const f32x4 *>(&part[i].acc[r][4 * group]);
         const float f = ref > -INFINITY ? exp2_raw(ref - m) : sum; // 0, or NaN where a score was
@@ -597,23 +414,25 @@ template <int DT, int D, bool PACK> __global__ __launch_bounds__(256) void attn_
             o[k] = fmaf(f, x[k], o[k]);
         l = fmaf(f, sum, l);
     }
-    s_o[share][group] = o;
-    s_ref[share][group] = m;
-    s_l[share][group] = l;
-    __syncthreads();
-    if (threadIdx.x >= COLS)
-        return;
-    for (int i = 0; i < SHARES; i++)
-        m = fmaxf(m, s_ref[i][group]);
-    o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    l = 0.0f;
-    for (int i = 0; i < SHARES; i++) {
-        const f32x4 x = s_o[i][group];
-        const float f = s_ref[i][group] > -INFINITY ? exp2_raw(s_ref[i][group] - m) : s_l[i][group];
+    if (apart) {
+        s_o[share][group] = o;
+        s_ref[share][group] = m;
+        s_l[share][group] = l;
+        __syncthreads();
+        if (share > 0)
+            return;
+        for (int i = 0; i < SHARES; i++)
+            m = fmaxf(m, s_ref[i][group]);
+        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
+        for (int i = 0; i < SHARES; i++) {
+            const f32x4 x = s_o[i][group];
+            const float f = s_ref[i][group] > -INFINITY ? exp2_raw(s_ref[i][group] - m) : s_l[i][group];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            o[k] = fmaf(f, x[k], o[k]);
-        l = fmaf(f, s_l[i][group], l);
+            for (int k = 0; k < 4; k++)
+                o[k] = fmaf(f, x[k], o[k]);
+            l = fmaf(f, s_l[i][group], l);
+        }
     }
     RowVec<DT, 4> v;
 #pragma unroll
@@ -623,7 +442,7 @@ template <int DT, int D, bool PACK> __global__ __launch_bounds__(256) void attn_
     *reinterpret_cast<RowVec<DT, 4> *>(op + 4 * group) = v;
 }
 
-static Geo geometry(const AttnArgs &a)
+static Geo geometry(int dtype, const AttnArgs &a)
 {
     Geo g;
     g.G = (int)(a.q_heads / a.kv_heads);
@@ -631,60 +450,91 @@ static Geo geometry(const AttnArgs &a)
     while (((int64_t)1 << g.shift) < a.page_tokens)
         g.shift++;
     const int64_t most = (a.max_q > 0 ? a.max_q : 1) * g.G; // rows of a request
-    g.pack = most <= 16 / (a.head_dim / 32);
-    g.tile = g.pack ? (int)(16 / (a.head_dim / 32)) : ATT_ROWS;
+    const int packed = (int)(16 / (a.head_dim / 32));
+    // fp32 rows need the wide kernel's exact keys and split operands
+    g.kind = most <= packed ? Geo::PACKED : most <= PROMPT_FROM || dtype == LB_F32 ? Geo::WIDE : Geo::PROMPT;
+    g.tile = g.kind == Geo::PACKED ? packed : g.kind == Geo::WIDE ? ATT_ROWS : PROMPT_ROWS;
+    if (g.kind == Geo::PROMPT && a.head_dim <= 128 && a.T * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= ATT_FILL / 2)
+        g.tile = 2 * PROMPT_ROWS;
     g.by_request = most <= g.tile;
     g.rows = (int)(g.by_request ? most : g.tile);
     g.slots = g.by_request ? a.B : a.T * g.G / g.tile + a.B;
     int64_t span = a.max_kv; // tokens a tile may see
     if (a.window > 0)
-        span = span < a.window + ATT_ROWS + ATT_STEP ? span : a.window + ATT_ROWS + ATT_STEP;
+        span = span < a.window + g.tile + ATT_STEP ? span : a.window + g.tile + ATT_STEP;
     const int64_t tiles = g.slots * a.kv_heads;
-    // Chunks long enough for one round of ATT_FILL workgroups, so that each one's start (about 3 us, a chunk of
-    // 2048 tokens takes 40) is paid once; but not over 2048 tokens, as lengths may differ, unless there are several
-    // rounds of tiles anyhow.
+    // Chunks long enough for one round of as many workgroups as fit the chip, so that each one's start (about 3 us;
+    // a chunk of 2048 tokens takes 40) is paid once; but not over 2048 tokens, as lengths may differ, unless there
+    // are several rounds of tiles anyhow.
+    const int64_t fill = g.kind == Geo::PROMPT ? 768 : ATT_FILL;
     constexpr int64_t UNIT = ATT_WAVES * ATT_STEP;
-    int64_t chunk = (span * tiles / ATT_FILL + UNIT - 1) / UNIT * UNIT;
-    chunk = chunk < UNIT ? UNIT : chunk > 2048 && tiles < 4 * ATT_FILL ? 2048 : chunk;
+    if (g.kind == Geo::PROMPT && tiles >= 256) { // every CU has one, and a part is 64 KB to write and read again
+        g.chunk = (int)(span > UNIT ? (span + UNIT - 1) / UNIT * UNIT : UNIT);
+        g.nsplit = 1;
+        return g;
+    }
+    int64_t chunk = (span * tiles / fill + UNIT - 1) / UNIT * UNIT;
+    chunk = chunk < UNIT ? UNIT : chunk > 2048 && tiles < 4 * fill && g.kind != Geo::PROMPT ? 2048 : chunk;
     g.chunk = (int)chunk;
     g.nsplit = (int)(span > 0 ? (span + chunk - 1) / chunk : 1);
     return g;
 }
 
-int64_t kv_attention_workspace(const AttnArgs &a)
+static int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+
+static int64_t part_bytes(const Geo &g, const AttnArgs &a)
 {
-    const Geo g = geometry(a);
-    return g.nsplit == 1 ? 0 : g.slots * a.kv_heads * g.nsplit * (g.tile * a.head_dim + 32) * 4;
+    const int64_t part = g.tile * a.head_dim + 2 * (g.kind == Geo::PROMPT ? g.tile : 16);
+    return g.nsplit == 1 ? 0 : g.slots * a.kv_heads * g.nsplit * part * 4;
 }
+
+// enough for any row type
+int64_t kv_attention_workspace(const AttnArgs &a) { return larger(part_bytes(geometry(LB_F32, a), a), part_bytes(geometry(LB_F16, a), a)); }
 
 int64_t kv_attention_workgroups(const AttnArgs &a)
 {
-    const Geo g = geometry(a);
-    return g.slots * a.kv_heads * (g.nsplit > g.rows ? g.nsplit : g.rows);
+    const Geo f = geometry(LB_F32, a), h = geometry(LB_F16, a);
+    return larger(f.slots * larger(f.nsplit, f.rows), h.slots * larger(h.nsplit, h.rows)) * a.kv_heads;
 }
 
-template <int DT, int D, bool PACK> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
+template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
 {
-    static_assert(sizeof(Partial<D, PACK>) == (Shape<D, PACK>::ROWS * D + 32) * 4, "the workspace's size");
+    static_assert(sizeof(Partial<D, true>) == (Shape<D, true>::ROWS * D + 32) * 4 && sizeof(Partial<D, false>) == (ATT_ROWS * D + 32) * 4 &&
+                      sizeof(PartialOf<D, PROMPT_ROWS, PROMPT_ROWS>) == (PROMPT_ROWS * D + 2 * PROMPT_ROWS) * 4,
+                  "the workspace's size");
     const int64_t tiles = g.slots * a.kv_heads;
-    hipLaunchKernelGGL((attn_kernel<DT, D, PACK>), dim3((unsigned)(tiles * g.nsplit)), dim3(64 * ATT_WAVES), 0, s, a, g);
-    hipError_t e = hipGetLastError();
+    const dim3 grid((unsigned)(tiles * g.nsplit)), join((unsigned)(tiles * (g.nsplit > 1024 / D ? g.rows : (g.rows + 1024 / D - 1) / (1024 / D))));
+    hipError_t e = hipSuccess;
+    if (g.kind == Geo::PROMPT) {
+        e = launch_attn_prompt(DT, a, g, s);
+    } else {
+        if (g.kind == Geo::PACKED)
+            hipLaunchKernelGGL((attn_kernel<DT, D, true>), grid, dim3(64 * ATT_WAVES), 0, s, a, g);
+        else
+            hipLaunchKernelGGL((attn_kernel<DT, D, false>), grid, dim3(64 * ATT_WAVES), 0, s, a, g);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || g.nsplit == 1)
         return e;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D, PACK>), dim3((unsigned)(tiles * g.rows)), dim3(256), 0, s, a, g);
+    if (g.kind == Geo::PACKED)
+        hipLaunchKernelGGL((attn_join_kernel<DT, D, true, 0>), join, dim3(256), 0, s, a, g);
+    else if (g.kind == Geo::WIDE)
+        hipLaunchKernelGGL((attn_join_kernel<DT, D, false, 0>), join, dim3(256), 0, s, a, g);
+    else if constexpr (DT != LB_F32) // tiles of twice as many rows are never split
+        hipLaunchKernelGGL((attn_join_kernel<DT, D, false, PROMPT_ROWS>), join, dim3(256), 0, s, a, g);
     return hipGetLastError();
 }
 
 template <int DT> static hipError_t run_d(const AttnArgs &a, hipStream_t s)
 {
-    const Geo g = geometry(a);
+    const Geo g = geometry(DT, a);
     switch (a.head_dim) {
     case 64:
-        return g.pack ? run<DT, 64, true>(a, g, s) : run<DT, 64, false>(a, g, s);
+        return run<DT, 64>(a, g, s);
     case 128:
-        return g.pack ? run<DT, 128, true>(a, g, s) : run<DT, 128, false>(a, g, s);
+        return run<DT, 128>(a, g, s);
     case 256:
-        return g.pack ? run<DT, 256, true>(a, g, s) : run<DT, 256, false>(a, g, s);
+        return run<DT, 256>(a, g, s);
     }
     return hipErrorInvalidValue;
 }

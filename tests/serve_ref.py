@@ -75,7 +75,7 @@ def random_cache(rng, pages, heads, P, D, scale=1.0):
     return rec
 
 
-def attention(cache, P, D, q, cu, lens, table, hk, scale, window, dtype, pages=None):
+def attention(cache, P, D, q, cu, lens, table, hk, scale, window, dtype, rounded=False):
     """Outputs [T, hq, D] and how far off a kernel of 32-bit sums may be, element by element.
 
     The weights' relative error (twice, for the numerator and for the sum): the score's, scale times
@@ -84,7 +84,10 @@ def attention(cache, P, D, q, cu, lens, table, hk, scale, window, dtype, pages=N
     exponential's 2^-22.  Then the rounding of weight times value scale (fp16: 2^-11, fp32 rows: two of them,
     2^-21), with what is lost below binary16's range: half its least step, 2^-25, a key, times a code of at most 6,
     where the row's largest such product is at least 2^6 (the kernel aims it at 2^7 and knows it within a factor of
-    2; fp32 rows' second number ends at the same step); sums over the keys in fp32, and the result's rounding."""
+    2; fp32 rows' second number ends at the same step); sums over the keys in fp32, and the result's rounding.
+
+    rounded: keys and values are code times scale rounded to binary16 (the kernel for many rows), each off by at most
+    half a step, 2^-11 of its size: the scores by 2^-11 scale sum |q||k|, the outputs by 2^-11 sum w |v|."""
     T, hq, _ = q.shape
     G = hq // hk
     out, tol = np.full((T, hq, D), np.nan), np.zeros((T, hq, D))
@@ -119,6 +122,8 @@ def attention(cache, P, D, q, cu, lens, table, hk, scale, window, dtype, pages=N
                     few = np.abs(scale) * np.abs(kk).sum(-1).max() * np.abs(x).max() * 2.0**-24
                     ds = size * ((48 + nb) * 2.0**-24 + (2.0**-22 if dtype == "f32" else 0.0)) + few + 2.0**-22 + np.abs(s).max() * 2.0**-23
                     dp = 2.0**-21 if dtype == "f32" else EPS["f16"] / 2
+                    if rounded:
+                        ds, dp = ds + size * EPS["f16"] / 2, dp + EPS["f16"] / 2
                     m = len(w)
                     A = w @ np.abs(vv)
                     floor = m * 6 * 2.0**-31 * (w * dd.max(-1)).max()

@@ -50,7 +50,8 @@ class Case:
         return out.double().cpu().numpy().reshape(self.T, self.hq, self.D)
 
     def want(self):
-        return R.attention(self.cache, self.P, self.D, self.q.double().numpy(), self.cu, self.lens, self.table, self.hk, self.scale, self.window, self.kind)
+        return R.attention(self.cache, self.P, self.D, self.q.double().numpy(), self.cu, self.lens, self.table, self.hk, self.scale, self.window, self.kind,
+                           rounded=self.kind != "f32" and self.max_q * self.hq // self.hk > 64)
 
     def check(self, what, **o):
         say("case " + what)
@@ -127,6 +128,61 @@ def test_values_of_mixed_ranges(kind):
     d[1] = 0
     d[2] *= np.float16(1e-3)
     c.check(f"mixed values {kind}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D,P,hq,hk,window,lens,news", [(128, 16, 4, 1, 0, [33, 300, 129], [33, 17, 128]), (64, 64, 14, 2, 0, [200, 65], [64, 65]),
+                                                        (256, 16, 4, 2, 0, [150], [70]), (128, 32, 4, 4, 0, [700, 3, 1], [130, 2, 1]),
+                                                        (128, 16, 8, 1, 40, [260, 100], [100, 90])])
+def test_prompts(kind, D, P, hq, hk, window, lens, news):
+    Case(D + P + hq, kind, D, P, hq, hk, lens, news, window, pad=8).check(f"prompts {kind} D={D} P={P} {hq}/{hk} window={window}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_a_prompt_after_a_long_context_is_split(kind):
+    c = Case(31, kind, 64, 16, 4, 1, [2500], [40], extra=0)
+    assert L.lowbit_kv_attention_workspace(c.T, c.B, 4, 1, 64, 40, 2500) > 0
+    c.check(f"split prompt {kind}")
+
+
+@pytest.mark.parametrize("first", ["keys", "values"])
+def test_prompt_scales_that_grow_on_the_way(first):
+    # tokens 70 and 300 pass the scales seen before by far: the tile is unpacked again
+    c = Case(32, "bf16", 128, 16, 4, 1, [400], [60])
+    for j, f in ((70, 300.0), (300, 20000.0)):
+        rec = c.cache[c.table[0, j // 16], 0]
+        for s in R.places(16, 128, j % 16)[4 if first == "keys" else 5]:
+            d = rec[s:s + 2].view(np.float16)
+            d[:] = np.float16(float(d[0]) * f)
+    if first == "keys":
+        c.q = c.q * 2.0**-12  # scores of some tens
+    c.check(f"growing {first}")
+
+
+def test_prompt_rows_see_what_is_not_finite_and_no_more():
+    c = Case(33, "f16", 64, 16, 4, 1, [100], [60])
+    ref, tol = c.want()
+    nan = np.float16(np.nan).view(np.uint16)
+    for j, which, block in ((60, 5, 1), (80, 4, 0), (99, 5, 0)):  # a value block, a key block, the last value
+        rec = c.cache[c.table[0, j // 16], 0]
+        s = R.places(16, 64, j % 16)[which][block]
+        rec[s], rec[s + 1] = nan & 255, nan >> 8
+    tail = c.cache[c.table[0, 6], 0]
+    for o in range(4, 16):  # behind the end
+        for s in R.places(16, 64, o)[4:]:
+            tail[s], tail[s + 1] = nan & 255, nan >> 8
+    say("case prompt NaN")
+    got = c.gpu()[:60]
+    at = 40 + np.arange(60)  # positions
+    bad = np.zeros((60, 64), bool)
+    bad[at >= 60, 32:] = True
+    bad[at >= 80] = True
+    bad[at >= 99, :32] = True
+    assert np.array_equal(np.isnan(got), np.broadcast_to(bad[:, None, :], got.shape))
+    fine = ~np.isnan(got)
+    assert (np.abs(got - ref[:60])[fine] <= tol[:60][fine]).all()
+    c.table[0, 1] = c.pages + 5  # a page that is none: all rows see it
+    assert np.isnan(c.gpu()[:60]).all()
 
 
 def test_masked_places_may_hold_anything():
