@@ -238,72 +238,92 @@ def lowbit_read_probe(buf, nbytes, sink, stream=None):
 
 
 # ---- serving: block tables, the 4-bit cache, attention over it, logits ----------------------------
+#
+# A decode step calls these once a layer, on a few KB to MB: the time of a call in Python is a good part of them, so
+# a tensor's checks here are few calls each.
 
 _DTYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
-_I32 = (torch.int32,)
+_I32, _I64T, _F32T = torch.int32, torch.int64, torch.float32
+_Tensor = torch.Tensor
+# the current stream's handle without a stream object about it, where this torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _serve(fn, stream, tensors, call):
-    """call(stream) on the tensors' device, which all of them have to share, whatever the current device is."""
-    on = [t for t in tensors if isinstance(t, torch.Tensor)]
-    for t in on:
-        if not t.is_cuda:
-            raise ValueError(f"device tensor required, got one on {t.device}")
-        if t.device != on[0].device:
-            raise ValueError(f"tensors on {on[0].device} and {t.device}: one device required")
-    if not on or on[0].device.index == torch.cuda.current_device():
-        _check(call(_stream(stream, *on)), fn)
-        return
-    with torch.cuda.device(on[0].device):
-        _check(call(_stream(stream, *on)), fn)
+def _call(name, fn, stream, tensors, args):
+    """fn(*args, stream) on the device of `tensors`, which all of them have to share, whatever the current one is."""
+    dev = -1
+    for t in tensors:
+        if isinstance(t, _Tensor):
+            if not t.is_cuda:
+                raise ValueError(f"device tensor required, got one on {t.device}")
+            i = t.get_device()
+            if i != dev:
+                if dev >= 0:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{i}: one device required")
+                dev = i
+    if stream is None:
+        stream = _raw_stream(dev) if dev >= 0 else None
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev < 0 or dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != LB_OK:
+        raise LowbitError(st, name)
+
+
+def _flat(t, name, count, dtype):
+    """The address of a dense argument of at least `count` elements (its device is checked by _call); None and
+    addresses pass through.  dtype None: `count` bytes of any type."""
+    if t is None or isinstance(t, int):
+        return t
+    if not isinstance(t, _Tensor):
+        raise ValueError(f"{name}: a torch tensor, an int address or None is required")
+    if dtype is None:
+        have = t.numel() * t.element_size()
+    else:
+        have = t.numel()
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: dtype {t.dtype} not accepted (expected {dtype})")
+    if have < count:
+        raise ValueError(f"{name}: needs at least {count} {'bytes' if dtype is None else 'elements'}, has {have}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor required (the C ABI takes dense row-major buffers)")
+    return t.data_ptr()
 
 
 def _row_arg(t, name, dtype, T, heads, D, stride):
     """Rows [T][heads][D]: (address, token stride).  A tensor may be a part of wider rows (any token stride, the
     row itself dense); an address takes `stride`, dense rows by default."""
-    width = max(int(heads), 0) * max(int(D), 0)
+    width = heads * D if heads > 0 and D > 0 else 0
     if t is None or isinstance(t, int):
         return t, width if stride is None else int(stride)
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise ValueError(f"{name}: a torch tensor, an int address or None is required")
-    if dtype in _DTYPES and t.dtype != _DTYPES[dtype]:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {_DTYPES[dtype]}")
+    want = _DTYPES.get(dtype)
+    if want is not None and t.dtype is not want:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {want}")
     if T <= 0:
         return t.data_ptr(), width if stride is None else int(stride)
-    if t.dim() == 2 and t.shape[1] == width:
-        dense = t.stride(1) == 1 or width == 1
-    elif t.dim() == 3 and tuple(t.shape[1:]) == (heads, D):
-        dense = (t.stride(2) == 1 or D == 1) and (t.stride(1) == D or heads == 1)
+    shape, steps = t.shape, t.stride()
+    if len(shape) == 3 and shape[1] == heads and shape[2] == D:
+        dense = (steps[2] == 1 or D == 1) and (steps[1] == D or heads == 1)
+    elif len(shape) == 2 and shape[1] == width:
+        dense = steps[1] == 1 or width == 1
     else:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {heads}, {D}] or [T, {width}]")
-    if t.shape[0] < T:
-        raise ValueError(f"{name}: needs at least {T} rows, has {t.shape[0]}")
-    step = t.stride(0) if T > 1 else max(t.stride(0), width)
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, {heads}, {D}] or [T, {width}]")
+    if shape[0] < T:
+        raise ValueError(f"{name}: needs at least {T} rows, has {shape[0]}")
+    step = steps[0]
+    if T == 1 and step < width:
+        step = width
     if not dense or step < width:
         raise ValueError(f"{name}: a row's elements have to be dense, and rows apart")
     if stride is not None and int(stride) != step:
         raise ValueError(f"{name}: stride {stride} given, the tensor's is {step}")
     return t.data_ptr(), step
-
-
-def _flat(*specs):
-    """Addresses of dense arguments (t, name, count[, dtypes]) after the checks of sizes, types and layout (the
-    device is checked for all of a call's tensors together)."""
-    out = []
-    for t, name, count, *types in specs:
-        _check_arg(t, name, count, *types)
-        if isinstance(t, torch.Tensor) and not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous tensor required (the C ABI takes dense row-major buffers)")
-        out.append(t.data_ptr() if isinstance(t, torch.Tensor) else t)
-    return out
-
-
-def _size(*v):
-    """The sizes' product for the extents checks, 0 if one is not positive (the library refuses negative ones)."""
-    n = 1
-    for x in v:
-        n *= max(int(x), 0)
-    return n
 
 
 def lowbit_kv_cache_bytes(pages: int, kv_heads: int, page_tokens: int, head_dim: int) -> int:
@@ -314,55 +334,68 @@ def lowbit_kv_plan(new_lens, B, page_tokens, kv_lens, kv_lens_out, block_table, 
                    free_count_out, cu_q, cu_pages, slots, positions, max_tokens, status, free_capacity=None, stream=None):
     """free_capacity: entries of free_pages (the tensor's size by default)."""
     if free_capacity is None:
-        if not isinstance(free_pages, torch.Tensor):
+        if not isinstance(free_pages, _Tensor):
             raise ValueError("free_capacity: needed where free_pages is no tensor")
         free_capacity = free_pages.numel()
-    b, n = _size(B), _size(max_tokens)
-    p = _flat((new_lens, "new_lens", b, _I32), (kv_lens, "kv_lens", b, _I32), (kv_lens_out, "kv_lens_out", b, _I32),
-              (block_table, "block_table", _size(B, table_stride), _I32), (free_pages, "free_pages", _size(free_capacity), _I32),
-              (free_count, "free_count", min(b, 1), _I32), (free_count_out, "free_count_out", min(b, 1), _I32),
-              (cu_q, "cu_q", b and b + 1, _I32), (cu_pages, "cu_pages", b and b + 1, _I32), (slots, "slots", b and n, (torch.int64,)),
-              (positions, "positions", b and n, _I32), (status, "status", b and 3, _I32))
-    ts = (new_lens, kv_lens, kv_lens_out, block_table, free_pages, free_count, free_count_out, cu_q, cu_pages, slots, positions, status)
-    _serve("lowbit_kv_plan", stream, ts, lambda s: lib.lowbit_kv_plan(
-        p[0], B, page_tokens, p[1], p[2], p[3], table_stride, p[4], free_capacity, p[5], p[6], p[7], p[8], p[9], p[10], max_tokens,
-        p[11], s))
+    one = 1 if B > 0 else 0
+    n = max_tokens * one
+    args = (_flat(new_lens, "new_lens", B, _I32), B, page_tokens, _flat(kv_lens, "kv_lens", B, _I32),
+            _flat(kv_lens_out, "kv_lens_out", B, _I32), _flat(block_table, "block_table", B * table_stride, _I32), table_stride,
+            _flat(free_pages, "free_pages", free_capacity, _I32), free_capacity, _flat(free_count, "free_count", one, _I32),
+            _flat(free_count_out, "free_count_out", one, _I32), _flat(cu_q, "cu_q", (B + 1) * one, _I32),
+            _flat(cu_pages, "cu_pages", (B + 1) * one, _I32), _flat(slots, "slots", n, _I64T), _flat(positions, "positions", n, _I32),
+            max_tokens, _flat(status, "status", 3 * one, _I32))
+    _call("lowbit_kv_plan", lib.lowbit_kv_plan, stream, (new_lens, kv_lens, kv_lens_out, block_table, free_pages, free_count,
+                                                         free_count_out, cu_q, cu_pages, slots, positions, status), args)
 
 
 def lowbit_kv_release(done, B, page_tokens, kv_lens, block_table, table_stride, free_pages, free_count, status, free_capacity=None,
                       stream=None):
+    """free_capacity: entries of free_pages (the tensor's size by default)."""
     if free_capacity is None:
-        if not isinstance(free_pages, torch.Tensor):
+        if not isinstance(free_pages, _Tensor):
             raise ValueError("free_capacity: needed where free_pages is no tensor")
         free_capacity = free_pages.numel()
-    b = _size(B)
-    p = _flat((done, "done", b, _I32), (kv_lens, "kv_lens", b, _I32), (block_table, "block_table", _size(B, table_stride), _I32),
-              (free_pages, "free_pages", _size(free_capacity), _I32), (free_count, "free_count", min(b, 1), _I32),
-              (status, "status", b and 2, _I32))
-    _serve("lowbit_kv_release", stream, (done, kv_lens, block_table, free_pages, free_count, status), lambda s: lib.lowbit_kv_release(
-        p[0], B, page_tokens, p[1], p[2], table_stride, p[3], free_capacity, p[4], p[5], s))
+    one = 1 if B > 0 else 0
+    args = (_flat(done, "done", B, _I32), B, page_tokens, _flat(kv_lens, "kv_lens", B, _I32),
+            _flat(block_table, "block_table", B * table_stride, _I32), table_stride, _flat(free_pages, "free_pages", free_capacity, _I32),
+            free_capacity, _flat(free_count, "free_count", one, _I32), _flat(status, "status", 2 * one, _I32))
+    _call("lowbit_kv_release", lib.lowbit_kv_release, stream, (done, kv_lens, block_table, free_pages, free_count, status), args)
 
 
 def lowbit_kv_append(dtype, k, v, T, kv_heads, head_dim, slots, cache, pages, page_tokens, k_stride=None, v_stride=None, stream=None):
     """k, v: [T][kv_heads][head_dim] tensors (any token stride), or addresses with k_stride, v_stride."""
-    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
-    (pk, sk), (pv, sv) = (_row_arg(t, n, dtype, T, kv_heads, head_dim, st) for t, n, st in ((k, "k", k_stride), (v, "v", v_stride)))
-    ps, pc = _flat((slots, "slots", _size(T), (torch.int64,)), (cache, "cache", nb if T > 0 else 0))
-    _serve("lowbit_kv_append", stream, (k, v, slots, cache), lambda s: lib.lowbit_kv_append(
-        dtype, pk, sk, pv, sv, T, kv_heads, head_dim, ps, pc, pages, page_tokens, s))
+    pk, sk = _row_arg(k, "k", dtype, T, kv_heads, head_dim, k_stride)
+    pv, sv = _row_arg(v, "v", dtype, T, kv_heads, head_dim, v_stride)
+    nb = lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim) if T > 0 else 0
+    args = (dtype, pk, sk, pv, sv, T, kv_heads, head_dim, _flat(slots, "slots", T, _I64T), _flat(cache, "cache", nb, None), pages, page_tokens)
+    _call("lowbit_kv_append", lib.lowbit_kv_append, stream, (k, v, slots, cache), args)
 
 
 def lowbit_kv_read(dtype, cache, pages, page_tokens, T, kv_heads, head_dim, slots, k, v, k_stride=None, v_stride=None, stream=None):
     """The rows of `slots` as the cache holds them, into k and v ([T][kv_heads][head_dim], any token stride)."""
-    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
-    (pk, sk), (pv, sv) = (_row_arg(t, n, dtype, T, kv_heads, head_dim, st) for t, n, st in ((k, "k", k_stride), (v, "v", v_stride)))
-    ps, pc = _flat((slots, "slots", _size(T), (torch.int64,)), (cache, "cache", nb if T > 0 else 0))
-    _serve("lowbit_kv_read", stream, (k, v, slots, cache), lambda s: lib.lowbit_kv_read(
-        dtype, pc, pages, page_tokens, T, kv_heads, head_dim, ps, pk, sk, pv, sv, s))
+    pk, sk = _row_arg(k, "k", dtype, T, kv_heads, head_dim, k_stride)
+    pv, sv = _row_arg(v, "v", dtype, T, kv_heads, head_dim, v_stride)
+    nb = lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim) if T > 0 else 0
+    args = (dtype, _flat(cache, "cache", nb, None), pages, page_tokens, T, kv_heads, head_dim, _flat(slots, "slots", T, _I64T), pk, sk, pv, sv)
+    _call("lowbit_kv_read", lib.lowbit_kv_read, stream, (k, v, slots, cache), args)
 
 
 def lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window=0) -> int:
     return lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
+
+
+def _workspace(need, out, stream):
+    """`need` bytes of torch's allocator, of the stream the call runs on: so that nothing else gets them while that
+    stream still works on them."""
+    dev = out.device if isinstance(out, _Tensor) and out.is_cuda else None
+    if stream is None or dev is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev if dev is not None else "cuda")
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if raw == _raw_stream(dev.index):
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev)):
+        return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 def lowbit_kv_attention(dtype, q, T, B, q_heads, kv_heads, head_dim, cu_q, kv_lens, block_table, table_stride, cache, pages,
@@ -370,45 +403,43 @@ def lowbit_kv_attention(dtype, q, T, B, q_heads, kv_heads, head_dim, cu_q, kv_le
     """q, out: [T][q_heads][head_dim] tensors (any token stride), or addresses with q_stride, out_stride.
     workspace: a tensor of at least lowbit_kv_attention_workspace(...) bytes; by default one is taken from torch's
     allocator for the stream the call runs on."""
-    nb = max(lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim), 0)
+    pq, sq = _row_arg(q, "q", dtype, T, q_heads, head_dim, q_stride)
+    po, so = _row_arg(out, "out", dtype, T, q_heads, head_dim, out_stride)
     some = T > 0 and B > 0
-    (pq, sq), (po, so) = (_row_arg(t, n, dtype, T, q_heads, head_dim, st) for t, n, st in ((q, "q", q_stride), (out, "out", out_stride)))
-    pcu, pl, pt, pc = _flat((cu_q, "cu_q", _size(B) + 1 if some else 0, _I32), (kv_lens, "kv_lens", _size(B) if some else 0, _I32),
-                            (block_table, "block_table", _size(B, table_stride) if some else 0, _I32),
-                            (cache, "cache", nb if some else 0))
+    nb = lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim) if some else 0
+    b = B if some else 0
+    pcu, pl = _flat(cu_q, "cu_q", B + 1 if some else 0, _I32), _flat(kv_lens, "kv_lens", b, _I32)
+    pt, pc = _flat(block_table, "block_table", b * table_stride, _I32), _flat(cache, "cache", nb, None)
     need = lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
-
-    def call(s):
-        ws = workspace
-        if ws is None and need > 0:
-            at = out if isinstance(out, torch.Tensor) else None
-            dev = at.device if at is not None else torch.device("cuda", torch.cuda.current_device())
-            if s == torch.cuda.current_stream(dev).cuda_stream:
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            else:  # of the other stream's own, so that nothing else gets it while that stream still works on it
-                with torch.cuda.stream(torch.cuda.ExternalStream(s or 0, device=dev)):
-                    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        have = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else max(need, 0)
-        (pw,) = _flat((ws, "workspace", max(need, 0)))
-        return lib.lowbit_kv_attention(dtype, pq, sq, T, B, q_heads, kv_heads, head_dim, pcu, pl, pt, table_stride, pc, pages,
-                                       page_tokens, max_q, max_kv, float(scale), window, po, so, pw, have, s)
-
-    _serve("lowbit_kv_attention", stream, (q, out, cu_q, kv_lens, block_table, cache, workspace), call)
+    if workspace is None and need > 0:
+        workspace = _workspace(need, out, stream)
+    pw = _flat(workspace, "workspace", need, None)
+    args = (dtype, pq, sq, T, B, q_heads, kv_heads, head_dim, pcu, pl, pt, table_stride, pc, pages, page_tokens, max_q, max_kv,
+            float(scale), window, po, so, pw, need if need > 0 else 0)
+    _call("lowbit_kv_attention", lib.lowbit_kv_attention, stream, (q, out, cu_q, kv_lens, block_table, cache, workspace), args)
 
 
-def _matrix(t, name, rows, width, types):
-    """A [rows][>= width] matrix with dense rows: (address, row stride in elements).  width None: any."""
+def _matrix(t, name, rows, width, dtype, other=None):
+    """A [rows][>= width] matrix with dense rows: (address, row stride in elements).  width None: any, but then
+    contiguous.  other: a second type that is accepted."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor) or t.dtype not in types:
-        raise ValueError(f"{name}: a tensor of one of {[str(d) for d in types]} is required")
-    if t.dim() != 2 or t.shape[0] < rows or (width is not None and t.shape[1] < width):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, needs at least [{rows}, {width if width is not None else 'any'}]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if not isinstance(t, _Tensor) or (t.dtype is not dtype and (other is None or t.dtype is not other)):
+        raise ValueError(f"{name}: a tensor of {dtype} is required")
+    shape, steps = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or (width is not None and shape[1] < width):
+        raise ValueError(f"{name}: shape {tuple(shape)}, needs at least [{rows}, {width if width is not None else 'any'}]")
+    if width is None:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous tensor required")
+        return t.data_ptr(), shape[1]
+    if shape[1] > 1 and steps[1] != 1:
         raise ValueError(f"{name}: dense rows required")
-    step = t.stride(0) if rows > 1 else max(t.stride(0), t.shape[1])
-    if rows > 1 and step < t.shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
+    step = steps[0]
+    if step < shape[1]:
+        if rows > 1:
+            raise ValueError(f"{name}: rows must not overlap")
+        step = shape[1]
     return t.data_ptr(), step
 
 
@@ -416,28 +447,21 @@ def lowbit_logits_process(dtype, logits, B, V, out, tokens=None, prompt_lens=Non
                           frequency=None, bias_tokens=None, bias_values=None, bias_lens=None, mask=None, stream=None):
     """logits, out [B][>= V] (out may be logits); tokens, bias_tokens, bias_values int32/int32/fp32 matrices with a
     row a request; mask: int32 or uint32 words [B][>= ceil(V / 32)]; the rest vectors of B (include/lowbit.h)."""
-    b = _size(B)
-    types = (_DTYPES[dtype],) if dtype in _DTYPES else tuple(_DTYPES.values())
-    pin, sin = _matrix(logits, "logits", b, _size(V), types)
-    po, so = _matrix(out, "out", b, _size(V), types)
+    b, v = max(B, 0), max(V, 0)
+    row = _DTYPES.get(dtype, _F32T)
+    pin, sin = _matrix(logits, "logits", b, v, row)
+    po, so = _matrix(out, "out", b, v, row)
     pt, st = _matrix(tokens, "tokens", b, None, _I32)
-    pm, sm = _matrix(mask, "mask", b, (_size(V) + 31) // 32, (torch.int32, torch.uint32))
-    f32 = (torch.float32,)
-    pp, ptl, pr, pps, pf, pbl = _flat((prompt_lens, "prompt_lens", b, _I32), (total_lens, "total_lens", b, _I32),
-                                      (repetition, "repetition", b, f32), (presence, "presence", b, f32),
-                                      (frequency, "frequency", b, f32), (bias_lens, "bias_lens", b, _I32))
+    pm, sm = _matrix(mask, "mask", b, (v + 31) // 32, _I32, torch.uint32)
     pbt, sbt = _matrix(bias_tokens, "bias_tokens", b, None, _I32)
-    pbv, sbv = _matrix(bias_values, "bias_values", b, None, f32)
-    if bias_tokens is not None:
-        if bias_values is None or bias_values.shape[1] != bias_tokens.shape[1] or sbv != sbt:
-            raise ValueError("bias_values: the shape and row stride of bias_tokens are required")
-        if sbt != bias_tokens.shape[1]:
-            raise ValueError("bias_tokens: contiguous tensor required")
-    if tokens is not None and st != tokens.shape[1]:
-        raise ValueError("tokens: contiguous tensor required")
-    ts = (logits, out, tokens, prompt_lens, total_lens, repetition, presence, frequency, bias_tokens, bias_values, bias_lens, mask)
-    _serve("lowbit_logits_process", stream, ts, lambda s: lib.lowbit_logits_process(
-        dtype, pin, sin, B, V, pt, st, pp, ptl, pr, pps, pf, pbt, pbv, sbt, pbl, pm, sm, po, so, s))
+    pbv, sbv = _matrix(bias_values, "bias_values", b, None, _F32T)
+    if sbt != sbv:
+        raise ValueError("bias_values: the shape of bias_tokens is required")
+    args = (dtype, pin, sin, B, V, pt, st, _flat(prompt_lens, "prompt_lens", b, _I32), _flat(total_lens, "total_lens", b, _I32),
+            _flat(repetition, "repetition", b, _F32T), _flat(presence, "presence", b, _F32T), _flat(frequency, "frequency", b, _F32T),
+            pbt, pbv, sbt, _flat(bias_lens, "bias_lens", b, _I32), pm, sm, po, so)
+    _call("lowbit_logits_process", lib.lowbit_logits_process, stream, (logits, out, tokens, prompt_lens, total_lens, repetition, presence,
+                                                                       frequency, bias_tokens, bias_values, bias_lens, mask), args)
 
 
 class Batch:
