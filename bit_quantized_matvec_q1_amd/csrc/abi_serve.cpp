@@ -119,8 +119,9 @@ static lb_status rows_common(const char *fn, int dtype, const void *k, int64_t k
     lb_status st = check_cache(fn, pages, kv_heads, page_tokens, head_dim);
     if (st != LB_OK)
         return st;
-    if (T < 0 || T * kv_heads > kMax)
-        return lb::abi_fail(LB_ESHAPE, fn, "negative T, or T * kv_heads over 2^31-1");
+    // a launch's threads are numbered in 32 bits, head_dim / 8 of them a row and head
+    if (T < 0 || T > kMax || (T + 31) * kv_heads * (head_dim / 8) >= (int64_t)1 << 32)
+        return lb::abi_fail(LB_ESHAPE, fn, "negative T, or T * kv_heads * head_dim of 2^35 or more");
     if (T == 0)
         return LB_OK;
     if (!slots || (!cache && pages))

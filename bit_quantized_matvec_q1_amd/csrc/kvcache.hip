@@ -11,17 +11,12 @@ namespace lb {
 
 constexpr uint32_t F16_NAN = 0x7e00u;
 
-// maximum over aligned groups of 4 (quads) or 16 lanes, of bit patterns of magnitudes: a NaN's pattern is above
-// an infinity's, and that above every number's
-template <int L> __device__ __forceinline__ uint32_t group_umax(uint32_t v)
+// maximum over quads of lanes of bit patterns of magnitudes: a NaN's pattern is above an infinity's, and that above
+// every number's
+__device__ __forceinline__ uint32_t quad_umax(uint32_t v)
 {
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false)); // quad_perm [1,0,3,2]
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false)); // quad_perm [2,3,0,1]
-    if (L == 16) {
-        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false)); // row_half_mirror
-        v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false)); // row_mirror
-    }
-    return v;
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false)); // quad_perm [2,3,0,1]
 }
 
 // The block's scale from its magnitude's bit pattern: saturated at the largest binary16, NaN if a value is not
@@ -60,72 +55,91 @@ __device__ __forceinline__ Slot slot_of(const RowsArgs &a, int64_t t, int head, 
     return {a.cache + ((s >> shift) * a.kv_heads + head) * kv_record_bytes((int64_t)1 << shift, a.head_dim), (int)(s & ((1 << shift) - 1))};
 }
 
-// 16 lanes a row (token and head).  Keys: a lane takes D/16 consecutive elements.  Values: a lane takes the
-// column c = lane, elements 16 n + c, whose codes are its D/32 consecutive bytes of the record.
+// Eight values' codes, element i in nibble i, for the scale d (0 and NaN: none).
+template <int DT> __device__ __forceinline__ uint32_t eight_codes(const float (&x)[8], float d)
+{
+    if (!(d > 0.0f))
+        return 0;
+    uint32_t w = 0;
+    if constexpr (DT == LB_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            w |= e2m1_code(x[i], d) << (4 * i);
+    } else {
+        // 16-bit values: x has at most 11 bits and d * border 14, so x / d is either a border or over 2^-15 of itself
+        // away from it, and a quotient right to 2^-23, and exact where it is a short number, rounds as the true one
+        // does, to the nearest and ties to even, by the conversion.  (fp32 values can lie closer to a border than
+        // their quotient's rounding, hence the comparisons.)  Past 6 it saturates.
+        const float r = __builtin_amdgcn_rcpf(d);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float t = x[i] * r;
+            y[i] = fmaf(fmaf(-t, d, x[i]), r, t); // also makes a -0 a 0
+        }
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], 1.0f, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 1.0f, 2);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 1.0f, 3);
+    }
+    return w;
+}
+
+// A workgroup takes 2048 / D tokens of one head, as the four tokens of a quad share the lines of its value codes and
+// scales: written from different workgroups, and so from different L2s, each line would go out in parts.  A lane has
+// a quarter of a block, 8 consecutive elements, of a row's key and of its value.  The key's four bytes of codes lie
+// together in the record.  The value's go through LDS: there a row's bytes are in the record's order (column c =
+// element mod 16, then block), each made of two lanes' codes, and every lane takes four of them.
 template <int DT, int D> __global__ __launch_bounds__(256) void append_kernel(RowsArgs a, int shift)
 {
     using R = RowType<DT>;
-    constexpr int E = D / 16, NB = D / 32;
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    if (row >= a.T * a.kv_heads) // whole groups of 16 lanes leave: the DPP maxima stay within a group
-        return;
-    const int64_t t = row / a.kv_heads;
-    const int head = (int)(row - t * a.kv_heads), P = 1 << shift, c = threadIdx.x & 15;
-    const Slot s = slot_of(a, t, head, shift);
+    constexpr int LR = D / 8, NB = D / 32; // lanes a row
+    __shared__ uint32_t lds[256];
+    const uint32_t group = blockIdx.x / (uint32_t)a.kv_heads;
+    const int64_t t = (int64_t)group * (256 / LR) + threadIdx.x / LR;
+    const int head = (int)(blockIdx.x - group * (uint32_t)a.kv_heads), P = 1 << shift;
+    const int at = threadIdx.x % LR, b = at >> 2, g = at & 3;
+    const bool row = t < a.T;
+    Slot s = {nullptr, 0};
+    if (row)
+        s = slot_of(a, t, head, shift);
+    uint32_t wv = 0;
+    if (s.rec) { // whole rows: the quads' maxima stay within them
+        auto load = [&](const void *p, int64_t stride, float (&x)[8]) {
+            const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(static_cast<const typename R::T *>(p) + t * stride + (int64_t)head * D + 8 * at);
+            uint32_t am = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                x[i] = R::get(v.v[i]);
+                am = max(am, __float_as_uint(x[i]) & 0x7fffffffu);
+            }
+            return am;
+        };
+        float xk[8], xv[8];
+        const uint32_t ak = load(a.k, a.k_stride, xk), av = load(a.v, a.v_stride, xv);
+        const uint32_t dk = scale_bits(quad_umax(ak)), dv = scale_bits(quad_umax(av));
+        *reinterpret_cast<uint32_t *>(s.rec + kv_k_byte(D, s.o, g, b)) = eight_codes<DT>(xk, half_bits_to_float((uint16_t)dk));
+        wv = eight_codes<DT>(xv, half_bits_to_float((uint16_t)dv));
+        if (g < 2) // one lane of a block writes the key's scale, another the value's
+            *reinterpret_cast<uint16_t *>(s.rec + kv_scale_byte(P, D, g, s.o, b)) = (uint16_t)(g ? dv : dk);
+    }
+    // columns 8 (g & 1) + 0, 2, 4, 6 in the lanes with the lower codes (g < 2), and 1, 3, 5, 7 in the others
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)wv, 0x4E, 0xF, 0xF, false); // quad_perm [2,3,0,1]
+    const uint32_t bytes = g < 2 ? (wv & 0x0f0f0f0fu) | ((other & 0x0f0f0f0fu) << 4) : ((other >> 4) & 0x0f0f0f0fu) | (wv & 0xf0f0f0f0u);
+    uint8_t *mine = reinterpret_cast<uint8_t *>(lds) + threadIdx.x / LR * (D / 2);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        mine[(8 * (g & 1) + 2 * j + (g >> 1)) * NB + b] = (uint8_t)(bytes >> (8 * j));
+    __syncthreads();
     if (!s.rec)
         return;
-    const typename R::T *k = static_cast<const typename R::T *>(a.k) + t * a.k_stride + (int64_t)head * D;
-    const typename R::T *v = static_cast<const typename R::T *>(a.v) + t * a.v_stride + (int64_t)head * D;
-
-    // keys, in runs of 8 elements (a quarter g of a block b, four codes' bytes each in the record); D = 64 has
-    // half a run a lane
-    constexpr int RUN = E < 8 ? E : 8, LB = 32 / RUN; // lanes a block
-    static_assert(LB == 4 || LB == 8, "");
-#pragma unroll
-    for (int r = 0; r < E / RUN; r++) {
-        const int e0 = (r * 16 + c) * RUN; // first element
-        const RowVec<DT, RUN> x = *reinterpret_cast<const RowVec<DT, RUN> *>(k + e0);
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < RUN; i++)
-            am = max(am, __float_as_uint(R::get(x.v[i])) & 0x7fffffffu);
-        am = group_umax<4>(am);
-        if (LB == 8)
-            am = max(am, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)am, 0x141, 0xF, 0xF, false)); // row_half_mirror
-        const uint32_t sb = scale_bits(am);
-        const float d = half_bits_to_float((uint16_t)sb);
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < RUN; i++)
-            w |= (d > 0.0f ? e2m1_code(R::get(x.v[i]), d) : 0u) << (4 * i);
-        uint8_t *to = s.rec + kv_k_byte(D, s.o, (e0 >> 3) & 3, e0 >> 5) + (e0 & 7) / 2;
-        if constexpr (RUN == 8)
-            *reinterpret_cast<uint32_t *>(to) = w;
-        else
-            *reinterpret_cast<uint16_t *>(to) = (uint16_t)w;
-        if ((e0 & 31) == 0)
-            *reinterpret_cast<uint16_t *>(s.rec + kv_scale_byte(P, D, 0, s.o, e0 >> 5)) = (uint16_t)sb;
+    const uint32_t out = lds[threadIdx.x]; // bytes 4 at .. 4 at + 3 of the row
+    if constexpr (NB == 2) { // two columns
+        *reinterpret_cast<uint16_t *>(s.rec + kv_v_byte(P, D, s.o, 2 * at)) = (uint16_t)out;
+        *reinterpret_cast<uint16_t *>(s.rec + kv_v_byte(P, D, s.o, 2 * at + 1)) = (uint16_t)(out >> 16);
+    } else {
+        *reinterpret_cast<uint32_t *>(s.rec + kv_v_byte(P, D, s.o, at * 4 / NB) + at * 4 % NB) = out;
     }
-
-    uint64_t w = 0;
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-        const float x0 = R::get(v[32 * b + c]), x1 = R::get(v[32 * b + 16 + c]);
-        const uint32_t am = group_umax<16>(max(__float_as_uint(x0) & 0x7fffffffu, __float_as_uint(x1) & 0x7fffffffu));
-        const uint32_t sb = scale_bits(am);
-        const float d = half_bits_to_float((uint16_t)sb);
-        if (d > 0.0f)
-            w |= (uint64_t)(e2m1_code(x0, d) | e2m1_code(x1, d) << 4) << (8 * b);
-        if (c == 0)
-            *reinterpret_cast<uint16_t *>(s.rec + kv_scale_byte(P, D, 1, s.o, b)) = (uint16_t)sb;
-    }
-    uint8_t *to = s.rec + kv_v_byte(P, D, s.o, c);
-    if constexpr (NB == 2)
-        *reinterpret_cast<uint16_t *>(to) = (uint16_t)w;
-    else if constexpr (NB == 4)
-        *reinterpret_cast<uint32_t *>(to) = (uint32_t)w;
-    else
-        *reinterpret_cast<uint64_t *>(to) = w;
 }
 
 // A lane gives 8 consecutive elements of a row's key and of its value; a row without a slot is zeros.
@@ -133,11 +147,11 @@ template <int DT, int D> __global__ __launch_bounds__(256) void read_kernel(Rows
 {
     using R = RowType<DT>;
     constexpr int LR = D / 8, NB = D / 32; // lanes a row
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LR;
-    if (row >= a.T * a.kv_heads)
+    const uint32_t group = blockIdx.x / (uint32_t)a.kv_heads;
+    const int64_t t = (int64_t)group * (256 / LR) + threadIdx.x / LR;
+    const int head = (int)(blockIdx.x - group * (uint32_t)a.kv_heads), P = 1 << shift, e0 = (threadIdx.x % LR) * 8, b = e0 >> 5;
+    if (t >= a.T)
         return;
-    const int64_t t = row / a.kv_heads;
-    const int head = (int)(row - t * a.kv_heads), P = 1 << shift, e0 = (threadIdx.x % LR) * 8, b = e0 >> 5;
     const Slot s = slot_of(a, t, head, shift);
     float xk[8], xv[8];
     if (s.rec) {
@@ -183,9 +197,8 @@ static int log2_of(int64_t p)
 template <int DT> static hipError_t rows_d(const RowsArgs &a, bool append, hipStream_t s)
 {
     const int shift = log2_of(a.page_tokens);
-    const int64_t rows = a.T * a.kv_heads;
-    const int per = append ? 16 : 2048 / (int)a.head_dim; // rows a workgroup
-    const dim3 grid((unsigned)((rows + per - 1) / per));
+    const int per = 2048 / (int)a.head_dim; // tokens a workgroup
+    const dim3 grid((unsigned)((a.T + per - 1) / per * a.kv_heads));
 #define LB_ROWS(d)                                                                                            \
     case d:                                                                                                   \
         if (append)                                                                                           \
