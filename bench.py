@@ -157,20 +157,79 @@ class DecodeToken:
 FEEDS = {"attn_q": 0, "attn_k": 0, "attn_v": 0, "attn_output": 1, "ffn_gate": 2, "ffn_up": 2, "ffn_down": 3}
 
 
+class TokenCache:
+    """A request's 4-bit key and value caches, one a layer, with `context` tokens in them (random codes, the scales
+    of rows of unit variance), and the steps that a token takes with them: its page and slot, once; then in every
+    layer its key and value into the cache, and its attention over all of it.  The length is not carried on, so
+    that every replay does the same work."""
+
+    PAGE, D = 32, 128
+
+    def __init__(self, tok, context):
+        import torch
+
+        self.tok, self.L, self.context = tok, tok.L, context
+        rows = {p["name"]: p["N"] for p in tok.products if p["layer"] == 0}
+        self.hq, self.hk = rows["attn_q"] // self.D, rows["attn_k"] // self.D
+        self.pages = -(-(context + 1) // self.PAGE) + 1
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        g = torch.Generator(device="cuda")
+        g.manual_seed(context)
+        order = torch.randperm(self.pages, generator=g, device="cuda").to(torch.int32)
+        held = -(-context // self.PAGE)
+        self.table = torch.full((1, self.pages), -1, dtype=torch.int32, device="cuda")
+        self.table[0, :held] = order[:held]
+        self.free, self.count = order[held:].contiguous(), i32([self.pages - held])
+        self.new, self.lens = i32([1]), i32([context])
+        self.lens_out, self.count_out, self.cu, self.cu_pages = i32([0]), i32([0]), i32([0, 0]), i32([0, 0])
+        self.slots, self.positions, self.status = torch.zeros(1, dtype=torch.int64, device="cuda"), i32([0]), i32([0, 0, 0])
+        codes = self.PAGE * self.D  # bytes of codes in a record; the scales follow
+        nbytes = self.L.lowbit_kv_cache_bytes(self.pages, self.hk, self.PAGE, self.D)
+        self.caches = []
+        for _ in range(tok.layers):
+            c = torch.randint(0, 256, (self.pages * self.hk, nbytes // (self.pages * self.hk)), dtype=torch.uint8, device="cuda", generator=g)
+            d = torch.rand(c.shape[0], (c.shape[1] - codes) // 2, device="cuda", generator=g).mul_(0.3).add_(0.25).to(torch.float16)
+            c[:, codes:] = d.view(torch.uint8)
+            self.caches.append(c)
+        need = self.L.lowbit_kv_attention_workspace(1, 1, self.hq, self.hk, self.D, 1, context + 1)
+        self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        self.y = {(p["layer"], p["name"]): p["y"] for p in tok.products}
+        self.bytes = tok.layers * (context + 1) * self.hk * self.D * 9 // 8
+
+    def plan(self):
+        self.L.lowbit_kv_plan(self.new, 1, self.PAGE, self.lens, self.lens_out, self.table, self.pages, self.free, self.count,
+                              self.count_out, self.cu, self.cu_pages, self.slots, self.positions, 1, self.status)
+
+    def attend(self, l):
+        L, hq, hk, D = self.L, self.hq, self.hk, self.D
+        q, k, v = (self.y[l, n].view(1, -1, D) for n in ("attn_q", "attn_k", "attn_v"))
+        K, r = self.tok.row_of[l, FEEDS["attn_output"]]
+        out = self.tok.x[K][r].view(1, hq, D)
+        L.lowbit_kv_append(L.F32, k, v, 1, hk, D, self.slots, self.caches[l], self.pages, self.PAGE)
+        L.lowbit_kv_attention(L.F32, q, 1, 1, hq, hk, D, self.cu, self.lens_out, self.table, self.pages, self.caches[l], self.pages,
+                              self.PAGE, 1, self.context + 1, D ** -0.5, out, workspace=self.workspace)
+
+
 class LayeredGraph:
     """A token in dependency order: per layer, the q/k/v products, then o, then gate/up, then down, captured
     once as a HIP graph and replayed.  Each phase is one batched launch after the quantisation of its own
     input row (288 launches for 36 layers), or, fused (ggml formats), one batched launch whose fp32 input
     the batch quantises itself (inside the launch; the long down-projection row by a quantise launch the
-    batch makes ahead of it: 180 launches)."""
+    batch makes ahead of it: 180 launches).  With context > 0 the token follows that many others: a layer's key
+    and value go into its 4-bit cache between the q/k/v phase and the o phase, and the attention over the cache
+    gives the o phase's input."""
 
-    def __init__(self, tok, fused=False):
+    def __init__(self, tok, fused=False, context=0):
         import torch
 
         L = tok.L
         self.tok, self.phases, self.fused = tok, [], fused
+        self.cache = TokenCache(tok, context) if context else None
+        self.after = {}  # phase index -> layer whose cache and attention follow it
         for l in range(tok.layers):
             for f in range(4):
+                if f == 0 and self.cache:
+                    self.after[len(self.phases)] = l
                 prods = [p for p in tok.products if p["layer"] == l and FEEDS[p["name"]] == f]
                 if not prods:
                     continue
@@ -194,12 +253,17 @@ class LayeredGraph:
 
     def eager(self):
         t, L = self.tok, self.tok.L
-        for K, r, b in self.phases:
+        if self.cache:
+            self.cache.plan()
+        for i, (K, r, b) in enumerate(self.phases):
             if not self.fused:
                 L.lowbit_quantize_act(t.afmt, t.x[K][r:r + 1], 1, K, t.xq[K][r:r + 1], t.xs[K][r:r + 1])
             b.run()
+            if i in self.after:
+                self.cache.attend(self.after[i])
 
     def launches(self):
+        """Launches of the products (the cache's and the attention's not among them)."""
         return sum(b.launches() for _, _, b in self.phases) + (0 if self.fused else len(self.phases))
 
     def close(self):
@@ -765,7 +829,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=300)
     ap.add_argument("--no-cpu-baseline", action="store_true", help="skip the oracle leg (profiling runs)")
     ap.add_argument("--secondary", default="layered,q1,planar,b3,q8,prefill,single",
-                    help="comma list of extra workloads: layered, q1, planar, b3, q8, prefill, single, none")
+                    help="comma list of extra workloads: layered, q1, planar, b3, q8, prefill, single, none; and context "
+                         "(not among the default ones): the dependency-ordered token with a 4-bit key/value cache")
     args = ap.parse_args()
     if args.gpus != 1:
         print(f"bench.py runs on one GPU: this library has no multi-GPU path (asked for --gpus {args.gpus}). "
@@ -899,6 +964,17 @@ def main():
     if "layered" in args.secondary.split(","):
         for key, v in layered.items():
             secondary["q2_0_8b_token_layered_graph" + ("" if key == "fused" else "_" + key)] = v
+    if "context" in args.secondary.split(","):
+        for context in (1024, 8192, 32768):
+            lg = LayeredGraph(tok, fused=True, context=context)
+            ms = time_graph(lg, max(20, args.steps // 4), 20)
+            secondary[f"q2_0_8b_token_layered_graph_context_{context}"] = {
+                "ms_per_token": round(ms, 5), "cache_bytes": lg.cache.bytes, "weight_bytes": tok.weight_bytes,
+                "gbs": round((tok.weight_bytes + lg.cache.bytes) / (ms * 1e-3) / 1e9, 1)}
+            log(f"layered token after {context} tokens: {ms:.4f} ms")
+            lg.close()
+            del lg
+            torch.cuda.empty_cache()
     tok.batch.close()
     del tok
     torch.cuda.empty_cache()
