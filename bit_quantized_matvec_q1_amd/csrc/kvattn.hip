@@ -100,14 +100,16 @@ template <int N> __device__ __forceinline__ float sum_columns(float v)
 
 template <int D, bool PACK> using Partial = PartialOf<D, Shape<D, PACK>::ROWS, 16>; // of a tile and chunk, in the workspace
 
-// waves a SIMD that the registers have to leave room for
-template <int DT, int D, bool PACK> constexpr int attn_waves()
+// Workgroups a CU (waves a SIMD) that the registers have to leave room for.
+constexpr int attn_waves(bool split, int D, bool pack)
 {
-    return PACK ? (D == 256 ? 2 : DT == LB_F32 ? 3 : 4) : D == 256 ? 1 : D == 128 ? (DT == LB_F32 ? 2 : 3) : 4;
+    if (pack)
+        return D == 256 ? 2 : D == 128 ? 4 : 5;
+    return D == 256 ? 1 : D == 128 ? (split ? 2 : 3) : 4;
 }
 
 template <int DT, int D, bool PACK>
-__global__ __launch_bounds__(64 * ATT_WAVES, (attn_waves<DT, D, PACK>())) void attn_kernel(AttnArgs a, Geo geo)
+__global__ __launch_bounds__(64 * ATT_WAVES, attn_waves(DT == LB_F32, D, PACK)) void attn_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
     using S = Shape<D, PACK>;
@@ -115,8 +117,11 @@ __global__ __launch_bounds__(64 * ATT_WAVES, (attn_waves<DT, D, PACK>())) void a
     constexpr int NB = D / 32, NC = D / 16, ROWS = S::ROWS;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const uint32_t sh = blockIdx.x / (uint32_t)geo.nsplit, slot = sh / (uint32_t)a.kv_heads;
-    const int split = (int)(blockIdx.x - sh * geo.nsplit), head = (int)(sh - slot * (uint32_t)a.kv_heads);
+    // All tiles' first chunks, then their second ones: workgroups go round the eight XCDs in order, and with a tile's
+    // chunks side by side, eight of them, the first chunks, which every request has, would all land on one (64
+    // requests of very different lengths: 137 us, and 101 us so).
+    const uint32_t split_u = blockIdx.x / geo.tiles, sh = blockIdx.x - split_u * geo.tiles, slot = sh / (uint32_t)a.kv_heads;
+    const int split = (int)split_u, head = (int)(sh - slot * (uint32_t)a.kv_heads);
     const Tile t = tile_of(a, geo, slot, ROWS);
     if (t.row0 >= t.rows)
         return;
@@ -454,7 +459,7 @@ static Geo geometry(int dtype, const AttnArgs &a)
     // fp32 rows need the wide kernel's exact keys and split operands
     g.kind = most <= packed ? Geo::PACKED : most <= PROMPT_FROM || dtype == LB_F32 ? Geo::WIDE : Geo::PROMPT;
     g.tile = g.kind == Geo::PACKED ? packed : g.kind == Geo::WIDE ? ATT_ROWS : PROMPT_ROWS;
-    if (g.kind == Geo::PROMPT && a.head_dim <= 128 && a.T * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= ATT_FILL / 2)
+    if (g.kind == Geo::PROMPT && a.head_dim <= 128 && a.T * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= 512)
         g.tile = 2 * PROMPT_ROWS;
     g.by_request = most <= g.tile;
     g.rows = (int)(g.by_request ? most : g.tile);
@@ -463,18 +468,21 @@ static Geo geometry(int dtype, const AttnArgs &a)
     if (a.window > 0)
         span = span < a.window + g.tile + ATT_STEP ? span : a.window + g.tile + ATT_STEP;
     const int64_t tiles = g.slots * a.kv_heads;
-    // Chunks long enough for one round of as many workgroups as fit the chip, so that each one's start (about 3 us;
-    // a chunk of 2048 tokens takes 40) is paid once; but not over 2048 tokens, as lengths may differ, unless there
-    // are several rounds of tiles anyhow.
-    const int64_t fill = g.kind == Geo::PROMPT ? 768 : ATT_FILL;
+    g.tiles = (uint32_t)(tiles < UINT32_MAX ? tiles : UINT32_MAX); // more are refused
+    // Chunks such that the workgroups fill the chip in whole rounds, each one's start (about 3 us; a chunk of 2048
+    // tokens takes 40) being paid once a round; one round, unless the chunks would pass 2048 tokens: lengths may
+    // differ.  Several rounds of tiles are not split at all.
+    const int64_t fill = g.kind == Geo::PROMPT ? 768 : 256 * attn_waves(dtype == LB_F32, (int)a.head_dim, g.kind == Geo::PACKED);
     constexpr int64_t UNIT = ATT_WAVES * ATT_STEP;
-    if (g.kind == Geo::PROMPT && tiles >= 256) { // every CU has one, and a part is 64 KB to write and read again
+    // a prompt's part is 64 KB to write and read again: none where every CU has a tile
+    if (tiles >= (g.kind == Geo::PROMPT ? 256 : 4 * fill)) {
         g.chunk = (int)(span > UNIT ? (span + UNIT - 1) / UNIT * UNIT : UNIT);
         g.nsplit = 1;
         return g;
     }
-    int64_t chunk = (span * tiles / fill + UNIT - 1) / UNIT * UNIT;
-    chunk = chunk < UNIT ? UNIT : chunk > 2048 && tiles < 4 * fill && g.kind != Geo::PROMPT ? 2048 : chunk;
+    const int64_t rounds = g.kind == Geo::PROMPT ? 1 : (span * tiles / fill + 2047) / 2048;
+    int64_t chunk = (span * tiles / (fill * (rounds > 1 ? rounds : 1)) + UNIT - 1) / UNIT * UNIT;
+    chunk = chunk < UNIT ? UNIT : chunk;
     g.chunk = (int)chunk;
     g.nsplit = (int)(span > 0 ? (span + chunk - 1) / chunk : 1);
     return g;

@@ -16,7 +16,6 @@ constexpr int ATT_ROWS = 16;     // query rows a tile
 constexpr int PROMPT_ROWS = 128; // of a prompt's, or twice as many
 constexpr int ATT_STEP = 32;  // tokens a step
 constexpr int ATT_WAVES = 4;
-constexpr int ATT_FILL = 1024;
 // Rows of a request up to which the 16-row tiles are taken: 16 requests of 2000 tokens, 20 / 64 / 96 rows each: 39 /
 // 54 / 88 us with them, 61 / 67 / 70 us with a prompt's; 64 requests of 500: 32 / 53 / 74 against 36 / 43 / 45 us.
 constexpr int PROMPT_FROM = 64;
@@ -109,6 +108,7 @@ struct Geo { // of a launch
     enum { PACKED, WIDE, PROMPT } kind;
     bool by_request; // a request has at most one tile: the tile's slot is the request
     int64_t slots;
+    uint32_t tiles; // slots times kv heads
 };
 
 struct Tile {
