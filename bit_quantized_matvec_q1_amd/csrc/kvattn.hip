@@ -52,9 +52,9 @@ template <int D, bool PACK> struct Step {
     Words<Shape<D, PACK>::SW> ks[2], vs[2]; // [block][token of the quad g], binary16; packed: the lane's block
 };
 
-// A lane's column of queries, elements 32 b + 8 g + j, as binary16 times 2^-e; returns 2^e.
+// A lane's column of queries, elements 32 b + 8 g + j, as binary16 times 2^-e; returns e.
 template <int DT, int D, bool PACK, bool SPLIT>
-__device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, int c, int g, bool negate, f16x8 (&hi)[D / 32], f16x8 (&lo)[SPLIT ? D / 32 : 1])
+__device__ __forceinline__ int load_query(const typename RowType<DT>::T *q, int c, int g, bool negate, f16x8 (&hi)[D / 32], f16x8 (&lo)[SPLIT ? D / 32 : 1])
 {
     constexpr int NB = D / 32;
     if constexpr (PACK) {
@@ -73,7 +73,7 @@ __device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, in
             if constexpr (SPLIT)
                 lo[b] = b == c / ROWS ? l : f16x8{};
         }
-        return ldexpf(1.0f, e);
+        return e;
     } else {
         float x[NB][8], am = 0.0f;
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ float load_query(const typename RowType<DT>::T *q, in
 #pragma unroll
         for (int b = 0; b < NB; b++)
             query_halves<SPLIT>(x[b], e, negate, hi[b], lo[SPLIT ? b : 0]);
-        return ldexpf(1.0f, e);
+        return e;
     }
 }
 
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, attn_waves(DT == LB_F32, D, PACK)) 
     const int from = a.window > 0 ? (int)max((int64_t)0, pos - a.window + 1) : 0; // and the first
     f16x8 qh[NB], ql[SPLIT ? NB : 1];
     const typename R::T *qp = static_cast<const typename R::T *>(a.q) + (int64_t)(a.cu_q[t.b] + tok) * a.q_stride + (int64_t)hq * D;
-    const float qscale = load_query<DT, D, PACK, SPLIT>(qp, c, g, a.scale < 0.0f, qh, ql) * (fabsf(a.scale) * 1.44269504088896341f); // scores in powers of two
+    const float qscale = score_scale(a.scale, load_query<DT, D, PACK, SPLIT>(qp, c, g, a.scale < 0.0f, qh, ql));
 
     f32x4 acc[NC];
 #pragma unroll

@@ -177,6 +177,13 @@ __device__ __forceinline__ int row_exponent(float am)
     }
     return e;
 }
+// What takes a row's scores to powers of two, e its exponent.  Never 0: a masked score of -inf has to stay one (with
+// 2^-100, which a scale of 0 and the smallest queries get, every score that is not is 0 for the exponential).
+__device__ __forceinline__ float score_scale(float scale, int e)
+{
+    const float s = ldexpf(1.0f, e) * (fabsf(scale) * 1.44269504088896341f);
+    return s < 0x1p-100f ? 0x1p-100f : s;
+}
 template <bool SPLIT> __device__ __forceinline__ void query_halves(const float (&x)[8], int e, bool negate, f16x8 &hi, f16x8 &lo)
 {
 #pragma unroll

@@ -92,7 +92,7 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
 #pragma unroll
         for (int k = 0; k < NK; k++)
             query_halves<false>(x[k], e, a.scale < 0.0f, q[k], none);
-        qscale = ldexpf(1.0f, e) * (fabsf(a.scale) * 1.44269504088896341f); // scores in powers of two
+        qscale = score_scale(a.scale, e);
     }
 
     f32x16 acc[NB];

@@ -120,6 +120,16 @@ def test_ranges(kind, v_scale, q_scale):
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("news", [[1, 1], [9, 30], [40, 40]])
+def test_scales_of_zero_below_zero_and_smallest_queries(kind, news):
+    # masked scores stay masked: with a scale of 0 every key that is seen has the same weight
+    for scale, q_scale in ((0.0, 1.0), (-0.3, 1.0), (1.0, {"f16": 2.0**-20, "bf16": 2.0**-130, "f32": 2.0**-146}[kind])):
+        c = Case(21, kind, 64, 16, 4, 1, [41, 70], news, q_scale=q_scale)
+        c.scale = scale
+        c.check(f"scale {scale} queries times {q_scale} {kind} {news}")
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
 def test_values_of_mixed_ranges(kind):
     # a few tokens' values are thousands of times the others', some are all zero
     c = Case(14, kind, 64, 16, 4, 1, [200], [1])
