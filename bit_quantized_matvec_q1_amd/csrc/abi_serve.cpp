@@ -172,8 +172,8 @@ static lb_status attn_sizes(const char *fn, lb::AttnArgs &a, int64_t T, int64_t 
     a.T = T, a.B = B, a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
     // a request has no more new tokens than the step, and a window longer than the cache is none
     a.max_q = max_q < T ? max_q : T, a.max_kv = max_kv, a.window = window >= max_kv ? 0 : window;
-    if (T && B && lb::kv_attention_workgroups(a) >= (1 << 24)) // a launch's threads are numbered in 32 bits
-        return lb::abi_fail(LB_ESHAPE, fn, "the step has 2^24 tiles or more");
+    if (T && B && lb::kv_attention_workgroups(a) >= (1 << 23)) // up to 512 threads each, numbered in 32 bits
+        return lb::abi_fail(LB_ESHAPE, fn, "the step has 2^23 tiles or more");
     return LB_OK;
 }
 

@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, attn_waves(DT == LB_F32, D, PACK)) 
     const int start = t.lo + split * geo.chunk;
     if (split > 0 && start >= t.hi)
         return;
-    const int end = min(t.hi, start + geo.chunk);
+    const int end = start + min(t.hi - start, geo.chunk); // start + chunk can pass 2^31
     const int P = 1 << geo.shift;
 
     // this lane's query row; the rows past the last repeat it, and are not stored

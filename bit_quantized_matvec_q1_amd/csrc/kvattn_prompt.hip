@@ -62,7 +62,7 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
     const int start = t.lo + split * geo.chunk;
     if (split > 0 && start >= t.hi)
         return;
-    const int end = min(t.hi, start + geo.chunk), P = 1 << geo.shift;
+    const int end = start + min(t.hi - start, geo.chunk), P = 1 << geo.shift; // start + chunk can pass 2^31
 
     if (tid < 4)
         s_need[tid >> 1][tid & 1] = 0;

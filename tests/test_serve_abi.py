@@ -68,7 +68,8 @@ def test_attention():
     assert attn(dtype=7) == L.LB_EINVAL
     for bad in (dict(T=-1), dict(B=-1), dict(hq=0), dict(hq=7), dict(hk=0), dict(hk=3), dict(D=112), dict(P=8), dict(P=17), dict(pages=-1),
                 dict(pages=0), dict(max_q=-1), dict(max_kv=-1), dict(window=-1), dict(stride=-1), dict(qs=1016), dict(os=512),
-                dict(T=2**29), dict(max_kv=2**31 - 1), dict(B=1 << 24, T=1 << 24)):
+                dict(T=2**29), dict(max_kv=2**31 - 1), dict(B=1 << 24, T=1 << 24),
+                dict(B=1 << 23, T=1 << 23, hq=1, hk=1, max_q=1)):
         assert attn(**bad) == L.LB_ESHAPE, bad
     for k in ("q", "out", "cu", "lens", "table", "cache"):
         assert attn(**{k: None}) == L.LB_EINVAL, k

@@ -295,3 +295,16 @@ def test_other_streams_graphs_and_workspaces():
         call(q2, again)
         torch.cuda.synchronize()
         assert torch.equal(again, eager)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("lens,news", [([1500, 40], [1, 1]), ([100, 40], [20, 7]), ([300, 80], [130, 40])])
+def test_outputs_in_the_queries_place(kind, lens, news):
+    """Single tokens in several chunks, the 16-row tiles and a prompt's: the same bits as with rows of their own."""
+    say(f"case in place {kind} {news}")
+    c = Case(22, kind, 64, 16, 4, 1, lens, news)
+    apart, q = c.gpu(), c.q.cuda()
+    L.lowbit_kv_attention(TYPES[kind][0], q, c.T, c.B, 4, 1, 64, dev(c.cu), dev(np.array(lens, np.int32)), dev(c.table), c.stride, dev(c.cache),
+                          c.pages, 16, c.max_q, c.max_kv, c.scale, q)
+    rows = c.cu[-1]
+    assert (q.double().cpu().numpy()[:rows] == apart[:rows]).all() and torch.equal(q[rows:].cpu(), c.q[rows:])
