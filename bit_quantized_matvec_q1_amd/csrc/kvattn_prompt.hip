@@ -13,12 +13,19 @@
 // has: tiles of 128 rows (four waves) spend 61 % of the cycles on vector instructions, tiles of 256 (eight waves,
 // each unpacking keys or values) a third less.  One prompt of 8192 tokens, 32 heads over 8: 740 us (745 TFLOP/s, a
 // large library matrix product reaches 1132 here); tiles of 128 rows 835 us, and 16 rows a wave, each unpacking for
-// itself, 1500 us.  LDS reads (16 bytes a lane, 16 KB a wave and 32 tokens) are at a quarter of their rate.
+// itself, 1500 us.  Counted: the matrix cores are busy for 34 % of the cycles and the vector unit for 48 %, the two
+// together leaving under a fifth to waits; raising a wave's priority around its products changes nothing.  Four
+// prompts' chunks of 777 tokens after up to 1800, 20 heads over 5: 108 us, its longest tiles' own time.  LDS reads
+// (16 bytes a lane, 16 KB a wave and 32 tokens) are at a quarter of their rate.
 //
 // Precision: a code times its block's scale is rounded to binary16 (scales have 11 bits and the codes 1.5, 3 and 6
-// two, so some lose one bit), and so are the weights.  The scales are taken times a power of two that brings the
-// largest seen so far to 2^9, for keys and for values, so that no range is lost; it changes, with the tile unpacked
-// again, if a later tile passes it by 2^5.  Scores are kept against a reference a row as in kvattn.hip.
+// two, so some lose one or two), and so are the weights: 2^-11 relative at most each, against the 2^-8 of a bfloat16
+// output, and of the order of a binary16 output's own rounding (on prompts of normal values the keys' rounding gives
+// 3.4e-4 of the result's size, the values' and the weights' 1.9e-4 each, the output's 2.0e-4; all of them 4.4e-4).
+// Keeping the keys' rest in a second number would take half as many matrix instructions again and half as much LDS.
+// The scales are taken times a power of two that brings the largest seen so far to 2^9, for keys and for values, so
+// that no range is lost; it changes, with the tile unpacked again, if a later tile passes it by 2^5.  Scores are kept
+// against a reference a row as in kvattn.hip.
 #include "kvattn_internal.h"
 
 namespace lb {

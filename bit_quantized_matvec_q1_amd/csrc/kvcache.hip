@@ -4,7 +4,9 @@
 // of them has 11 + 3 significant bits: the comparisons |x| against d * border are exact in fp32, without a
 // division, for every input type, and so is the code.
 //
-// Both directions are bound by HBM (2 to 4 bytes a value in or out, 9/16 byte in the cache).
+// Both directions are bound by HBM (2 to 4 bytes a value in or out, 9/16 byte in the cache).  16384 tokens of 8 heads
+// of 128: bfloat16 rows appended in 18.6 us (86 MB, 4.6 TB/s), read back as fp32 in 35 us (153 MB, 4.4 TB/s); a large
+// copy reaches 4.7 to 5.0 here.
 #include "serve_internal.h"
 
 namespace lb {

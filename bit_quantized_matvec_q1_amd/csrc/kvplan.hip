@@ -6,7 +6,8 @@
 // A few KB are moved: the time is launches and dependent loads.  One workgroup computes both sums; where the
 // step is small (a decode step, or a few prompts) the same workgroup also writes the tokens' slots, with the
 // sums in LDS, so there is one launch.  A larger step's slots are written by a second launch over the whole
-// chip, each token finding its request by bisection in the sums.
+// chip, each token finding its request by bisection in the sums.  64 requests of one token: 4.9 us; 512 requests of
+// 400 tokens: 3.8 + 6.5 us.
 #include "serve_internal.h"
 
 namespace lb {

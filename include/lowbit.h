@@ -331,7 +331,7 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  * out may be q, with the same stride, but not overlap it otherwise.
  * fp32 rows are computed to fp32's accuracy (2^-20).  For bf16 and fp16 rows the weights times the values' scales are
  * rounded to binary16 before they meet the values; where requests may have over 64 rows (max_q times q_heads /
- * kv_heads), the keys and values (code times scale) are too, 2^-12 relative at most each.
+ * kv_heads), the keys and values (code times scale) are too, 2^-11 relative at most each.
  * workspace: lowbit_kv_attention_workspace(...) bytes, 16-byte aligned, for the joining of long requests' parts
  * (0 bytes, NULL, where none are split); calls that may run at the same time need one each.
  */
