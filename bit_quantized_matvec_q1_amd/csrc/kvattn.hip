@@ -22,8 +22,8 @@
 //
 // Decode is bound by HBM, so the tokens of one (request, kv head) are cut into chunks, one workgroup each, and the
 // chunks' results joined by a second launch.  Measured at head size 128, four heads a kv head, one new token a
-// request (attention + join): 32 requests of up to 4000 tokens over 5 kv heads, 49 MB of cache, 18.2 + 4.0 us; one of
-// 131071 over 8, 151 MB, 29.4 + 6.3 us (5.1 TB/s); 64 of up to 12345 over 8, 482 MB, 101 + 4.9 us (4.8 TB/s, a plain
+// request (attention + join): 32 requests of up to 4000 tokens over 5 kv heads, 54 MB of cache, 18.2 + 4.0 us; one of
+// 131071 over 8, 151 MB, 29.4 + 6.3 us (5.1 TB/s); 64 of up to 12345 over 8, 537 MB, 101 + 4.9 us (5.3 TB/s, a plain
 // read of as much reaches 6.7).  A copy of the kernel that does nothing but its loads takes 18.0, 27.5 and 95.4 us, so
 // what bounds it is how the pages' records stream in; the vector unit (unpacking, softmax) is at 50 % of its cycles,
 // the matrix cores at 12 %.

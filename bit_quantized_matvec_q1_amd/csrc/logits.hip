@@ -10,8 +10,8 @@
 // stretch in LDS, by integer atomics, whose order does not matter.  Every stretch reads the whole history (from
 // L2, after the first), so the stretches are as long as the number of rows lets them be.  96 fp32 rows of 151669, 6000
 // tokens of history, 64 biases, a mask: 33 us (118 MB, 3.6 TB/s; a plain copy of the rows 24 us); the rest is the
-// histories' reads and the counts' round through LDS, five barriers and three passes over 64 KB.  Stretches of 4096,
-// 8192 or more threads' worth took 33 to 42 us, a bitmap of the touched logits 34.  One row of 128256: 4.4 us.
+// histories' reads and the counts' round through LDS, five barriers and three passes over 64 KB.  Other stretches
+// and sizes of workgroups took 33 to 42 us, a bitmap of the touched logits 34.  One row of 128256: 4.4 us.
 #include "serve_internal.h"
 
 namespace lb {
