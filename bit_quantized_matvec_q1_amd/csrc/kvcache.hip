@@ -1,5 +1,5 @@
 // Rows into the paged 4-bit cache, and back.  32 consecutive values of a head share the scale
-// d = fp16_rne(amax / 6) (the fp32 quotient), and each value becomes the E2M1 number nearest to x / d, ties to
+// d = fp16_rne(amax / 6) (amax times the fp32 number next to 1/6, in fp32), and each value becomes the E2M1 number nearest to x / d, ties to
 // the even code.  The borders between neighbouring E2M1 numbers are .25 .75 1.25 1.75 2.5 3.5 5, and d times one
 // of them has 11 + 3 significant bits: the comparisons |x| against d * border are exact in fp32, without a
 // division, for every input type, and so is the code.
@@ -22,12 +22,13 @@ __device__ __forceinline__ uint32_t quad_umax(uint32_t v)
 }
 
 // The block's scale from its magnitude's bit pattern: saturated at the largest binary16, NaN if a value is not
-// finite (the block then reads back as NaN rather than as some number).
+// finite (the block then reads back as NaN rather than as some number).  The product with 1/6 is what PyTorch makes of
+// a division by 6 on the GPU, so scales computed there have the same bits; it is exact for 6 times a binary16.
 __device__ __forceinline__ uint32_t scale_bits(uint32_t amax)
 {
     if (amax >= 0x7f800000u)
         return F16_NAN;
-    return __half_as_ushort(__float2half_rn(fminf(__uint_as_float(amax) / 6.0f, 65504.0f)));
+    return __half_as_ushort(__float2half_rn(fminf(__uint_as_float(amax) * (1.0f / 6.0f), 65504.0f)));
 }
 
 __device__ __forceinline__ uint32_t e2m1_code(float x, float d)

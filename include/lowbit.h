@@ -260,7 +260,7 @@ lb_status lowbit_matvec_batched_static(const lb_matvec_desc *list, int32_t n, hi
  *
  * The cache of a layer (lowbit_kv_cache_bytes): `pages` pages of page_tokens tokens P (a power of two, 16 to
  * 1024), a record of P * head_dim * 9 / 8 bytes per page and kv head, [pages][kv_heads][record].  32 consecutive
- * values of a head share a binary16 scale d = fp16_rne(amax / 6) (the fp32 quotient, at most 65504), and a code
+ * values of a head share a binary16 scale d = fp16_rne(amax * fp32(1/6)) (an fp32 product, at most 65504), and a code
  * is the E2M1 number (sign, then 0 .5 1 1.5 2 3 4 6) nearest to x / d, ties to the even code; all codes are 0
  * where d = 0, and a block with a value that is not finite reads back as NaN.  With nb = head_dim / 32:
  *   K codes  [P][4][nb][4 bytes]     byte (g, b, i): elements 32b + 8g + 2i (lower code) and 32b + 8g + 2i + 1
@@ -292,7 +292,8 @@ int64_t lowbit_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_toke
  *                      one beyond its table or 2^31 - 1, 8: a free count below 0 or above free_capacity;
  *                      then the pages and the tokens that the step asked for.
  * All or nothing: where status[0] is not 0, no table entry, length or count changes, the sums are 0 and all slots
- * -1, so that the step's other calls do nothing.  One launch up to 2048 requests and max_tokens 8192, else two.
+ * -1, so that the step's other calls do nothing.  B = 0: nothing is read or written, slots included.  One launch up
+ * to 2048 requests and max_tokens 8192, else two.
  */
 lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens, const int32_t *kv_lens, int32_t *kv_lens_out,
                          int32_t *block_table, int64_t table_stride, const int32_t *free_pages, int64_t free_capacity,

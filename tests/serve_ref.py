@@ -17,7 +17,7 @@ def quantise(x):
     amax = a.max(-1)
     fine = np.isfinite(x).all(-1)
     with np.errstate(over="ignore", invalid="ignore"):
-        q = (np.where(fine, amax, 0.0).astype(np.float32) / np.float32(6)).astype(np.float32)
+        q = np.where(fine, amax, 0.0).astype(np.float32) * (np.float32(1) / np.float32(6))  # as the format defines it
         d = np.where(fine, np.minimum(q, np.float32(65504)), np.float32(np.nan)).astype(np.float16)
     codes = np.zeros(x.shape, np.uint8)
     live = fine & (d > 0)

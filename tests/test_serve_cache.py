@@ -194,3 +194,18 @@ def test_release_gives_pages_back(B):
     bad = i32([10**6] + [0] * (B - 1))
     L.lowbit_kv_release(i32([1] * B), B, 16, bad, args[4], args[5], pages, dc, st)
     assert host(st)[0] & 4 and host(bad)[0] == 10**6 and host(dc).tolist() == [len(want)]
+
+
+def test_scales_are_those_of_a_division_on_the_gpu():
+    """Enough blocks that a quotient rounded otherwise in its last bit would show."""
+    say("case scales")
+    T, H, D, P = 8192, 8, 128, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k, v = (torch.randn(T, H, D, generator=g, device="cuda") for _ in range(2))
+    cache = torch.zeros(T // P, H, R.record_bytes(P, D), dtype=torch.uint8, device="cuda")
+    L.lowbit_kv_append(L.F32, k, v, T, H, D, torch.arange(T, device="cuda"), cache, T // P, P)
+    got = cache[:, :, P * D:].contiguous().view(torch.float16).view(T // P, H, 2, P // 4, D // 32, 4)
+    for i, x in enumerate((k, v)):
+        want = (x.view(T // P, P // 4, 4, H, D // 32, 32).abs().amax(-1) / 6).half()
+        assert torch.equal(got[:, :, i], want.permute(0, 3, 1, 4, 2))

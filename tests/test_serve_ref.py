@@ -13,6 +13,15 @@ def test_codes_of_exact_values_and_ties():
     assert c[:16].tolist() == [7, 15, 1, 11, 0, 2, 2, 4, 4, 6, 6, 14, 1, 6, 0, 8]
 
 
+def test_scales_of_six_times_a_binary16_are_exact():
+    m = np.arange(1, 31744, dtype=np.uint16).view(np.float16).astype(np.float64)  # every one above 0
+    m = m[m <= 65504 / 2]
+    x = np.zeros((m.size, 32))
+    x[:, 3] = -6 * m
+    _, d = R.quantise(x)
+    assert np.array_equal(d[:, 0].astype(np.float64), m)
+
+
 def test_nearest_by_brute_force():
     rng = np.random.default_rng(1)
     x = rng.standard_normal((200, 64)).astype(np.float32)
