@@ -50,15 +50,17 @@ template <int D> struct StagedValues { // column i % 16 of two quads of tokens, 
 };
 
 // NW waves of 32 query rows.  With four, every thread unpacks keys and values; with eight, half of the waves do each.
-template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnArgs a, Geo geo)
+// HALVES: waves w and w + NW / 2 have the same rows, and each one half of every 64 tokens; joined at the end.
+template <int DT, int D, int NW, bool HALVES> __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
-    constexpr int NB = D / 32, NK = D / 16, ROWS = 32 * NW;
+    constexpr int NB = D / 32, NK = D / 16, SETS = HALVES ? NW / 2 : NW, ROWS = 32 * SETS;
     constexpr int HALF = PR_TOKENS * D; // binary16 numbers of 64 keys, or values
     __shared__ __align__(16) _Float16 lds[2][2][HALF];
     __shared__ int s_need[2][2], s_nan[2];
+    __shared__ float s_ref[HALVES ? SETS : 1][64], s_sum[HALVES ? SETS : 1][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int c = lane & 31, h = lane >> 5;
+    const int c = lane & 31, h = lane >> 5, set = wave % SETS;
     const bool does_k = NW == 4 || wave < NW / 2, does_v = NW == 4 || wave >= NW / 2;
     const uint32_t sh = blockIdx.x / (uint32_t)geo.nsplit, rev = sh / (uint32_t)a.kv_heads;
     const int split = (int)(blockIdx.x - sh * geo.nsplit), head = (int)(sh - rev * (uint32_t)a.kv_heads);
@@ -77,7 +79,7 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
         s_nan[tid] = 0;
 
     // this lane's query row; the rows past the last repeat it, and are not stored
-    const int w0 = t.row0 + wave * 32;
+    const int w0 = t.row0 + set * 32;
     const bool some = w0 < t.rows; // the wave has rows
     const int row = min(w0 + c, t.rows - 1);
     const int tok = row / geo.G, hq = head * geo.G + row % geo.G;
@@ -310,7 +312,8 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
         const float qs = qscale * ldexpf(1.0f, -shift_k);
         const f16x8 *K = reinterpret_cast<const f16x8 *>(lds[par][0]), *V = reinterpret_cast<const f16x8 *>(lds[par][1]);
 #pragma unroll
-        for (int sub = 0; sub < 2; sub++) {
+        for (int turn = 0; turn < (HALVES ? 1 : 2); turn++) {
+            const int sub = HALVES ? wave / SETS : turn;
             const int j0 = t0 + 32 * sub;
             if (!some || j0 >= end || j0 > pos_z || j0 + 31 < from_a)
                 continue;
@@ -384,16 +387,44 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
             }
         }
     }
+    sum += __shfl_xor(sum, 32);
+    if constexpr (HALVES) { // the second half of the waves hands over, through the LDS of the tiles
+        static_assert(sizeof(lds) >= SETS * 16 * NB * 64 * sizeof(float), "room for the accumulators");
+        float *theirs = reinterpret_cast<float *>(lds) + set * 16 * NB * 64 + lane;
+        __syncthreads();
+        if (wave >= SETS) {
+            s_ref[set][lane] = ref, s_sum[set][lane] = sum;
+#pragma unroll
+            for (int n = 0; n < NB; n++)
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    theirs[(n * 16 + i) * 64] = acc[n][i];
+        }
+        __syncthreads();
+        if (wave >= SETS)
+            return;
+        const float ref2 = s_ref[set][lane], sum2 = s_sum[set][lane], m = fmaxf(ref, ref2);
+        // a half without a score above -inf has a sum of 0, or NaN where a score was
+        const float f = ref > -INFINITY ? exp2_raw(ref - m) : sum, f2 = ref2 > -INFINITY ? exp2_raw(ref2 - m) : sum2;
+        ref = m;
+        sum = fmaf(f, sum, f2 * sum2);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const float fr = __shfl(f, 8 * (i / 4) + 4 * h + i % 4), fr2 = __shfl(f2, 8 * (i / 4) + 4 * h + i % 4);
+#pragma unroll
+            for (int n = 0; n < NB; n++)
+                acc[n][i] = fmaf(fr, acc[n][i], fr2 * theirs[(n * 16 + i) * 64]);
+        }
+    }
     if (!some)
         return;
-    sum += __shfl_xor(sum, 32);
     const float back = ldexpf(1.0f, -shift_v);
     const bool only = t.hi - t.lo <= geo.chunk;
     using Part = PartialOf<D, ROWS, ROWS>;
     Part *part = static_cast<Part *>(a.workspace) + (slot * a.kv_heads + head) * geo.nsplit + split;
     const float inv = t.over ? NAN : sum == 0.0f ? 0.0f : back / sum;
     if (!only && h == 0)
-        part->ref[wave * 32 + c] = ref, part->sum[wave * 32 + c] = sum;
+        part->ref[set * 32 + c] = ref, part->sum[set * 32 + c] = sum;
 #pragma unroll
     for (int i = 0; i < 16; i++) {
         const int r = 8 * (i / 4) + 4 * h + i % 4, rr = w0 + r;
@@ -406,20 +437,27 @@ template <int DT, int D, int NW> __global__ __launch_bounds__(64 * NW, D == 256 
             if (only)
                 op[32 * n + c] = R::put(acc[n][i] * f);
             else
-                part->acc[wave * 32 + r][32 * n + c] = acc[n][i] * back;
+                part->acc[set * 32 + r][32 * n + c] = acc[n][i] * back;
         }
     }
 }
+
+constexpr unsigned PROMPT_HALVES = 512;
 
 template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
 {
     const dim3 grid((unsigned)(g.slots * a.kv_heads * g.nsplit));
     if constexpr (D <= 128) // at 256 the registers are enough for one wave a SIMD
         if (g.tile == 2 * PROMPT_ROWS) {
-            hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 8>), grid, dim3(512), 0, s, a, g);
+            hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 8, false>), grid, dim3(512), 0, s, a, g);
             return hipGetLastError();
         }
-    hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 4>), grid, dim3(256), 0, s, a, g);
+    if constexpr (D <= 128)
+        if (grid.x < PROMPT_HALVES) {
+            hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 8, true>), grid, dim3(512), 0, s, a, g);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 4, false>), grid, dim3(256), 0, s, a, g);
     return hipGetLastError();
 }
 
