@@ -464,7 +464,11 @@ static Geo geometry(int dtype, const AttnArgs &a)
     // fp32 rows need the wide kernel's exact keys and split operands
     g.kind = most <= packed ? Geo::PACKED : most <= PROMPT_FROM || dtype == LB_F32 ? Geo::WIDE : Geo::PROMPT;
     g.tile = g.kind == Geo::PACKED ? packed : g.kind == Geo::WIDE ? ATT_ROWS : PROMPT_ROWS;
-    if (g.kind == Geo::PROMPT && a.head_dim <= 128 && a.T * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= 512)
+    // Larger tiles where every CU gets two of them.  They are counted from what the requests may bring, not from the
+    // rows of a padded step, so that there really are as many: tiles of 256 rows are never split (below), and the
+    // parts and their join know 128.
+    const int64_t real = a.T < a.B * a.max_q ? a.T : a.B * a.max_q;
+    if (g.kind == Geo::PROMPT && a.head_dim <= 128 && real * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= 512)
         g.tile = 2 * PROMPT_ROWS;
     g.by_request = most <= g.tile;
     g.rows = (int)(g.by_request ? most : g.tile);
