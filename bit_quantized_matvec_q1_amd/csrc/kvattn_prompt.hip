@@ -50,7 +50,8 @@ template <int D> struct StagedValues { // column i % 16 of two quads of tokens, 
 };
 
 // NW waves of 32 query rows.  With four, every thread unpacks keys and values; with eight, half of the waves do each.
-// HALVES: waves w and w + NW / 2 have the same rows, and each one half of every 64 tokens; joined at the end.
+// HALVES: waves w and w + NW / 2 have the same rows, and each one half of every 64 tokens; joined at the end (where the
+// longest tiles' own time is what counts: in_halves).
 template <int DT, int D, int NW, bool HALVES> __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnArgs a, Geo geo)
 {
     using R = RowType<DT>;
@@ -442,7 +443,33 @@ template <int DT, int D, int NW, bool HALVES> __global__ __launch_bounds__(64 * 
     }
 }
 
-constexpr unsigned PROMPT_HALVES = 512;
+// Whether tiles of 128 rows take eight waves in halves (one workgroup a CU) or four (two a CU, each nearly as fast as
+// one alone).  Per 64 tokens, head size 128: a workgroup of four waves 2.3 us, alone or beside another; one of eight
+// 1.76.  So halves pay where one round of 256 workgroups has nearly all of the work, and cost up to half where there are
+// two rounds of equal tiles.  Measured, four waves against halves, us at head size 128 (64 behaves alike, a little in
+// favour of halves), 32 heads over 8 where nothing else is said:
+//   one round, not split:  one prompt of 1024 after 0 / 700 / 3000 others 50 / 72 / 145 against 44 / 59 / 113; 8 requests
+//       of 128 after 470 34 against 30; two windows of 300 over 1024 32 against 31.  Of 100 tokens in all 22 against 24;
+//       16 of 64 (512 slots of which 256 have rows, in 384 places) 62 against 85: hence the bounds on both.
+//   two, uneven requests:  4 of 777 to 2600, 20 / 5 heads 104 against 86; 6 of 330 to 4000 150 against 129; 12 of 160 to
+//       6000 (400 slots) 220 against 192; 5 of 380 to 800 47 against 56; 10 of 190 to 1500 (376 slots) 70 against 77
+//   two, one prompt:  from its start, 1100 / 1400 / 1700 / 1800 tokens (432 and 456 slots the last) 55 / 64 / 74 / 77
+//       against 47 / 60 / 74 / 79; after half and as many others again 81 / 100 against 82 / 110
+//   two, equal requests:  4 prompts of 300 33 against 48; 4 of 777 (20 / 5) 53 against 70; a window of 300 38 against 58
+//   parts of split tiles:  47 to 90 against 65 to 126; fewer than 256 workgroups (short requests) 19 to 27 against 21 to 29
+static bool in_halves(const AttnArgs &a, const Geo &g)
+{
+    const int64_t tiles = g.slots * a.kv_heads, rows = a.T < a.B * a.max_q ? a.T : a.B * a.max_q;
+    const int64_t filled = g.by_request ? tiles : (rows * g.G + g.tile - 1) / g.tile * a.kv_heads;
+    const int64_t span = a.window > 0 ? a.window : a.max_kv;
+    if (g.nsplit > 1 || span < 256)
+        return false;
+    if (filled <= 256)
+        return tiles <= 320;
+    if (4 * rows <= 3 * a.B * a.max_q)
+        return filled <= 320 && (span >= 2048 ? tiles <= 400 : span >= 1024 && tiles <= 336);
+    return a.B == 1 && a.window == 0 && tiles <= 432 && 5 * a.max_kv <= 6 * a.max_q;
+}
 
 template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
 {
@@ -453,7 +480,7 @@ template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, 
             return hipGetLastError();
         }
     if constexpr (D <= 128)
-        if (grid.x < PROMPT_HALVES) {
+        if (in_halves(a, g)) {
             hipLaunchKernelGGL((attn_prompt_kernel<DT, D, 8, true>), grid, dim3(512), 0, s, a, g);
             return hipGetLastError();
         }
