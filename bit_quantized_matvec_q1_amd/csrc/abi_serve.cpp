@@ -13,6 +13,7 @@ bool is_page(int64_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 bool is_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int64_t kMax = INT32_MAX;
+constexpr const char *kTiles = "the step has 2^23 tiles, or parts of tiles, or more";
 
 // The cache's shape; LB_OK or the failure.
 lb_status check_cache(const char *fn, int64_t pages, int64_t heads, int64_t P, int64_t D)
@@ -172,18 +173,20 @@ static lb_status attn_sizes(const char *fn, lb::AttnArgs &a, int64_t T, int64_t 
     a.T = T, a.B = B, a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
     // a request has no more new tokens than the step, and a window longer than the cache is none
     a.max_q = max_q < T ? max_q : T, a.max_kv = max_kv, a.window = window >= max_kv ? 0 : window;
-    if (T && B && lb::kv_attention_workgroups(a) >= (1 << 23)) // up to 512 threads each, numbered in 32 bits
-        return lb::abi_fail(LB_ESHAPE, fn, "the step has 2^23 tiles or more");
     return LB_OK;
 }
 
 int64_t lowbit_kv_attention_workspace(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
                                       int64_t max_kv, int64_t window)
 {
+    const char *fn = "lowbit_kv_attention_workspace";
     lb::AttnArgs a = {};
-    if (attn_sizes("lowbit_kv_attention_workspace", a, T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window) != LB_OK)
+    if (attn_sizes(fn, a, T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window) != LB_OK)
         return -1;
-    return T && B ? lb::kv_attention_workspace(a) : 0;
+    const int64_t need = T && B ? lb::kv_attention_workspace(a) : 0;
+    if (need < 0)
+        (void)lb::abi_fail(LB_ESHAPE, fn, kTiles);
+    return need;
 }
 
 lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
@@ -201,6 +204,8 @@ lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_
         st = attn_sizes(fn, a, T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window);
     if (st != LB_OK)
         return st;
+    if (T && B && !lb::kv_attention_fits(dtype, a))
+        return lb::abi_fail(LB_ESHAPE, fn, kTiles);
     if (table_stride < 0 || table_stride > kMax)
         return lb::abi_fail(LB_ESHAPE, fn, "negative table stride, or over 2^31-1");
     if (max_kv > 0 && pages == 0)

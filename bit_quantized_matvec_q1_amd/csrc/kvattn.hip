@@ -505,13 +505,28 @@ static int64_t part_bytes(const Geo &g, const AttnArgs &a)
     return g.nsplit == 1 ? 0 : g.slots * a.kv_heads * g.nsplit * part * 4;
 }
 
-// enough for any row type
-int64_t kv_attention_workspace(const AttnArgs &a) { return larger(part_bytes(geometry(LB_F32, a), a), part_bytes(geometry(LB_F16, a), a)); }
-
-int64_t kv_attention_workgroups(const AttnArgs &a)
+// Workgroups of the join: a row each, or as many rows as a workgroup has shares.
+static int64_t join_workgroups(const Geo &g, const AttnArgs &a)
 {
-    const Geo f = geometry(LB_F32, a), h = geometry(LB_F16, a);
-    return larger(f.slots * larger(f.nsplit, f.rows), h.slots * larger(h.nsplit, h.rows)) * a.kv_heads;
+    const int64_t shares = 1024 / a.head_dim;
+    return g.nsplit == 1 ? 0 : g.slots * a.kv_heads * (g.nsplit > shares ? g.rows : (g.rows + shares - 1) / shares);
+}
+
+// Up to 512 threads a workgroup, numbered in 32 bits.
+bool kv_attention_fits(int dtype, const AttnArgs &a)
+{
+    const Geo g = geometry(dtype, a);
+    return larger(g.slots * a.kv_heads * g.nsplit, join_workgroups(g, a)) < (1 << 23);
+}
+
+// Enough for any row type whose launch fits; -1 where none does.
+int64_t kv_attention_workspace(const AttnArgs &a)
+{
+    int64_t need = -1;
+    for (int dtype : {LB_F32, LB_F16})
+        if (kv_attention_fits(dtype, a))
+            need = larger(need, part_bytes(geometry(dtype, a), a));
+    return need;
 }
 
 template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, hipStream_t s)
@@ -520,7 +535,7 @@ template <int DT, int D> static hipError_t run(const AttnArgs &a, const Geo &g, 
                       sizeof(PartialOf<D, PROMPT_ROWS, PROMPT_ROWS>) == (PROMPT_ROWS * D + 2 * PROMPT_ROWS) * 4,
                   "the workspace's size");
     const int64_t tiles = g.slots * a.kv_heads;
-    const dim3 grid((unsigned)(tiles * g.nsplit)), join((unsigned)(tiles * (g.nsplit > 1024 / D ? g.rows : (g.rows + 1024 / D - 1) / (1024 / D))));
+    const dim3 grid((unsigned)(tiles * g.nsplit)), join((unsigned)join_workgroups(g, a));
     hipError_t e = hipSuccess;
     if (g.kind == Geo::PROMPT) {
         e = launch_attn_prompt(DT, a, g, s);

@@ -93,7 +93,7 @@ struct AttnArgs {
     void *workspace;
 };
 int64_t kv_attention_workspace(const AttnArgs &a);
-int64_t kv_attention_workgroups(const AttnArgs &a);
+bool kv_attention_fits(int dtype, const AttnArgs &a);
 hipError_t launch_kv_attention(int dtype, const AttnArgs &a, hipStream_t s);
 
 struct LogitsArgs {

@@ -335,6 +335,10 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  * kv_heads), the keys and values (code times scale) are too, 2^-11 relative at most each.
  * workspace: lowbit_kv_attention_workspace(...) bytes, 16-byte aligned, for the joining of long requests' parts
  * (0 bytes, NULL, where none are split); calls that may run at the same time need one each.
+ * Limits (LB_ESHAPE beyond them; the workspace call answers -1 where no row type is left): B and T * q_heads at most
+ * 2^31 - 1, and fewer than 2^23 tiles, or parts of split ones.  A kv head has a tile for every 16 rows (query token
+ * and head of its group), and one more a request; for 16-bit rows, where requests may have over 64, every 128 or 256:
+ * T * q_heads below about 2^27 for fp32 rows, and all of 2^31 for the others where B is small.
  */
 int64_t lowbit_kv_attention_workspace(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_q,
                                       int64_t max_kv, int64_t window);
