@@ -385,17 +385,23 @@ def lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_
     return lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
 
 
-def _workspace(need, out, stream):
-    """`need` bytes of torch's allocator, of the stream the call runs on: so that nothing else gets them while that
-    stream still works on them."""
-    dev = out.device if isinstance(out, _Tensor) and out.is_cuda else None
-    if stream is None or dev is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev if dev is not None else "cuda")
-    raw = stream if isinstance(stream, int) else stream.cuda_stream
-    if raw == _raw_stream(dev.index):
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev)):
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+def _workspace(need, tensors, stream):
+    """`need` bytes of torch's allocator on the device of `tensors` (the current one, where all are addresses), of the
+    stream the call runs on: so that nothing else gets them while that stream still works on them."""
+    for t in tensors:
+        if isinstance(t, _Tensor) and t.is_cuda:
+            i = t.get_device()
+            break
+    else:
+        i = torch.cuda.current_device()
+    dev = torch.device("cuda", i)
+    if stream is not None:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+        if raw != _raw_stream(i):
+            # the default stream's handle is 0, which ExternalStream takes for "any"
+            with torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)):
+                return torch.empty(need, dtype=torch.uint8, device=dev)
+    return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 def lowbit_kv_attention(dtype, q, T, B, q_heads, kv_heads, head_dim, cu_q, kv_lens, block_table, table_stride, cache, pages,
@@ -412,7 +418,10 @@ def lowbit_kv_attention(dtype, q, T, B, q_heads, kv_heads, head_dim, cu_q, kv_le
     pt, pc = _flat(block_table, "block_table", b * table_stride, _I32), _flat(cache, "cache", nb, None)
     need = lib.lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window)
     if workspace is None and need > 0:
-        workspace = _workspace(need, out, stream)
+        tensors = (out, q, cu_q, kv_lens, block_table, cache)
+        if stream is None and not any(isinstance(t, _Tensor) for t in tensors):
+            stream = 0  # addresses alone run on the default stream, as in every other call
+        workspace = _workspace(need, tensors, stream)
     pw = _flat(workspace, "workspace", need, None)
     args = (dtype, pq, sq, T, B, q_heads, kv_heads, head_dim, pcu, pl, pt, table_stride, pc, pages, page_tokens, max_q, max_kv,
             float(scale), window, po, so, pw, need if need > 0 else 0)
