@@ -60,9 +60,10 @@ lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens
                          int32_t *positions, int64_t max_tokens, int32_t *status, hipStream_t s)
 {
     const char *fn = "lowbit_kv_plan";
-    if (B < 0 || B > kMax || table_stride < 0 || table_stride > kMax || free_capacity < 0 || free_capacity > kMax || max_tokens < 0 ||
+    // the kernels bisect over the requests with 32-bit sums of two numbers of them
+    if (B < 0 || B > (1 << 30) || table_stride < 0 || table_stride > kMax || free_capacity < 0 || free_capacity > kMax || max_tokens < 0 ||
         max_tokens > kMax)
-        return lb::abi_fail(LB_ESHAPE, fn, "negative size, or over 2^31-1");
+        return lb::abi_fail(LB_ESHAPE, fn, "negative size, over 2^30 requests, or another size over 2^31-1");
     if (!is_page(page_tokens))
         return lb::abi_fail(LB_ESHAPE, fn, "page_tokens must be a power of two from 16 to 1024");
     if (B == 0)

@@ -17,7 +17,8 @@ constexpr int PLAN_SMALL_B = 2048; // requests whose sums are held in LDS (16 KB
 
 __device__ __forceinline__ int64_t ceil_div_pos(int64_t a, int shift) { return (a + ((int64_t)1 << shift) - 1) >> shift; }
 
-// Last b in [0, n) with cu[b] <= t (cu[0] = 0 <= t < cu[n]): requests without tokens are passed over.
+// Last b in [0, n) with cu[b] <= t (cu[0] = 0 <= t < cu[n]): requests without tokens are passed over.  n is at most
+// 2^30, so that lo + hi stays below 2^31.
 template <class P> __device__ __forceinline__ int find_request(P cu, int n, int t)
 {
     int lo = 0, hi = n; // cu[lo] <= t < cu[hi]

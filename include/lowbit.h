@@ -292,8 +292,8 @@ int64_t lowbit_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_toke
  *                      one beyond its table or 2^31 - 1, 8: a free count below 0 or above free_capacity;
  *                      then the pages and the tokens that the step asked for.
  * All or nothing: where status[0] is not 0, no table entry, length or count changes, the sums are 0 and all slots
- * -1, so that the step's other calls do nothing.  B = 0: nothing is read or written, slots included.  One launch up
- * to 2048 requests and max_tokens 8192, else two.
+ * -1, so that the step's other calls do nothing.  B = 0: nothing is read or written, slots included.  At most 2^30
+ * requests.  One launch up to 2048 requests and max_tokens 8192, else two.
  */
 lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens, const int32_t *kv_lens, int32_t *kv_lens_out,
                          int32_t *block_table, int64_t table_stride, const int32_t *free_pages, int64_t free_capacity,
@@ -303,7 +303,8 @@ lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens
 /*
  * The pages of the requests with done[b] != 0 go back on top of the free list (in order of requests and blocks),
  * and their lengths become 0.  status [2]: 0, or a sum of 4: a length beyond its table, 8: the list would pass
- * free_capacity, or its count is below 0 (then no length and no count changes); and the pages given back.
+ * free_capacity, or its count is below 0 (then no length and no count changes); and the pages given back.  Fewer than
+ * 2^24 requests.
  */
 lb_status lowbit_kv_release(const int32_t *done, int64_t B, int64_t page_tokens, int32_t *kv_lens, const int32_t *block_table,
                             int64_t table_stride, int32_t *free_pages, int64_t free_capacity, int32_t *free_count, int32_t *status,
@@ -311,7 +312,8 @@ lb_status lowbit_kv_release(const int32_t *done, int64_t B, int64_t page_tokens,
 
 /*
  * Quantises T rows of keys and values into the slots of a layer's cache.  A row whose slot is negative or past
- * the cache is left out.  Two rows with the same slot leave a mixture of both there.
+ * the cache is left out.  Two rows with the same slot leave a mixture of both there.  T * kv_heads * head_dim below
+ * about 2^35 (here and in lowbit_kv_read).
  */
 lb_status lowbit_kv_append(int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t T, int64_t kv_heads,
                            int64_t head_dim, const int64_t *slots, void *cache, int64_t pages, int64_t page_tokens, hipStream_t s);
@@ -359,7 +361,7 @@ lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_
  *   mask       l = -inf where bit t % 32 of mask[b][t / 32] is 0
  * tokens, repetition, presence, frequency, bias_tokens and mask may be NULL (left out), prompt_lens too (all of the
  * history is output).  Lengths are cut to the strides; token numbers outside 0 .. V-1 are passed over.  At most
- * 16384 biases a row.  Results do not depend on the order in which anything runs.
+ * 16384 biases a row, and B * ceil(V / 1024) below 2^22.  Results do not depend on the order in which anything runs.
  */
 lb_status lowbit_logits_process(int dtype, const void *logits, int64_t in_stride, int64_t B, int64_t V, const int32_t *tokens,
                                 int64_t tok_stride, const int32_t *prompt_lens, const int32_t *total_lens, const float *repetition,

@@ -2,7 +2,7 @@
 import pytest
 
 import bit_quantized_matvec_q1_amd.lowbit as L
-from test_serve_abi import attn
+from test_serve_abi import attn, plan
 
 WS = L.lowbit_kv_attention_workspace
 
@@ -39,3 +39,9 @@ def test_what_a_type_cannot_take_does_not_refuse_the_others():
     size = dict(T=520, B=8, hq=8, hk=8, max_q=65, max_kv=1 << 27, qs=1024, os=1024, q=None)
     assert WS(520, 8, 8, 8, 128, 65, 1 << 27) == 64 * 12 * (128 * 128 + 256) * 4
     assert attn(dtype=L.F32, **size) == L.LB_ESHAPE and attn(dtype=L.BF16, **size) == L.LB_EINVAL
+
+
+def test_the_most_requests_of_a_plan():
+    # beyond 2^30 the sum of two request numbers passes 31 bits in the kernels' bisection
+    assert plan(B=(1 << 30) + 1, new=None) == plan(B=(1 << 31) - 1, new=None) == L.LB_ESHAPE
+    assert plan(B=1 << 30, new=None) == L.LB_EINVAL
