@@ -167,13 +167,17 @@ __device__ __forceinline__ float groups_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// The exponent e that takes a row whose largest magnitude is am below 2^e.
+// Queries are held as binary16 numbers times 2^e, the row's largest from 2^14 up to 2^15: what is far below it keeps
+// its bits down to 2^-29 of it, and is off by half the least step, 2^-39 of it, from there on.  (A small element can
+// meet a block of keys as much larger.)
+constexpr int QUERY_TOP = 15;
+// The exponent e for a row whose largest magnitude is am.
 __device__ __forceinline__ int row_exponent(float am)
 {
     int e = 0;
     if (am > 0.0f && am < INFINITY) { // not finite: the row stays as it is, and its result is not finite either
         (void)frexpf(am, &e);
-        e = min(e, 127);
+        e -= QUERY_TOP;
     }
     return e;
 }
@@ -181,7 +185,7 @@ __device__ __forceinline__ int row_exponent(float am)
 // 2^-100, which a scale of 0 and the smallest queries get, every score that is not is 0 for the exponential).
 __device__ __forceinline__ float score_scale(float scale, int e)
 {
-    const float s = ldexpf(1.0f, e) * (fabsf(scale) * 1.44269504088896341f);
+    const float s = ldexpf(fabsf(scale) * 1.44269504088896341f, e);
     return s < 0x1p-100f ? 0x1p-100f : s;
 }
 template <bool SPLIT> __device__ __forceinline__ void query_halves(const float (&x)[8], int e, bool negate, f16x8 &hi, f16x8 &lo)

@@ -1,0 +1,67 @@
+"""Attention over blocks of very different sizes: keys, queries and values whose 32-element blocks lie far apart, against
+64 bits, with bounds derived for each kernel."""
+import numpy as np
+import pytest
+
+import serve_ref as R
+from gpu_util import say
+from test_serve_attention import Case
+
+pytestmark = pytest.mark.gpu
+
+# heads (over one kv head) and new tokens that take the kernel for few rows, the one for up to 64, and a prompt's
+FORMS = {"few": (4, 1), "some": (8, 2), "many": (4, 40)}
+
+
+def scales_of(c, which):
+    """The keys' (0) or values' (1) scales as an array [pages, hk, P / 4, blocks, 4] that writes through."""
+    n = c.P * c.D // 32 * 2
+    steps = (c.cache.strides[0], c.cache.strides[1], c.D // 32 * 8, 8, 2)
+    return np.ndarray((c.pages, c.hk, c.P // 4, c.D // 32, 4), np.float16, c.cache, c.P * c.D + which * n, steps)
+
+
+def rows(c, t):
+    """Keys, values and value scales that query token t of the (single) request sees."""
+    z = c.lens[0] - c.news[0] + t + 1
+    got = [R.load(c.cache, c.P, c.D, int(c.table[0, j // c.P]) * c.P + j % c.P, 0) for j in range(z)]
+    return [np.array([g[i] for g in got]) for i in range(3)]
+
+
+@pytest.mark.parametrize("kind,form", [("f32", "few"), ("f32", "some"), ("f32", "many"), ("bf16", "few"), ("bf16", "some"), ("f16", "few"),
+                                       ("f16", "some")])
+def test_small_query_elements_against_large_keys(kind, form):
+    """Queries whose second block is 2^-20 of the first, keys where it is 2^20 times the first: both count alike.
+
+    The score's error, beside what serve_ref counts (a chain of 32 products, the block sums and scalings, fp32 queries
+    in 22 bits): queries are held as binary16 numbers up to 2^15, so what is small there is off by half its least step,
+    2^-25, that is 2^-39 of the row's largest (fp32 rows' second number ends at the same step)."""
+    hq, new = FORMS[form]
+    say(f"case small queries {kind} {form}")
+    c = Case(71, kind, 128, 16, hq, 1, [57], [new], extra=0)
+    f = 2.0**-10
+    d = scales_of(c, 0)
+    d[:, :, :, 0] *= np.float16(f)
+    d[:, :, :, 1] /= np.float16(f)
+    d[:, :, :, 2:] *= np.float16(f)
+    c.q[:, :, 32:64] *= f * f
+    c.q *= 2.0**7  # scores of about one
+    got = c.gpu()
+    worst = 0.0
+    for t in range(new):
+        k, v, dv = rows(c, t)
+        for h in range(hq):
+            x = c.q[t, h].double().numpy()
+            s = k @ x * c.scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            want, A, m = w @ v, w @ np.abs(v), len(w)
+            size = c.scale * (np.abs(k) @ np.abs(x)).max()
+            few = c.scale * np.abs(k).sum(-1).max() * np.abs(x).max() * 2.0**-39
+            ds = size * (52 * 2.0**-24 + (2.0**-22 if kind == "f32" else 0.0)) + few + 2.0**-22 + np.abs(s).max() * 2.0**-23
+            dp = 2.0**-21 if kind == "f32" else R.EPS["f16"] / 2
+            tol = np.abs(want) * R.EPS[kind] / 2 + A * (2 * ds + dp + (m + 64) * 2.0**-24) + m * 6 * 2.0**-31 * (w * dv.max(-1)).max() + 1e-37
+            if kind == "f16":
+                tol += 2.0**-25
+            worst = max(worst, float((np.abs(got[t, h] - want) / tol).max()))
+    say(f"  worst {worst:.3g} of the bound")
+    assert worst <= 1.0
