@@ -16,7 +16,9 @@
 // some score passes it by 15 (in powers of two), so the usual step has no reduction across lanes and no
 // rescaling.  A score counts with its value's scale (s + log2 max_b dv_b): p times the scale then stays below
 // binary16's 2^16 whatever the values' range, and the largest are far above its lower end (2^-24), so that what
-// is rounded away there is 2^-31 of them.
+// is rounded away there is 2^-31 of them: of the block's largest where a block has columns, and with them a reference,
+// of its own (packed), of the row's where one reference serves all blocks (wide; there a block of values 2^-12 of
+// another's keeps 2^-19 of itself in fp32 rows.  A reference a block would take a product more for every weight).
 // fp32 queries and outputs: the queries and p times the scale are split into two binary16 numbers each (22
 // bits), and every product is done twice.
 //

@@ -23,9 +23,10 @@
 // output, and of the order of a binary16 output's own rounding (on prompts of normal values the keys' rounding gives
 // 3.4e-4 of the result's size, the values' and the weights' 1.9e-4 each, the output's 2.0e-4; all of them 4.4e-4).
 // Keeping the keys' rest in a second number would take half as many matrix instructions again and half as much LDS.
-// The scales are taken times a power of two that brings the largest seen so far to 2^9, for keys and for values, so
-// that no range is lost; it changes, with the tile unpacked again, if a later tile passes it by 2^5.  Scores are kept
-// against a reference a row as in kvattn.hip.
+// The scales are taken times a power of two that brings the largest seen so far to 2^9, for keys and for values; it
+// changes, with the tile unpacked again, if a later tile passes it by 2^5.  So only what is below 2^-22 of the largest
+// loses more than that (7 * 2^-33 of the largest at most).  Scores are kept against a reference a row as in kvattn.hip,
+// without the values' scales: weights end at 2^-31 of the row's largest.
 #include "kvattn_internal.h"
 
 namespace lb {

@@ -65,3 +65,51 @@ def test_small_query_elements_against_large_keys(kind, form):
             worst = max(worst, float((np.abs(got[t, h] - want) / tol).max()))
     say(f"  worst {worst:.3g} of the bound")
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("kind,form", [("f32", "few"), ("f32", "some"), ("f32", "many"), ("bf16", "few"), ("bf16", "some"), ("bf16", "many"),
+                                       ("f16", "few"), ("f16", "some"), ("f16", "many")])
+@pytest.mark.parametrize("ratio", [2.0**-10, 2.0**-17])
+def test_blocks_of_small_values(kind, form, ratio):
+    """One block's values a small fraction of the others', and one block's keys.
+
+    Weights times value scales end at binary16's least step: half of it, 2^-25, a key, times a code of at most 6, where
+    the largest such product is at least 2^6: of the block's own products in the kernel for few rows, of all blocks'
+    in the one for some (and fp32's many).  The kernel for many rows rounds the weights alone (2^-25 where the largest
+    is 2^7, taken as 2^6), and keys and values, code times scale, to 2^-11, and where the largest scale is 2^8 or more
+    to half the least step, 2^-25, for the scale (times 6) and once more for the product: 7 * 2^-33 of it."""
+    hq, new = FORMS[form]
+    say(f"case small values {kind} {form} {ratio}")
+    c = Case(72, kind, 128, 16, hq, 1, [90], [new], extra=0)
+    scales_of(c, 1)[:, :, :, 2] *= np.float16(ratio)
+    scales_of(c, 0)[:, :, :, 1] *= np.float16(ratio)
+    got = c.gpu()
+    many = form == "many" and kind != "f32"
+    worst = 0.0
+    kd, vd = (float(scales_of(c, i).max()) for i in (0, 1))
+    for t in range(new):
+        k, v, dv = rows(c, t)
+        for h in range(hq):
+            x = c.q[t, h].double().numpy()
+            s = k @ x * c.scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            want, A, m = w @ v, w @ np.abs(v), len(w)
+            size = c.scale * (np.abs(k) @ np.abs(x)).max()
+            few = c.scale * np.abs(k).sum(-1).max() * np.abs(x).max() * 2.0**-39
+            ds = size * (52 * 2.0**-24 + (2.0**-22 if kind == "f32" else 0.0)) + few + 2.0**-22 + np.abs(s).max() * 2.0**-23
+            dp = 2.0**-21 if kind == "f32" else R.EPS["f16"] / 2
+            if many:
+                ds += size * R.EPS["f16"] / 2 + c.scale * np.abs(x).sum() * 7 * 2.0**-33 * kd
+                dp += R.EPS["f16"] / 2
+                floor = 2.0**-31 * w.max() * np.abs(v).sum(0) + 7 * 2.0**-33 * vd
+            elif form == "few":
+                floor = m * 6 * 2.0**-31 * np.repeat((w[:, None] * dv).max(0), 32)
+            else:
+                floor = m * 6 * 2.0**-31 * (w[:, None] * dv).max()
+            tol = np.abs(want) * R.EPS[kind] / 2 + A * (2 * ds + dp + (m + 64) * 2.0**-24) + floor + 1e-37
+            if kind == "f16":
+                tol += 2.0**-25
+            worst = max(worst, float((np.abs(got[t, h] - want) / tol).max()))
+    say(f"  worst {worst:.3g} of the bound")
+    assert worst <= 1.0
