@@ -49,9 +49,9 @@ extern "C" {
 
 int64_t lowbit_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_tokens, int64_t head_dim)
 {
-    if (pages < 0 || pages > kMax || kv_heads < 1 || kv_heads > 65536 || !is_page(page_tokens) || !is_head_dim(head_dim))
+    if (check_cache("lowbit_kv_cache_bytes", pages, kv_heads, page_tokens, head_dim) != LB_OK)
         return -1;
-    return pages * kv_heads * lb::kv_record_bytes(page_tokens, head_dim);
+    return pages * kv_heads * lb::kv_record_bytes(page_tokens, head_dim); // below 2^63, a page being below 2^32
 }
 
 lb_status lowbit_kv_plan(const int32_t *new_lens, int64_t B, int64_t page_tokens, const int32_t *kv_lens, int32_t *kv_lens_out,

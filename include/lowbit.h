@@ -275,7 +275,7 @@ lb_status lowbit_matvec_batched_static(const lb_matvec_desc *list, int32_t n, hi
  */
 typedef enum { LB_F32 = 0, LB_BF16 = 1, LB_F16 = 2 } lb_dtype;
 
-/* Bytes of one layer's cache; -1 for a bad shape. */
+/* Bytes of one layer's cache; -1 for a bad shape (also one of pages of 4 GiB or more, which nothing here takes). */
 int64_t lowbit_kv_cache_bytes(int64_t pages, int64_t kv_heads, int64_t page_tokens, int64_t head_dim);
 
 /*

@@ -45,3 +45,11 @@ def test_the_most_requests_of_a_plan():
     # beyond 2^30 the sum of two request numbers passes 31 bits in the kernels' bisection
     assert plan(B=(1 << 30) + 1, new=None) == plan(B=(1 << 31) - 1, new=None) == L.LB_ESHAPE
     assert plan(B=1 << 30, new=None) == L.LB_EINVAL
+
+
+def test_cache_bytes_of_pages_that_nothing_takes():
+    # 2^31 pages of 65536 heads' records would pass 2^63; a page of 2^32 bytes is refused by every entry point
+    assert L.lowbit_kv_cache_bytes((1 << 31) - 1, 65536, 1024, 256) == -1
+    assert L.lowbit_kv_cache_bytes(1, 65536, 1024, 256) == -1
+    assert L.lowbit_kv_cache_bytes((1 << 31) - 1, 65536, 16, 256) == ((1 << 31) - 1) * 65536 * 16 * 288
+    assert L.lowbit_kv_cache_bytes(1, 65536, 512, 64) == 65536 * 512 * 72
