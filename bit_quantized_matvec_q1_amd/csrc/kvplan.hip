@@ -175,7 +175,8 @@ hipError_t launch_kv_plan(const PlanArgs &a, hipStream_t s)
 }
 
 // --- release: the pages of finished requests go back on top of the free list, in request and block order.
-// The first launch (a workgroup per request) only reads lengths and count, the second changes them.
+// The first launch only reads lengths and count, the second changes them.  64 requests of up to 4000 tokens in pages of
+// 16: 4.7 us for both (two launches: 3.7 is one alone); 4096 of up to 500: 18.5 us (24.5 with a workgroup each).
 
 __device__ __forceinline__ int64_t held_pages(const ReleaseArgs &a, int shift, int64_t b)
 {
@@ -207,15 +208,30 @@ __device__ __forceinline__ Released released_before(const ReleaseArgs &a, int sh
     return {ws[0] + ws[1] + ws[2] + ws[3], wr[0] | wr[1] | wr[2] | wr[3]};
 }
 
-__global__ __launch_bounds__(256) void release_copy_kernel(ReleaseArgs a, int shift)
+// A workgroup a request; beyond RELEASE_WGS requests, each takes a run of them, so that the sums of the requests
+// before are read that many times and not once a request.
+constexpr int64_t RELEASE_WGS = 1024;
+__global__ __launch_bounds__(256) void release_copy_kernel(ReleaseArgs a, int shift, int per)
 {
-    const int64_t b = blockIdx.x, n = held_pages(a, shift, b), count = *a.free_count;
-    if (n == 0 || n > a.table_stride || count < 0)
+    const int64_t end = (int64_t)(blockIdx.x + 1) * per < a.B ? (int64_t)(blockIdx.x + 1) * per : a.B, count = *a.free_count;
+    int64_t b = (int64_t)blockIdx.x * per, n = 0;
+    for (; b < end && n == 0; b++) // the first one that gives something back
+        n = held_pages(a, shift, b);
+    if (n == 0 || count < 0)
         return;
-    const int64_t at = count + released_before(a, shift, b).before;
-    // what lies above the count is nobody's: a release that is refused in the end has lost nothing by this
-    for (int64_t i = threadIdx.x; i < n && at + i < a.free_capacity; i += 256)
-        a.free_pages[at + i] = a.block_table[b * a.table_stride + i];
+    b--;
+    int64_t at = count + released_before(a, shift, b).before;
+    for (;;) {
+        if (n > a.table_stride) // the release is refused in the end
+            return;
+        // what lies above the count is nobody's: a release that is refused has lost nothing by this
+        for (int64_t i = threadIdx.x; i < n && at + i < a.free_capacity; i += 256)
+            a.free_pages[at + i] = a.block_table[b * a.table_stride + i];
+        if (++b >= end)
+            return;
+        at += n;
+        n = held_pages(a, shift, b);
+    }
 }
 
 __global__ __launch_bounds__(256) void release_end_kernel(ReleaseArgs a, int shift)
@@ -238,7 +254,8 @@ __global__ __launch_bounds__(256) void release_end_kernel(ReleaseArgs a, int shi
 hipError_t launch_kv_release(const ReleaseArgs &a, hipStream_t s)
 {
     const int shift = log2_of(a.page_tokens);
-    hipLaunchKernelGGL(release_copy_kernel, dim3((unsigned)a.B), dim3(256), 0, s, a, shift);
+    const int64_t per = (a.B + RELEASE_WGS - 1) / RELEASE_WGS;
+    hipLaunchKernelGGL(release_copy_kernel, dim3((unsigned)((a.B + per - 1) / per)), dim3(256), 0, s, a, shift, (int)per);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
