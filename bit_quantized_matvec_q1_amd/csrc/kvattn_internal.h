@@ -139,8 +139,8 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs &a, const Geo &g, int64_t
     }
     const int q0 = a.cu_q[t.b], q1 = a.cu_q[t.b + 1];
     t.n = max(0, min(q1, (int)a.T) - q0);
-    if (q0 < 0 || tile < 0) // no offsets of a step
-        t.n = 0;
+    if (q0 < 0 || tile < 0) // no offsets of a step, or a slot of the rows before the first request's
+        t.n = tile = 0;
     t.rows = (int)min((int64_t)t.n * g.G, (int64_t)INT32_MAX);
     t.row0 = tile * rows_per_tile;
     const int len = max(a.kv_lens[t.b], 0);

@@ -328,9 +328,10 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  * already appended), found through block_table[b].  Query i of n, at position pos = kv_lens[b] - n + i, sees the
  * keys j with j <= pos, and with window > 0 only those with j > pos - window:
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j - max),  head h reading kv head h / (q_heads / kv_heads).
- * A query that sees no key (kv_lens[b] < n) gives zeros; rows behind the last request are left as they were.  A
- * page number outside the cache, among those that a query sees, makes the query's result NaN, as does a request
- * longer than max_kv or than its table.  A request of more than max_q tokens may leave rows unwritten.
+ * A query that sees no key (kv_lens[b] < n) gives zeros; rows before the first request's (cu_q[0] of them) and behind
+ * the last's are left as they were.  A page number outside the cache, among those that a query sees, makes the
+ * query's result NaN, as does a request longer than max_kv or than its table.  A request of more than max_q tokens may
+ * leave rows unwritten.
  * out may be q, with the same stride, but not overlap it otherwise.
  * Precision: sums, maxima and exponents are 32-bit, the result is rounded to dtype once.  On the way, in relative terms
  * and for what is far below its row's largest in terms of that:

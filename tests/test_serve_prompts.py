@@ -20,7 +20,7 @@ def check_rows(c, got, tokens, heads, rounded=True):
     G, worst = c.hq // c.hk, 0.0
     for t in tokens:
         b = int(np.searchsorted(c.cu, t, side="right")) - 1
-        length = c.lens[b] - int(c.cu[b + 1] - t) + 1
+        length = c.lens[b] - int(c.cu[b + 1] - t) + 1  # up to its own token
         for h in heads:
             q = c.q[t, h * G:(h + 1) * G].double().cpu().numpy()[None]
             ref, tol = R.attention(c.cache[:, h:h + 1], c.P, c.D, q, [0, 1], [length], c.table[b:b + 1], 1, c.scale, c.window, c.kind, rounded=rounded)
@@ -158,3 +158,19 @@ def test_forms_see_what_is_not_finite_and_no_more(D, form):
     got, sees = c.gpu(), np.zeros(c.T, bool)
     sees[:n] = at >= 16
     assert np.isnan(got[sees]).all() and np.array_equal(got[~sees], clean[~sees])
+
+
+@pytest.mark.parametrize("kind,D,hq,hk,lens,news", [
+    ("f32", 128, 40, 2, [30, 50], [1, 3]), ("bf16", 128, 10, 2, [70, 20, 5], [2, 3, 5]), ("f16", 256, 12, 3, [40], [1]),  # 16-row tiles
+    ("f32", 64, 4, 4, [100, 30], [40, 30]), ("bf16", 128, 16, 4, [200, 90], [130, 40]), ("f16", 64, 14, 2, [600], [70]),  # and a prompt's
+    ("bf16", 64, 16, 4, [40, 300], [1, 1]), ("f16", 128, 128, 32, [300, 260], [130, 70])])
+@pytest.mark.parametrize("first", [1, 5, 100])
+def test_a_step_behind_other_rows(first, kind, D, hq, hk, lens, news):
+    """A step's rows from `first` on: what lies before them is not its own."""
+    say(f"case rows from {first} on {kind} D={D} {hq}/{hk} {news}")
+    c = Case(90, kind, D, 16, hq, hk, lens, news, extra=first + 3, pad=8)
+    c.q = torch.cat([c.q[-first - 3:-3], c.q[:-first - 3], c.q[-3:]])
+    c.cu = c.cu + np.int32(first)
+    got = c.gpu()
+    assert (got[:first] == 7).all() and (got[c.cu[-1]:] == 7).all()
+    check_rows(c, got, sample(c), sorted({0, 1 % hk, hk - 1}), rounded=kind != "f32" and c.max_q * hq // hk > 64)
