@@ -276,8 +276,10 @@ __global__ __launch_bounds__(64 * ATT_WAVES, attn_waves(DT == LB_F32, D, PACK)) 
                 for (int i = 0; i < 4; i++) {
                     uint32_t w = 0;
 #pragma unroll
-                    for (int k = i / 2; k < S::SW; k += 2)
-                        w = max(w, (i & 1 ? vs[u].w[k] >> 16 : vs[u].w[k]) & 0x7fffu);
+                    for (int k = i / 2; k < S::SW; k += 2) {
+                        const uint32_t d = (i & 1 ? vs[u].w[k] >> 16 : vs[u].w[k]) & 0x7fffu;
+                        w = max(w, d < 0x7c00u ? d : 0u); // a block that is not finite has no say over the others
+                    }
                     m = fmaxf(m, fmaf(sc[u][i], qscale, log2_above(w)));
                 }
             const bool past = m > ref + REF_MOST;

@@ -74,8 +74,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
-// An upper bound, by less than 2, of the log2 of a binary16 magnitude's bits.
-__device__ __forceinline__ float log2_above(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
+// An upper bound, by at most 1, of the log2 of a binary16 magnitude's bits; above every number's for what is not finite,
+// and -64 for 0: far below the least number's -23, and a weight of 2^64 times as much still is far from fp32's end.
+__device__ __forceinline__ float log2_above(uint32_t bits)
+{
+    return (float)max((int)(__float_as_uint(half_bits_to_float((uint16_t)bits)) >> 23) - 126, -64);
+}
 
 // Column c of four consecutive tokens (nb bytes each, byte b holding elements 32 b + c and 32 b + 16 + c) as
 // pairs of tokens: byte b of word [pair][half][b / 4] has element 32 b + 16 half + c of tokens 2 pair, 2 pair + 1.

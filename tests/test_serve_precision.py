@@ -113,3 +113,74 @@ def test_blocks_of_small_values(kind, form, ratio):
             worst = max(worst, float((np.abs(got[t, h] - want) / tol).max()))
     say(f"  worst {worst:.3g} of the bound")
     assert worst <= 1.0
+
+
+def expect(c, got, t, h, blocks, form):
+    """Query t, head h against 64 bits in the elements of `blocks`: the worst error over its bound.  The bounds are those
+    of test_blocks_of_small_values; largest products over all keys that are finite."""
+    k, v, dv = rows(c, t)
+    dv = np.where(np.isfinite(dv), dv, 0.0)
+    x = c.q[t, h].double().numpy()
+    s = k @ x * c.scale
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    m = len(w)
+    size = c.scale * (np.abs(k) @ np.abs(x)).max()
+    ds = size * (52 * 2.0**-24 + (2.0**-22 if c.kind == "f32" else 0.0)) + c.scale * np.abs(k).sum(-1).max() * np.abs(x).max() * 2.0**-39
+    ds += 2.0**-22 + np.abs(s).max() * 2.0**-23
+    dp = 2.0**-21 if c.kind == "f32" else R.EPS["f16"] / 2
+    largest = (w[:, None] * dv).max(0) if form == "few" else np.full(c.D // 32, (w[:, None] * dv).max())
+    worst = 0.0
+    for b in blocks:
+        e = slice(32 * b, 32 * b + 32)
+        want, A = w @ v[:, e], w @ np.abs(v[:, e])
+        tol = np.abs(want) * R.EPS[c.kind] / 2 + A * (2 * ds + dp + (m + 64) * 2.0**-24) + m * 6 * 2.0**-31 * largest[b] + 1e-37
+        if c.kind == "f16":
+            tol += 2.0**-25
+        err = np.abs(got[t, h, e] - want)
+        assert np.isfinite(err).all()
+        worst = max(worst, float((err / tol).max()))
+    return worst
+
+
+SMALL = [("f32", "few"), ("f32", "some"), ("f32", "many"), ("bf16", "few"), ("bf16", "some")]
+
+
+@pytest.mark.parametrize("kind,form", SMALL)
+@pytest.mark.parametrize("zero", [[37], [5, 37, 60], "tiny"])
+def test_the_heaviest_keys_have_no_values(kind, form, zero):
+    """Keys that take nearly all of the weight, and values that are zero there (or all values below binary16's normal
+    range): what is left has its own size."""
+    hq, new = FORMS[form]
+    say(f"case zero values {kind} {form} {zero}")
+    c = Case(73, kind, 64, 16, hq, 1, [90], [new], extra=0)
+    c.scale = 2.0 if zero != "tiny" else 0.125
+    if zero == "tiny":
+        scales_of(c, 1)[:] *= np.float16(2.0**-20)
+    else:
+        scales_of(c, 0)[:] *= np.float16(0.125)
+        for j in zero:
+            page, o = c.table[0, j // 16], j % 16
+            scales_of(c, 0)[page, 0, o // 4, :, o % 4] *= np.float16(8)
+            scales_of(c, 1)[page, 0, o // 4, :, o % 4] = 0
+            rec = c.cache[page, 0]
+            rec[o * 32:(o + 1) * 32] = 0x22  # all elements 1 times the scale
+        c.q = c.q.abs()  # scores there: about 2 * 64 * 0.8 * 0.4, the others' a few
+    got = c.gpu()
+    worst = max(expect(c, got, t, h, range(2), form) for t in range(max(0, new - 10), new) for h in range(hq))
+    say(f"  worst {worst:.3g} of the bound")
+    assert worst <= 1.0
+
+
+@pytest.mark.parametrize("kind,form", SMALL)
+def test_a_block_that_is_not_finite_leaves_the_others(kind, form):
+    hq, new = FORMS[form]
+    say(f"case NaN block {kind} {form}")
+    c = Case(74, kind, 128, 16, hq, 1, [90], [new], extra=0)
+    for j in (3, 40):
+        scales_of(c, 1)[c.table[0, j // 16], 0, j % 16 // 4, 2, j % 4] = np.nan
+    got = c.gpu()
+    assert np.isnan(got[:, :, 64:96]).all()
+    worst = max(expect(c, got, t, h, (0, 1, 3), form) for t in range(max(0, new - 10), new) for h in range(hq))
+    say(f"  worst {worst:.3g} of the bound")
+    assert worst <= 1.0
