@@ -336,12 +336,12 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  * Precision: sums, maxima and exponents are 32-bit, the result is rounded to dtype once.  On the way, in relative terms
  * and for what is far below its row's largest in terms of that:
  *   queries  fp32 2^-22, the others exact; 2^-39 of the row's largest element
- *   weights  p_j times the value's scale: fp32 2^-21, the others 2^-11; 6 * 2^-31 of the largest such product a key: of
- *            the element's own 32-block where requests have at most 512 / head_dim rows (max_q times q_heads / kv_heads),
- *            else of all blocks.  So fp32 elements are good to 2^-20 of sum_j p_j |v_j| where their block's values are
- *            not below some 2^-10 of the row's largest.
+ *   weights  p_j times the value's scale: fp32 2^-21, the others 2^-11; 6 * 2^-31 a key of the largest such product (a
+ *            scale of 0 counted as 2^-64): of the element's own 32-block where requests have at most 512 / head_dim
+ *            rows (max_q times q_heads / kv_heads), else of all blocks.  So fp32 elements are good to 2^-20 of
+ *            sum_j p_j |v_j| where their block's values are not below some 2^-10 of the row's largest.
  *   and for 16-bit rows where requests may have over 64: p_j alone, 2^-11 and 2^-31 of the largest; and the keys and
- *            values (code times scale), 2^-11 and 2^-30 of the largest scale among the request's keys, or values
+ *            values (code times scale), 2^-11 and 2^-30 of the largest scale among the request's keys, or values.
  * workspace: lowbit_kv_attention_workspace(...) bytes, 16-byte aligned, for the joining of long requests' parts
  * (0 bytes, NULL, where none are split); calls that may run at the same time need one each.
  * Limits (LB_ESHAPE beyond them; the workspace call answers -1 where no row type is left): B and T * q_heads at most
