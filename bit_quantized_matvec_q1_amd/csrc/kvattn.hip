@@ -271,17 +271,22 @@ __global__ __launch_bounds__(64 * ATT_WAVES, attn_waves(DT == LB_F32, D, PACK)) 
         if (__ballot(bound > ref + REF_MOST)) {
             float m = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < 2; u++)
+            for (int u = 0; u < 2; u++) {
+                Words<S::SW> d = vs[u];
+#pragma unroll
+                for (int k = 0; k < S::SW; k++)
+                    asm volatile("" : "+v"(d.w[k])); // nothing made of them here is kept for what follows: registers
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     uint32_t w = 0;
 #pragma unroll
                     for (int k = i / 2; k < S::SW; k += 2) {
-                        const uint32_t d = (i & 1 ? vs[u].w[k] >> 16 : vs[u].w[k]) & 0x7fffu;
-                        w = max(w, d < 0x7c00u ? d : 0u); // a block that is not finite has no say over the others
+                        const uint32_t x = (i & 1 ? d.w[k] >> 16 : d.w[k]) & 0x7fffu;
+                        w = max(w, x < 0x7c00u ? x : 0u); // a block that is not finite has no say over the others
                     }
-                    m = fmaxf(m, fmaf(sc[u][i], qscale, log2_above(w)));
+                    m = fmaxf(m, fmaf(sc[u][i], qscale, log2_above_all(w)));
                 }
+            }
             const bool past = m > ref + REF_MOST;
             if (__ballot(past)) {
                 const float now = fmaxf(ref, groups_max(m) - REF_BELOW);

@@ -74,11 +74,14 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
-// An upper bound, by at most 1, of the log2 of a binary16 magnitude's bits; above every number's for what is not finite,
-// and -64 for 0: far below the least number's -23, and a weight of 2^64 times as much still is far from fp32's end.
-__device__ __forceinline__ float log2_above(uint32_t bits)
+// An upper bound of the log2 of a binary16 magnitude's bits, by less than 1 from its normal range on.
+__device__ __forceinline__ float log2_above(uint32_t bits) { return (float)((int)(bits >> 10) - 14); }
+// The same for every number, down to -64 for 0: far below the least number's -23, and a weight of 2^64 times as much
+// still is far from fp32's end.
+__device__ __forceinline__ float log2_above_all(uint32_t bits)
 {
-    return (float)max((int)(__float_as_uint(half_bits_to_float((uint16_t)bits)) >> 23) - 126, -64);
+    const int e = (int)(bits >> 10);
+    return (float)(e ? e - 14 : bits ? 8 - __clz((int)bits) : -64);
 }
 
 // Column c of four consecutive tokens (nb bytes each, byte b holding elements 32 b + c and 32 b + 16 + c) as
