@@ -333,8 +333,9 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  * query's result NaN, as does a request longer than max_kv or than its table.  A request of more than max_q tokens may
  * leave rows unwritten.
  * out may be q, with the same stride, but not overlap it otherwise.
- * Precision: sums, maxima and exponents are 32-bit, the result is rounded to dtype once.  On the way, in relative terms
- * and for what is far below its row's largest in terms of that:
+ * Precision: sums, maxima and exponents are 32-bit, the result is rounded to dtype once.  Scores (scale * q . k) are
+ * taken up to 2^24 in size; beyond, where fp32 no longer tells neighbours apart, a result may not be finite.  On the
+ * way, in relative terms and for what is far below its row's largest in terms of that:
  *   queries  fp32 2^-22, the others exact; 2^-39 of the row's largest element
  *   weights  p_j times the value's scale: fp32 2^-21, the others 2^-11; 6 * 2^-31 a key of the largest such product (a
  *            scale of 0 counted as 2^-64): of the element's own 32-block where requests have at most 512 / head_dim

@@ -184,3 +184,30 @@ def test_a_block_that_is_not_finite_leaves_the_others(kind, form):
     worst = max(expect(c, got, t, h, (0, 1, 3), form) for t in range(max(0, new - 10), new) for h in range(hq))
     say(f"  worst {worst:.3g} of the bound")
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_the_largest_scores(kind, form):
+    """Scores of 2^24 and less, two keys' equal and far above the others': the mean of their values is the result.
+
+    The other keys' scores are over 2^23 below, so their weights are 0; the values are codes times their scales, for
+    16-bit rows of many tokens rounded to binary16 (2^-11), weighed and divided by the same weight (2^-11 for the
+    weight's rounding against the sum's, 2^-21 in fp32 rows), and rounded."""
+    hq, new = FORMS[form]
+    say(f"case largest scores {kind} {form}")
+    c = Case(75, kind, 64, 16, hq, 1, [90], [new], extra=0)
+    scales_of(c, 0)[:] = np.float16(0.5)
+    for j in range(90):
+        rec = c.cache[c.table[0, j // 16], 0]
+        rec[j % 16 * 32:(j % 16 + 1) * 32] = 0x77 if j in (20, 50) else 0x11  # 6 * 0.5, twice the same, and 0.5 * 0.5
+    c.q = (c.q * 0 + 2.0**10)
+    c.scale = 2.0**24 / (64 * 3 * 2.0**10)
+    j = 90 - new  # the first query's position
+    got = c.gpu()
+    k, v, _ = rows(c, new - 1)
+    assert abs((k @ c.q[0, 0].double().numpy()).max() * c.scale - 2.0**24) < 2.0
+    assert j >= 50
+    want = (v[20] + v[50]) / 2
+    tol = np.abs(want) * R.EPS[kind] / 2 + (np.abs(v[20]) + np.abs(v[50])) / 2 * (2.0**-20 if kind == "f32" else 3 * 2.0**-11) + 1e-6
+    assert (np.abs(got - want) <= tol).all()
