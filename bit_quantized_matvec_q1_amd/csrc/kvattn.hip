@@ -25,10 +25,12 @@
 // Decode is bound by HBM, so the tokens of one (request, kv head) are cut into chunks, one workgroup each, and the
 // chunks' results joined by a second launch.  Measured at head size 128, four heads a kv head, one new token a
 // request (attention + join): 32 requests of up to 4000 tokens over 5 kv heads, 54 MB of cache, 18.2 + 4.0 us; one of
-// 131071 over 8, 151 MB, 29.4 + 6.3 us (5.1 TB/s); 64 of up to 12345 over 8, 537 MB, 101 + 4.9 us (5.3 TB/s, a plain
-// read of as much reaches 6.7).  A copy of the kernel that does nothing but its loads takes 18.0, 27.5 and 95.4 us, so
-// what bounds it is how the pages' records stream in; the vector unit (unpacking, softmax) is at 50 % of its cycles,
-// the matrix cores at 12 %.
+// 131071 over 8, 151 MB, 29.2 + 6.3 us (5.2 TB/s); 64 of up to 12345 over 8, 537 MB, 102 + 5.1 us (5.3 TB/s, a plain
+// read of as much reaches 6.7).  A copy of the kernel that does nothing but its loads, in the same chunks, takes 18.0,
+// 27.5 and 95.4 us: the arithmetic is hidden behind them (the vector unit, unpacking and softmax, is at 51 % of its
+// cycles, the matrix cores at 12 %).  For the one long request that is the rate at which a plain read of as much goes
+// (5.6 TB/s).  For the others the chunks' places count too: of 1120 workgroups launched some 650 have tokens, of 4096
+// some 2500, so that the last round is mostly empty.
 #include <type_traits>
 
 #include "kvattn_internal.h"
@@ -473,9 +475,11 @@ static Geo geometry(int dtype, const AttnArgs &a)
     // fp32 rows need the wide kernel's exact keys and split operands
     g.kind = most <= packed ? Geo::PACKED : most <= PROMPT_FROM || dtype == LB_F32 ? Geo::WIDE : Geo::PROMPT;
     g.tile = g.kind == Geo::PACKED ? packed : g.kind == Geo::WIDE ? ATT_ROWS : PROMPT_ROWS;
-    // Larger tiles where every CU gets two of them.  They are counted from what the requests may bring, not from the
-    // rows of a padded step, so that there really are as many: tiles of 256 rows are never split (below), and the
-    // parts and their join know 128.
+    // Larger tiles where every CU gets two of them: of 32 heads over 8 at head size 128, prompts of 2048 / 4096 / 8192
+    // tokens (256, 512 and 1024 such tiles) 91 / 215 / 719 us with 128 rows, 94 / 188 / 663 us with 256; 64 requests of
+    // 64 after 936 156 and 119; 16 of 256 57 and 58; 8000 with a window of 1000 231 and 233.  They are counted from
+    // what the requests may bring, not from the rows of a padded step, so that there really are as many: tiles of 256
+    // rows are never split (below), and the parts and their join know 128.
     const int64_t real = a.T < a.B * a.max_q ? a.T : a.B * a.max_q;
     if (g.kind == Geo::PROMPT && a.head_dim <= 128 && real * g.G / (2 * PROMPT_ROWS) * a.kv_heads >= 512)
         g.tile = 2 * PROMPT_ROWS;
@@ -487,9 +491,12 @@ static Geo geometry(int dtype, const AttnArgs &a)
         span = span < a.window + g.tile + ATT_STEP ? span : a.window + g.tile + ATT_STEP;
     const int64_t tiles = g.slots * a.kv_heads;
     g.tiles = (uint32_t)(tiles < UINT32_MAX ? tiles : UINT32_MAX); // more are refused
-    // Chunks such that the workgroups fill the chip in whole rounds, each one's start (about 3 us; a chunk of 2048
-    // tokens takes 40) being paid once a round; one round, unless the chunks would pass 2048 tokens: lengths may
-    // differ.  Several rounds of tiles are not split at all.
+    // Single tokens and the 16-row tiles: chunks such that the workgroups fill the chip in whole rounds of what the
+    // registers allow, each one's start (about 3 us; a chunk of 2048 tokens takes 40) being paid once a round; one
+    // round, unless the chunks would pass 2048 tokens: lengths may differ.  Several rounds of tiles are not split at
+    // all.  The chunks come from max_kv, the longest request: of requests of uneven lengths some workgroups are empty.
+    // A prompt's tiles: 768 parts, a round and a half of four-wave workgroups (310 tiles whole 107 us, in 512 / 768 /
+    // 1024 parts 126 / 105 / 113 with their join).
     const int64_t fill = g.kind == Geo::PROMPT ? 768 : 256 * attn_waves(dtype == LB_F32, (int)a.head_dim, g.kind == Geo::PACKED);
     constexpr int64_t UNIT = ATT_WAVES * ATT_STEP;
     // a prompt's part is 64 KB to write and read again: none where every CU has a tile

@@ -1,22 +1,27 @@
 // Attention of many new tokens over the 4-bit cache (the operator of kvattn.hip, for bfloat16 and binary16 rows).
 //
-// A workgroup takes 128 query rows (token, head of the kv head's group) and walks the tokens 64 at a time.  Its four
-// waves unpack the 64 keys and values once, into binary16 in LDS, and each wave multiplies them with its own 32
-// rows: S^T = K Q^T and O += P V on v_mfma_f32_32x32x16_f16.  S^T leaves the matrix core with a query row along the
-// lanes and runs of four tokens in each lane's registers, which is the order of the second product's left operand;
-// LDS holds the operands as the instructions read them, 16 bytes a lane and lanes side by side, so nothing is
-// shuffled and no bank is met twice.
+// A workgroup takes 128 or 256 query rows (token, head of the kv head's group) and walks the tokens 64 at a time.  Its
+// waves unpack the 64 keys and values once, into binary16 in LDS, and each multiplies them with its own 32 rows:
+// S^T = K Q^T and O += P V on v_mfma_f32_32x32x16_f16.  S^T leaves the matrix core with a query row along the lanes
+// and runs of four tokens in each lane's registers, which is the order of the second product's left operand; LDS holds
+// the operands as the instructions read them, 16 bytes a lane and lanes side by side, so nothing is shuffled and no
+// bank is met twice.
+//
+// Three forms, of about 250 registers a wave, so two waves a SIMD: four waves of 32 rows, two workgroups a CU; eight
+// waves of 32 rows, half of them unpacking keys and half values (geometry in kvattn.hip says where); eight waves in
+// halves, two of them with the same 32 rows and each with 32 of the 64 tokens (in_halves below).  At head size 256 the
+// registers are enough for one wave a SIMD, and there are four waves.
 //
 // What bounds it: instruction issue.  Per 32 rows and 32 tokens at head size 128 there are 512 cycles of matrix
 // instructions, about 280 of the vector unit for the scores (16 exponentials of 8 cycles, and a fused multiply-add,
 // a sum, a maximum and half a conversion each), and a share of the unpacking that falls with the rows a workgroup
-// has: tiles of 128 rows (four waves) spend 61 % of the cycles on vector instructions, tiles of 256 (eight waves,
-// each unpacking keys or values) a third less.  One prompt of 8192 tokens, 32 heads over 8: 740 us (745 TFLOP/s, a
-// large library matrix product reaches 1132 here); tiles of 128 rows 835 us, and 16 rows a wave, each unpacking for
-// itself, 1500 us.  Counted: the matrix cores are busy for 34 % of the cycles and the vector unit for 48 %, the two
-// together leaving under a fifth to waits; raising a wave's priority around its products changes nothing.  Four
-// prompts' chunks of 777 tokens after up to 1800, 20 heads over 5: 108 us, its longest tiles' own time.  LDS reads
-// (16 bytes a lane, 16 KB a wave and 32 tokens) are at a quarter of their rate.
+// has.  One prompt of 8192 tokens, 32 heads over 8: 653 us in an undisturbed stream (842 TFLOP/s, a large library
+// matrix product reaches 1132 here), 739 us a pass in the profiler's trace; tiles of 128 rows 719 us, and 16 rows a
+// wave, each unpacking for itself, 1500 us.  Counted: the matrix cores are busy for 34 % of the cycles and the vector
+// unit for 48 %, the two together leaving under a fifth to waits; raising a wave's priority around its products
+// changes nothing.  LDS reads (16 bytes a lane, 16 KB a wave and 32 tokens) are at a quarter of their rate.
+// Four prompts' chunks of 777 tokens after up to 1800, 20 heads over 5 (300 tiles, in halves): 87 us, matrix cores
+// 13 %, vector unit 31 %: neither bounds it, but the chain of a step in the longest tiles, 1.76 us per 64 tokens.
 //
 // Precision: a code times its block's scale is rounded to binary16 (scales have 11 bits and the codes 1.5, 3 and 6
 // two, so some lose one or two), and so are the weights: 2^-11 relative at most each, against the 2^-8 of a bfloat16

@@ -1,12 +1,13 @@
 // Rows into the paged 4-bit cache, and back.  32 consecutive values of a head share the scale
-// d = fp16_rne(amax / 6) (amax times the fp32 number next to 1/6, in fp32), and each value becomes the E2M1 number nearest to x / d, ties to
-// the even code.  The borders between neighbouring E2M1 numbers are .25 .75 1.25 1.75 2.5 3.5 5, and d times one
+// d = fp16_rne(amax * fp32(1/6)), and each value becomes the E2M1 number nearest to x / d, ties to the even code.  The
+// borders between neighbouring E2M1 numbers are .25 .75 1.25 1.75 2.5 3.5 5, and d times one
 // of them has 11 + 3 significant bits: the comparisons |x| against d * border are exact in fp32, without a
 // division, for every input type, and so is the code.
 //
 // Both directions are bound by HBM (2 to 4 bytes a value in or out, 9/16 byte in the cache).  16384 tokens of 8 heads
-// of 128: bfloat16 rows appended in 18.6 us (86 MB, 4.6 TB/s), read back as fp32 in 35 us (153 MB, 4.4 TB/s); a large
-// copy reaches 4.7 to 5.0 here.
+// of 128: 16-bit rows appended in 18.6 us (86 MB, 4.6 TB/s), fp32 rows in 35.6 us (153 MB, 4.3 TB/s: seven comparisons
+// a value in place of a conversion); read back as fp32 in 34 us (153 MB, 4.5 TB/s), as bfloat16 in 26 us (86 MB, 3.3
+// TB/s: there the single bytes of values, eight loads a lane, show).  A large copy reaches 4.7 to 5.0 here.
 #include "serve_internal.h"
 
 namespace lb {
@@ -22,8 +23,10 @@ __device__ __forceinline__ uint32_t quad_umax(uint32_t v)
 }
 
 // The block's scale from its magnitude's bit pattern: saturated at the largest binary16, NaN if a value is not
-// finite (the block then reads back as NaN rather than as some number).  The product with 1/6 is what PyTorch makes of
-// a division by 6 on the GPU, so scales computed there have the same bits; it is exact for 6 times a binary16.
+// finite (the block then reads back as NaN rather than as some number).  The format takes the product with fp32(1/6)
+// for amax / 6: one rounding like a quotient's, without a division, and for 6 times a binary16 it rounds to that
+// binary16, so that fp32 rows read back and appended again keep their values (scales below binary16's normal range
+// may not: there the largest code need not be 6).
 __device__ __forceinline__ uint32_t scale_bits(uint32_t amax)
 {
     if (amax >= 0x7f800000u)
