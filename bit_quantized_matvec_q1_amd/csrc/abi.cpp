@@ -37,10 +37,10 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool is_wfmt(int f)
 {
-    return f == LB_Q1_0 || f == LB_Q2_0_G64 || f == LB_TERNARY_PLANAR || f == LB_Q8_0 || f == LB_TERNARY_B3;
+    return f >= LB_Q1_0 && f <= LB_Q4_0;
 }
 // K must be a multiple of this (base-3 rows are whole planar widths; their beats hold 80 columns)
-int64_t block_weights(int f) { return f == LB_Q1_0 ? 128 : f == LB_Q8_0 ? 32 : 64; }
+int64_t block_weights(int f) { return lb::slice_weights(f); }
 int64_t block_bytes(int f) { return f == LB_TERNARY_PLANAR ? 16 : f == LB_Q8_0 ? 34 : 18; }
 int paired_afmt(int f) { return f == LB_TERNARY_PLANAR || f == LB_TERNARY_B3 ? LB_ACT_I8_ROW : LB_ACT_Q8_0; }
 // bytes of an N x K tensor (K a multiple of block_weights)
@@ -87,17 +87,17 @@ lb_status check_product(const char *fn, int fmt, const void *W, int64_t N, int64
         return fail(LB_EINVAL, fn, "unknown weight or activation format");
     if (afmt != paired_afmt(fmt))
         return fail(LB_EINVAL, fn, "activation format does not match the weight format "
-                                   "(Q1_0/Q2_0_g64/Q8_0 take LB_ACT_Q8_0, planar takes LB_ACT_I8_ROW)");
+                                   "(Q1_0/Q2_0_g64/Q4_0/Q8_0 take LB_ACT_Q8_0, planar takes LB_ACT_I8_ROW)");
     if (N < 0 || K < 0)
         return fail(LB_ESHAPE, fn, "negative size");
     if (K % block_weights(fmt))
-        return fail(LB_ESHAPE, fn, "K is not a multiple of the weight block (128 for Q1_0, 32 for Q8_0, 64 otherwise)");
+        return fail(LB_ESHAPE, fn, "K is not a multiple of the weight block (128 for Q1_0, 32 for Q4_0 and Q8_0, 64 otherwise)");
     if (fmt == LB_TERNARY_B3 && K > 30720) // a row is at most 64 lanes of six 80-column beats
         return fail(LB_ESHAPE, fn, "K above 30720 for base-3 beats");
     if (K > 32768 || N > INT32_MAX)
         return fail(LB_ESHAPE, fn, "K above 32768 or N above 2^31-1");
-    if (fmt == LB_Q8_0 && K > 16384) // a row is at most one wave of lanes with 8 blocks each
-        return fail(LB_ESHAPE, fn, "K above 16384 for Q8_0");
+    if ((fmt == LB_Q8_0 || fmt == LB_Q4_0) && K > 16384) // a row is at most one wave of lanes with 8 blocks each
+        return fail(LB_ESHAPE, fn, "K above 16384 for Q4_0 or Q8_0");
     if (tensor_bytes(fmt, N, K) >= (int64_t(1) << 32))
         return fail(LB_ESHAPE, fn, "weight tensor of 4 GiB or more");
     if (N == 0)
@@ -248,8 +248,8 @@ static lb_status gemm_common(const char *fn, int fmt, const void *W, int64_t N, 
         return fail(LB_ESHAPE, fn, "output of 2^31 elements or more");
     if (M * K >= (int64_t(1) << 32))
         return fail(LB_ESHAPE, fn, "activation matrix of 4 GiB or more");
-    if (fmt == LB_Q8_0 && K % 128)
-        return fail(LB_ESHAPE, fn, "Q8_0 prefill needs K to be a multiple of 128");
+    if ((fmt == LB_Q8_0 || fmt == LB_Q4_0) && K % 128)
+        return fail(LB_ESHAPE, fn, "Q4_0 and Q8_0 prefill need K to be a multiple of 128");
     st = check_device(fn);
     if (st != LB_OK)
         return st;
@@ -382,7 +382,7 @@ lb_status lowbit_read_probe(const void *buf, int64_t nbytes, uint32_t *sink, hip
 // 256 KiB and base-3 with 224 KiB.
 static int64_t default_tile_bytes(int fmt, int64_t K)
 {
-    if (fmt == LB_Q1_0 || fmt == LB_Q2_0_G64)
+    if (fmt == LB_Q1_0 || fmt == LB_Q2_0_G64 || fmt == LB_Q4_0)
         return (K > 8192 ? 96 : 64) * 1024;
     return (fmt == LB_TERNARY_B3 ? 224 : 256) * 1024;
 }
@@ -574,8 +574,8 @@ lb_status batch_plan(const char *fn, const lb_matvec_desc *list, int32_t n, Batc
         lb_status st;
         if (d.afmt == LB_ACT_F32_Q8_0) {
             // fp32 activations quantised in the product's own launch
-            if (is_wfmt(d.fmt) && d.fmt != LB_Q1_0 && d.fmt != LB_Q2_0_G64)
-                return fail(LB_EUNSUPPORTED, fn, "LB_ACT_F32_Q8_0 is for Q1_0 and Q2_0_g64 weights only");
+            if (is_wfmt(d.fmt) && d.fmt != LB_Q1_0 && d.fmt != LB_Q2_0_G64 && d.fmt != LB_Q4_0)
+                return fail(LB_EUNSUPPORTED, fn, "LB_ACT_F32_Q8_0 is for Q1_0, Q2_0_g64 and Q4_0 weights only");
             if (d.N > 0 && !d.x)
                 return fail(LB_EINVAL, fn, "null x for LB_ACT_F32_Q8_0");
             if (d.N > 0 && !aligned(d.x, 16))

@@ -12,7 +12,7 @@
 //    double-buffered LDS -- the weights unpacked to int8 in natural column order (shift and mask, a 4x4
 //    byte transpose with v_perm_b32, and a v_perm_b32 lookup from code to weight byte: Q2_0 c -> c - 1,
 //    Q1_0 bit -> +/-1, planar (pos, neg) -> pos - neg; Q8_0 weights are int8 already and copied as they
-//    are) -- and one barrier per step separates the writes from the reads.  Every thread loads and
+//    are; a Q4_0 nibble w, moved to its byte's upper half, is the int8 16 w, whose factor the weight scale takes back) -- and one barrier per step separates the writes from the reads.  Every thread loads and
 //    unpacks an equal share of the weight tile and issues an equal share of the activation tile.
 //  * A workgroup is 8 waves (512 threads), two per SIMD, and two workgroups fit a CU.  Wave w computes
 //    the 32 x 32 output tile (weight rows 32 (w mod 2), activation rows 32 (w / 2)) over every step's
@@ -20,7 +20,7 @@
 //    operand (activations) from LDS, one MFMA, one exact int32 sum per (weight row, activation row,
 //    block).  The weight unpack is shared by the 128 activation rows of the tile and the activation copy
 //    by its 64 weight rows, so per MFMA the per-step work stays small next to the rescale below.
-//  * Q1_0, Q2_0 and Q8_0: the accumulator input of every MFMA is a constant register tile holding
+//  * Q1_0, Q2_0, Q4_0 and Q8_0: the accumulator input of every MFMA is a constant register tile holding
 //    0x4B400000 (1.5 * 2^23), so each result, read as fp32, is 1.5 * 2^23 + isum exactly; one FMA with the
 //    block's activation scale and -d_x * 1.5 * 2^23 gives round(d_x * isum) without a conversion.  The
 //    weight block scale is then applied with one more FMA (bankml technical report, section III.3: one
@@ -78,8 +78,8 @@ __device__ __forceinline__ void unpack_q2_dword(uint32_t v, uint32_t *out)
 
 // What one thread carries from global memory into a K-step's weight tile.  Every thread takes one share of
 // it -- Q2_0: one code dword (16 weights); Q1_0: one sign dword, of which it builds two of the four
-// activation blocks; planar: one (pos, neg) dword pair, of which it builds half; Q8_0: 16 weight bytes --
-// in a (planar neg in a.y; the weight block scale's binary16 where the thread stores it in
+// activation blocks; planar: one (pos, neg) dword pair, of which it builds half; Q4_0: two dwords (16
+// weights); Q8_0: 16 weight bytes -- in a (planar neg in a.y; the weight block scale's binary16 where the thread stores it in
 // sc, sh), and, for the first TM threads, the four binary16 activation scales of one activation row in c.
 struct StepRegs {
     uint4 a;
@@ -110,16 +110,19 @@ struct LaneOffs {
     uint32_t x[2];  // its two activation-tile slots: row offset + 16 x chunk (x_slot)
 };
 
-// Bytes a step advances each base by: weight records (16 bytes per 64 Q2_0 / planar or 128 Q1_0 weights, 32
+// Whether every 32 weights have a scale of their own: Q4_0, Q8_0
+constexpr bool scale32(int fmt) { return fmt == LB_Q8_0 || fmt == LB_Q4_0; }
+
+// Bytes a step advances each base by: weight records (16 bytes per 64 Q2_0 / planar, 128 Q1_0 or 32 Q4_0 weights, 32
 // per 32 Q8_0 weights), their binary16 scales, the activation scales (binary16 per 32) and the activation
 // bytes themselves.
 template <int FMT> __device__ __forceinline__ uint32_t step_wbytes(int kk)
 {
-    return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 16u : FMT == LB_Q8_0 ? (uint32_t)kk : (uint32_t)(kk / 64) * 16u;
+    return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 16u : FMT == LB_Q8_0 ? (uint32_t)kk : FMT == LB_Q4_0 ? (uint32_t)kk / 2 : (uint32_t)(kk / 64) * 16u;
 }
 template <int FMT> __device__ __forceinline__ uint32_t step_sbytes(int kk)
 {
-    return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 2u : FMT == LB_Q8_0 ? (uint32_t)(kk / 32) * 2u : (uint32_t)(kk / 64) * 2u;
+    return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 2u : scale32(FMT) ? (uint32_t)(kk / 32) * 2u : (uint32_t)(kk / 64) * 2u;
 }
 
 template <int FMT>
@@ -132,6 +135,9 @@ __device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, in
         o.ws = (uint32_t)row * (uint32_t)(K / 128) * 2u;
     } else if (FMT == LB_Q8_0) { // four 32-byte records per row; thread p takes half p % 2 of record p / 2
         o.w = (uint32_t)row * (uint32_t)K + 32u * (uint32_t)(p >> 1) + 16u * (uint32_t)(p & 1);
+        o.ws = ((uint32_t)row * (uint32_t)(K / 32) + (uint32_t)(p >> 1)) * 2u;
+    } else if (FMT == LB_Q4_0) { // four 16-byte records per row; thread p takes half p % 2 of record p / 2
+        o.w = (uint32_t)row * (uint32_t)(K / 2) + 16u * (uint32_t)(p >> 1) + 8u * (uint32_t)(p & 1);
         o.ws = ((uint32_t)row * (uint32_t)(K / 32) + (uint32_t)(p >> 1)) * 2u;
     } else if (FMT == LB_Q2_0_G64) { // two 64-weight records per row; thread p takes dword p % 4 of record p / 4
         o.w = ((uint32_t)row * (uint32_t)(K / 64) + (uint32_t)(p >> 2)) * 16u + 4u * (uint32_t)(p & 3);
@@ -189,6 +195,9 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
     if (FMT == LB_Q8_0) {
         const v4u t = *(const gv4u *)((const gu8 *)W + ow);
         r.a = make_uint4(t.x, t.y, t.z, t.w);
+    } else if (FMT == LB_Q4_0) {
+        const v2u_a4 t = *(const gv2u *)((const gu8 *)W + ow);
+        r.a.x = t.x, r.a.y = t.y;
     } else if (FMT == LB_TERNARY_PLANAR) {
         r.a.x = *(const gu32 *)((const gu8 *)W + ow);        // pos
         r.a.y = *(const gu32 *)((const gu8 *)W + (ow + 8u)); // neg
@@ -285,6 +294,15 @@ __device__ __forceinline__ void store_step(Lds &lds, int buf, const StepRegs &r,
         *reinterpret_cast<uint4 *>(wrow + 8 * j + 4 * (p & 1)) = r.a;
         if ((p & 1) == 0)
             lds.dw[buf][j * TN + rr] = half_bits_to_float((uint16_t)(r.sc >> r.sh));
+    } else if (FMT == LB_Q4_0) {
+        // nibble n of a dword is its weight n: even and odd ones to the upper halves of bytes, then interleaved
+        const int j = p >> 1;
+        const uint32_t e0 = (r.a.x << 4) & 0xF0F0F0F0u, o0 = r.a.x & 0xF0F0F0F0u;
+        const uint32_t e1 = (r.a.y << 4) & 0xF0F0F0F0u, o1 = r.a.y & 0xF0F0F0F0u;
+        *reinterpret_cast<uint4 *>(wrow + 8 * j + 4 * (p & 1)) =
+            make_uint4(perm(o0, e0, 0x05010400u), perm(o0, e0, 0x07030602u), perm(o1, e1, 0x05010400u), perm(o1, e1, 0x07030602u));
+        if ((p & 1) == 0) // the products are 16 isum: exact powers of two, |16 isum| <= 16 * 32 * 8 * 128 < 2^22
+            lds.dw[buf][j * TN + rr] = half_bits_to_float((uint16_t)(r.sc >> r.sh)) * 0.0625f;
     } else if (FMT == LB_Q2_0_G64) {
         const int bb = p >> 2, d = p & 3;
         const bool live = 2 * bb < kab;
@@ -324,7 +342,7 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
                                              int32_t *__restrict__ sums)
 {
     constexpr bool PLANAR = FMT == LB_TERNARY_PLANAR;
-    constexpr int JW = FMT == LB_Q1_0 ? 4 : FMT == LB_Q8_0 ? 1 : 2; // activation blocks per weight block
+    constexpr int JW = FMT == LB_Q1_0 ? 4 : scale32(FMT) ? 1 : 2; // activation blocks per weight block
     const uint32_t *wl = lds.w[buf] + (32 * wn + l32) * WROW + 4 * h;
     auto mfma = [&](int j, const v16i &c) {
         const uint4 a4 = *reinterpret_cast<const uint4 *>(wl + 8 * j);
@@ -375,7 +393,7 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
             for (int i = 0; i < 16; i++) {
                 const int n = n0 + 32 * wn + 8 * (i >> 2) + 4 * h + (i & 3);
                 if (m < M && n < N && kb < nab) // (the zero blocks of a half step have no sums)
-                    sums[((int64_t)m * N + n) * nab + kb] = Dj[i] - (int)BIAS;
+                    sums[((int64_t)m * N + n) * nab + kb] = (Dj[i] - (int)BIAS) >> (FMT == LB_Q4_0 ? 4 : 0);
             }
         }
     }
@@ -404,7 +422,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     const int wn = wave & 1, wm = wave >> 1;
     const int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
     const int n0 = bn * TN, m0 = bm * TM;
-    const int64_t rowcode = FMT == LB_Q1_0 ? K / 8 : FMT == LB_Q8_0 ? K : K / 4; // code bytes per weight row
+    const int64_t rowcode = FMT == LB_Q1_0 ? K / 8 : FMT == LB_Q8_0 ? K : FMT == LB_Q4_0 ? K / 2 : K / 4; // code bytes per weight row
     const int nab = K / QK8;                                                  // activation blocks per row
     const uint8_t *wsc = W + (int64_t)N * rowcode;
     const uint8_t *xsc = reinterpret_cast<const uint8_t *>(Xscale);
@@ -601,6 +619,9 @@ hipError_t launch_gemm(int fmt, const uint8_t *W, int64_t N, int64_t K, float w_
     case LB_Q8_0:
         return emit ? launch_fmt<LB_Q8_0, true>(W, N, K, w_scale, Xq, Xscale, M, Y, sums, s)
                     : launch_fmt<LB_Q8_0, false>(W, N, K, w_scale, Xq, Xscale, M, Y, sums, s);
+    case LB_Q4_0:
+        return emit ? launch_fmt<LB_Q4_0, true>(W, N, K, w_scale, Xq, Xscale, M, Y, sums, s)
+                    : launch_fmt<LB_Q4_0, false>(W, N, K, w_scale, Xq, Xscale, M, Y, sums, s);
     case LB_TERNARY_B3:
         return hipErrorNotSupported; // decode only
     }

@@ -12,10 +12,10 @@ namespace lb {
 constexpr int QK8 = 32;   // activations per q8_0 block
 constexpr int WG = 256;   // threads per workgroup for the streaming kernels (4 wave64)
 
-// Weights per 16-byte code record ("slice"): one Q2_0_g64 block, one Q1_0 block's sign bits, one
+// Weights per 16-byte code record ("slice"): one Q2_0_g64 block, one Q1_0 block's sign bits, one Q4_0 block, one
 // planar beat.  The device layout of the ggml formats is [N][K/QK][16 B] code records followed by
 // [N][K/QK] binary16 scales.
-constexpr int slice_weights(int fmt) { return fmt == LB_Q1_0 ? 128 : fmt == LB_Q8_0 ? 32 : 64; }
+constexpr int slice_weights(int fmt) { return fmt == LB_Q1_0 ? 128 : fmt == LB_Q8_0 || fmt == LB_Q4_0 ? 32 : 64; }
 
 inline __device__ float half_bits_to_float(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 
@@ -151,6 +151,12 @@ hipError_t launch_q8(const uint8_t *W, int64_t N, int64_t K, const int8_t *xq, c
                      int32_t *sums, hipStream_t s);
 hipError_t launch_q8_batched(const BatchGroup &g, size_t lds, hipStream_t s);
 int q8_blocks_per_cu(int cfg, size_t lds);
+
+// Q4_0 weights x q8_0 activations (q4.hip): the kernels and configurations of matvec_tile.h
+hipError_t launch_q4(int cfg, const uint8_t *W, int64_t N, int64_t K, const int8_t *xq, const uint16_t *xs, float *y, int32_t *sums,
+                     int tile_rows, hipStream_t s);
+hipError_t launch_q4_batched(const BatchGroup &g, size_t lds, hipStream_t s);
+int q4_blocks_per_cu(int cfg, bool full, bool qin, size_t lds);
 
 // the planar product by bit-serial popcounts (popcount.hip): a third implementation for differential tests
 hipError_t launch_popcount(const uint8_t *W, int64_t N, int64_t K, float w_scale, const int8_t *xq, const float *xs,

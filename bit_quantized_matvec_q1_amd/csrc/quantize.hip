@@ -167,6 +167,30 @@ __device__ __forceinline__ void q1_from_device(const uint32_t (&dev)[4], uint32_
     }
 }
 
+// Q4_0: byte j of the ggml block holds the codes (weight + 8) of weights j (low nibble) and j + 16; dword k of the device
+// record holds weights 8k .. 8k + 7, nibble by nibble, in two's complement.
+__device__ __forceinline__ void q4_to_device(const uint32_t (&nat)[4], uint32_t (&dev)[4])
+{
+    for (int k = 0; k < 4; k++) { // weights 8k + n are in bytes 8 (k & 1) + n, the upper nibbles where k >= 2
+        const int sh = k < 2 ? 0 : 4, b = 2 * (k & 1);
+        uint32_t v = 0;
+        for (int n = 0; n < 8; n++)
+            v |= ((nat[b + (n >> 2)] >> (8 * (n & 3) + sh)) & 15u) << (4 * n);
+        dev[k] = v ^ 0x88888888u;
+    }
+}
+
+__device__ __forceinline__ void q4_from_device(const uint32_t (&dev)[4], uint32_t (&nat)[4])
+{
+    for (int d = 0; d < 4; d++) { // bytes 4d + i: weights 4d + i and 4d + i + 16
+        const uint32_t lo = (dev[d >> 1] ^ 0x88888888u) >> (16 * (d & 1)), hi = (dev[2 + (d >> 1)] ^ 0x88888888u) >> (16 * (d & 1));
+        uint32_t v = 0;
+        for (int i = 0; i < 4; i++)
+            v |= (((lo >> (4 * i)) & 15u) | ((hi >> (4 * i)) & 15u) << 4) << (8 * i);
+        nat[d] = v;
+    }
+}
+
 __global__ __launch_bounds__(WG) void pack_kernel(int fmt, const uint8_t *__restrict__ src, int64_t nblk,
                                                   uint8_t *__restrict__ dst, int unpack)
 {
@@ -202,7 +226,7 @@ __global__ __launch_bounds__(WG) void pack_kernel(int fmt, const uint8_t *__rest
         return;
     }
     // 16 code bytes of an 18-byte ggml block <-> one 16-byte device record (+ the binary16 scale in the
-    // scale array); Q1_0 records also permute their bits (above), Q2_0_g64 records keep them as they are
+    // scale array); Q1_0 and Q4_0 records also permute their bits (above), Q2_0_g64 records keep them as they are
     const uint8_t *in = unpack ? src + b * 16 : src + b * 18 + 2;
     uint8_t *out = unpack ? dst + b * 18 + 2 : dst + b * 16;
     uint32_t w[4], o[4];
@@ -214,6 +238,11 @@ __global__ __launch_bounds__(WG) void pack_kernel(int fmt, const uint8_t *__rest
             q1_from_device(w, o);
         else
             q1_to_device(w, o);
+    } else if (fmt == LB_Q4_0) {
+        if (unpack)
+            q4_from_device(w, o);
+        else
+            q4_to_device(w, o);
     } else {
         for (int d = 0; d < 4; d++)
             o[d] = w[d];
@@ -234,7 +263,7 @@ hipError_t launch_pack(int fmt, const uint8_t *blocks, int64_t N, int64_t K, uin
                        hipStream_t s)
 {
     const int64_t nblk = fmt == LB_TERNARY_B3 ? N * ((K + 79) / 80) // beats of 16 bytes
-                                              : N * (K / (fmt == LB_Q1_0 ? 128 : fmt == LB_Q8_0 ? 32 : 64));
+                                              : N * (K / slice_weights(fmt));
     const int64_t grid = (nblk + WG - 1) / WG;
     if (unpack)
         hipLaunchKernelGGL(pack_kernel, dim3((unsigned)grid), dim3(WG), 0, s, fmt, (const uint8_t *)packed, nblk,

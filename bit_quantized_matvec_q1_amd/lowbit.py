@@ -12,7 +12,7 @@ import os
 
 import torch
 
-Q1_0, Q2_0_G64, TERNARY_PLANAR, Q8_0, TERNARY_B3 = 1, 2, 3, 4, 5
+Q1_0, Q2_0_G64, TERNARY_PLANAR, Q8_0, TERNARY_B3, Q4_0 = 1, 2, 3, 4, 5, 6
 ACT_Q8_0, ACT_I8_ROW, ACT_F32_Q8_0 = 1, 2, 3
 F32, BF16, F16 = 0, 1, 2
 LB_OK, LB_EINVAL, LB_ESHAPE, LB_EALIGN, LB_EUNSUPPORTED, LB_EDEVICE, LB_ENOMEM = range(7)

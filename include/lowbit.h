@@ -17,6 +17,10 @@
  *                     III.2, used for weights ("Q8_0 weights" and vec_dot_q8_0_q8_0 for the KV cache in
  *                     the bankml build history's 0.3.9 entry).  Decode takes K up to 16384; prefill
  *                     (lowbit_gemm, lowbit_block_sums with M > 1) also needs K % 128 == 0 (LB_ESHAPE).
+ *   LB_Q4_0           ggml Q4_0: 18-byte blocks of 32 weights, binary16 scale d then 16 bytes of 4-bit codes, byte j
+ *                     holding weight j in its low and weight j + 16 in its high nibble; weight = (code - 8) * d.
+ *                     Decode takes K up to 16384; prefill (lowbit_gemm, lowbit_block_sums with M > 1) also needs
+ *                     K % 128 == 0 (LB_ESHAPE).
  *   LB_TERNARY_B3     base-3 ternary beats: 16 bytes per 80 consecutive columns of one row, byte j holding
  *                     columns 5j..5j+4 as the integer sum_t (w + 1) * 3^t, lowest digit first (0..242);
  *                     a row of K columns (K % 64 == 0) takes ceil(K/80) beats, the columns past K coded 0.
@@ -28,12 +32,12 @@
  * Activation formats:
  *   LB_ACT_Q8_0       ggml q8_0: int8 xq[M][K] plus binary16 scales xscale[M][K/32]; one block of 32
  *                     activations per scale (bankml technical report, section III.2).  Used with the
- *                     two ggml weight formats.
+ *                     ggml weight formats.
  *   LB_ACT_I8_ROW     int8 xq[M][K] plus one fp32 scale per row (per token), xscale[M] (tritium
  *                     "Architecture", section 1: activations are int8).  Used with the planar format.
  *   LB_ACT_F32_Q8_0   fp32 x[K], quantised to q8_0 by the batch itself, with exactly the arithmetic of
  *                     lowbit_quantize_act(LB_ACT_Q8_0) (so the results are bit-identical to quantising
- *                     first).  Batched decode of LB_Q1_0 and LB_Q2_0_G64 only: a product that depends on the
+ *                     first).  Batched decode of LB_Q1_0, LB_Q2_0_G64 and LB_Q4_0 only: a product that depends on the
  *                     previous one's output then needs no quantise call of its own.  Rows of at most 8192
  *                     columns are quantised inside the products' own launch (every workgroup quantises
  *                     the row it stages); a batch from lowbit_batch_create quantises longer rows with one
@@ -62,13 +66,13 @@
 extern "C" {
 #endif
 
-typedef enum { LB_Q1_0 = 1, LB_Q2_0_G64 = 2, LB_TERNARY_PLANAR = 3, LB_Q8_0 = 4, LB_TERNARY_B3 = 5 } lb_wfmt;
+typedef enum { LB_Q1_0 = 1, LB_Q2_0_G64 = 2, LB_TERNARY_PLANAR = 3, LB_Q8_0 = 4, LB_TERNARY_B3 = 5, LB_Q4_0 = 6 } lb_wfmt;
 typedef enum { LB_ACT_Q8_0 = 1, LB_ACT_I8_ROW = 2, LB_ACT_F32_Q8_0 = 3 } lb_afmt;
 
 typedef enum {
     LB_OK = 0,
     LB_EINVAL = 1,       /* null pointer, unknown enum, or a weight/activation format pairing that is not defined */
-    LB_ESHAPE = 2,       /* negative size, K not a multiple of the weight block (128, 64, 64, 32, 64), or over a limit */
+    LB_ESHAPE = 2,       /* negative size, K not a multiple of the weight block (128, 64, 64, 32, 64, 32), or over a limit */
     LB_EALIGN = 3,       /* a pointer is not aligned as its argument requires */
     LB_EUNSUPPORTED = 4, /* the current device is not gfx950, or the entry point has no kernel for the format */
     LB_EDEVICE = 5,      /* a HIP call failed; lowbit_last_error() holds the runtime's message */
@@ -83,9 +87,9 @@ const char *lowbit_status_str(lb_status st);
 const char *lowbit_last_error(void);
 
 /*
- * Bytes of the device layout of an N x K weight tensor in format `fmt`: 18 per Q1_0 / Q2_0_g64 block (128
- * or 64 weights), 34 per Q8_0 block (32 weights), 16 per planar beat (64 columns) or base-3 beat (80
- * columns, ceil(K/80) per row) -- the same count as the on-disk format (1.125, 2.25, 8.5, 2 and 1.6 bits
+ * Bytes of the device layout of an N x K weight tensor in format `fmt`: 18 per Q1_0 / Q2_0_g64 / Q4_0 block (128,
+ * 64 or 32 weights), 34 per Q8_0 block (32 weights), 16 per planar beat (64 columns) or base-3 beat (80
+ * columns, ceil(K/80) per row) -- the same count as the on-disk format (1.125, 2.25, 4.5, 8.5, 2 and 1.6 bits
  * per weight; bankml technical report sections III.2, III.5 and III.8).
  * Returns -1 for a bad format or shape.
  */
@@ -100,7 +104,8 @@ int64_t lowbit_weight_bytes(int fmt, int64_t N, int64_t K);
  *           A Q2_0_g64 record is the block's 16 code bytes as they are.  A Q1_0 record permutes the
  *           block's 128 sign bits: the sign of weight 32r + 8m + k (r, m in 0..3, k in 0..7), at bit
  *           8m + k of little-endian dword r in the ggml block, sits at bit 4k + r of dword m, so one
- *           mask (0x11111111 << r) isolates eight weights of activation block r as nibbles.
+ *           mask (0x11111111 << r) isolates eight weights of activation block r as nibbles.  A Q4_0 record holds
+ *           weight 8k + n (k in 0..3, n in 0..7), in 4-bit two's complement, at bits 4n..4n+3 of dword k.
  * Lossless (lowbit_unpack_weights is its inverse).  For LB_TERNARY_PLANAR the beat stream already is
  * the device layout (tritium "Architecture", section 2: the file layout is the beat stream) and pack
  * copies it unchanged.  For LB_TERNARY_B3 pack keeps the beat stream and writes each base-3 byte v as
@@ -130,7 +135,7 @@ lb_status lowbit_quantize_act(int afmt, const float *x, int64_t M, int64_t K, in
  *   afmt:   LB_ACT_Q8_0 for the ggml formats, LB_ACT_I8_ROW for planar and base-3 beats.
  *   xq:     device int8 [K], 16-byte aligned.  xscale: binary16 [K/32] or one fp32, 4-byte aligned.
  *   y:      device fp32 [N], 4-byte aligned.
- * Limits: K <= 32768 (16384 for LB_Q8_0, 30720 for LB_TERNARY_B3) and N <= 2^31 - 1; the weight tensor must
+ * Limits: K <= 32768 (16384 for LB_Q4_0 and LB_Q8_0, 30720 for LB_TERNARY_B3) and N <= 2^31 - 1; the weight tensor must
  * be smaller than 4 GiB.
  */
 lb_status lowbit_matvec(int fmt, const void *W, int64_t N, int64_t K, float w_tensor_scale, int afmt,
@@ -145,7 +150,7 @@ lb_status lowbit_matvec(int fmt, const void *W, int64_t N, int64_t K, float w_te
  *   Xq: device int8 [M][K], 16-byte aligned; Xscale: binary16 [M][K/32] (ggml formats) or fp32 [M].
  *   Y:  device fp32 [M][N], 4-byte aligned.
  * Limits (else LB_ESHAPE): those of lowbit_matvec, M * N < 2^31 outputs, M * K < 2^32 activation bytes,
- * and K % 128 == 0 for LB_Q8_0.  LB_TERNARY_B3 has no prefill kernel (LB_EUNSUPPORTED).
+ * and K % 128 == 0 for LB_Q4_0 and LB_Q8_0.  LB_TERNARY_B3 has no prefill kernel (LB_EUNSUPPORTED).
  */
 lb_status lowbit_gemm(int fmt, const void *W, int64_t N, int64_t K, float w_tensor_scale, int afmt,
                       const int8_t *Xq, const void *Xscale, int64_t M, float *Y, hipStream_t s);
@@ -219,7 +224,7 @@ typedef struct lb_batch lb_batch;
 /* list: HOST array of n descriptors (n >= 1).  On success *out owns device memory until destroyed;
  * lowbit_batch_destroy frees it (hipFree, which waits for the device), so no launch may use it after.
  * The buffers the descriptors point to must stay valid while the batch is used.  A descriptor with
- * afmt LB_ACT_F32_Q8_0 takes its activations from x and needs fmt LB_Q1_0 or LB_Q2_0_G64 (else
+ * afmt LB_ACT_F32_Q8_0 takes its activations from x and needs fmt LB_Q1_0, LB_Q2_0_G64 or LB_Q4_0 (else
  * LB_EUNSUPPORTED); null x is LB_EINVAL, x not 16-byte aligned LB_EALIGN. */
 lb_status lowbit_batch_create(const lb_matvec_desc *list, int32_t n, lb_batch **out);
 lb_status lowbit_matvec_batched(const lb_batch *b, hipStream_t s);
