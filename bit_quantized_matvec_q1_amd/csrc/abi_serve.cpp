@@ -159,6 +159,57 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
                        s);
 }
 
+lb_status lowbit_kv_append_rotary(int dtype, const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, const int32_t *positions, const float *inv_freq, int64_t rotary_dim, int style,
+                                  float factor, const int64_t *slots, void *cache, int64_t pages, int64_t page_tokens, hipStream_t s)
+{
+    const char *fn = "lowbit_kv_append_rotary";
+    if (!is_dtype(dtype))
+        return lb::abi_fail(LB_EINVAL, fn, "unknown row type");
+    if (style != LB_ROTARY_HALVES && style != LB_ROTARY_PAIRS)
+        return lb::abi_fail(LB_EINVAL, fn, "unknown style of rotation");
+    lb_status st = check_cache(fn, pages, kv_heads, page_tokens, head_dim);
+    if (st != LB_OK)
+        return st;
+    if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16)
+        return lb::abi_fail(LB_ESHAPE, fn, "rotary_dim must be a multiple of 16, from 16 to head_dim");
+    if (q_heads < 0 || q_heads > 65536)
+        return lb::abi_fail(LB_ESHAPE, fn, "q_heads must be from 0 to 65536");
+    // a launch's threads are numbered in 32 bits, head_dim / 8 of them a row and head; a grid has 65535 runs of heads at most
+    const int64_t heads = q_heads + kv_heads;
+    if (heads > 65535)
+        return lb::abi_fail(LB_ESHAPE, fn, "over 65535 heads in all");
+    if (T < 0 || T > kMax || (T + 31) * heads * (head_dim / 8) >= (int64_t)1 << 32)
+        return lb::abi_fail(LB_ESHAPE, fn, "negative T, or T * (q_heads + kv_heads) * head_dim of 2^35 or more");
+    if (T == 0)
+        return LB_OK;
+    if (!positions || !inv_freq || !slots || (!cache && pages))
+        return lb::abi_fail(LB_EINVAL, fn, "null pointer");
+    st = check_rows(fn, k, k_stride, kv_heads * head_dim, dtype);
+    if (st == LB_OK)
+        st = check_rows(fn, v, v_stride, kv_heads * head_dim, dtype);
+    if (st == LB_OK && q_heads)
+        st = check_rows(fn, q, q_stride, q_heads * head_dim, dtype);
+    if (st == LB_OK && q_heads)
+        st = check_rows(fn, q_out, q_out_stride, q_heads * head_dim, dtype);
+    if (st != LB_OK)
+        return st;
+    if (q_heads && q_out == q && q_stride != q_out_stride)
+        return lb::abi_fail(LB_ESHAPE, fn, "in place, both strides of the queries have to be the same");
+    if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(inv_freq, 4))
+        return lb::abi_fail(LB_EALIGN, fn, "the cache needs 16-byte alignment, slots 8-byte, positions and inv_freq 4-byte alignment");
+    st = lb::abi_check_device(fn);
+    if (st != LB_OK)
+        return st;
+    lb::RotaryArgs a = {};
+    a.q = q, a.k = k, a.v = v, a.q_out = q_out, a.q_stride = q_stride, a.q_out_stride = q_out_stride, a.k_stride = k_stride;
+    a.v_stride = v_stride, a.T = T, a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim, a.rotary_dim = rotary_dim;
+    a.positions = positions, a.inv_freq = inv_freq, a.factor = factor, a.pairs = style == LB_ROTARY_PAIRS, a.slots = slots;
+    a.cache = static_cast<uint8_t *>(cache), a.pages = pages, a.page_tokens = page_tokens;
+    return lb::abi_hip(fn, lb::launch_kv_append_rotary(dtype, a, s));
+}
+
 // Sizes of an attention call; the ones the workspace depends on.
 static lb_status attn_sizes(const char *fn, lb::AttnArgs &a, int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                             int64_t max_q, int64_t max_kv, int64_t window)

@@ -81,6 +81,20 @@ struct RowsArgs { // append (k, v read) and read (k, v written)
 hipError_t launch_kv_append(int dtype, const RowsArgs &a, hipStream_t s);
 hipError_t launch_kv_read(int dtype, const RowsArgs &a, hipStream_t s);
 
+struct RotaryArgs {
+    const void *q, *k, *v; // q, q_out unused where q_heads is 0
+    void *q_out;
+    int64_t q_stride, q_out_stride, k_stride, v_stride, T, q_heads, kv_heads, head_dim, rotary_dim;
+    const int32_t *positions;
+    const float *inv_freq;
+    float factor;
+    bool pairs;
+    const int64_t *slots;
+    uint8_t *cache;
+    int64_t pages, page_tokens;
+};
+hipError_t launch_kv_append_rotary(int dtype, const RotaryArgs &a, hipStream_t s);
+
 struct AttnArgs {
     const void *q;
     void *out;

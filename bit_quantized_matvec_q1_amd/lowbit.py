@@ -15,6 +15,7 @@ import torch
 Q1_0, Q2_0_G64, TERNARY_PLANAR, Q8_0, TERNARY_B3, Q4_0 = 1, 2, 3, 4, 5, 6
 ACT_Q8_0, ACT_I8_ROW, ACT_F32_Q8_0 = 1, 2, 3
 F32, BF16, F16 = 0, 1, 2
+ROTARY_HALVES, ROTARY_PAIRS = 0, 1
 LB_OK, LB_EINVAL, LB_ESHAPE, LB_EALIGN, LB_EUNSUPPORTED, LB_EDEVICE, LB_ENOMEM = range(7)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblowbit.so")
@@ -50,6 +51,8 @@ SIGNATURES = {
     "lowbit_kv_release": (_I, [_P, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _P, _P]),
     "lowbit_kv_append": (_I, [_I, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P]),
     "lowbit_kv_read": (_I, [_I, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P]),
+    "lowbit_kv_append_rotary": (_I, [_I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I, _F, _P, _P, _I64, _I64,
+                                     _P]),
     "lowbit_kv_attention_workspace": (_I64, [_I64] * 8),
     "lowbit_kv_attention": (_I, [_I, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _F, _I64,
                                  _P, _I64, _P, _I64, _P]),
@@ -379,6 +382,26 @@ def lowbit_kv_read(dtype, cache, pages, page_tokens, T, kv_heads, head_dim, slot
     nb = lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim) if T > 0 else 0
     args = (dtype, _flat(cache, "cache", nb, None), pages, page_tokens, T, kv_heads, head_dim, _flat(slots, "slots", T, _I64T), pk, sk, pv, sv)
     _call("lowbit_kv_read", lib.lowbit_kv_read, stream, (k, v, slots, cache), args)
+
+
+def lowbit_kv_append_rotary(dtype, q, q_out, k, v, T, q_heads, kv_heads, head_dim, positions, inv_freq, rotary_dim, style, slots, cache,
+                            pages, page_tokens, factor=1.0, q_stride=None, q_out_stride=None, k_stride=None, v_stride=None, stream=None):
+    """q, q_out: [T][q_heads][head_dim], k, v: [T][kv_heads][head_dim] tensors (any token stride), or addresses with
+    their strides; q_out may be q.  With q_heads 0, q and q_out are not looked at."""
+    pq = po = None
+    sq = so = 0
+    if q_heads != 0:
+        pq, sq = _row_arg(q, "q", dtype, T, q_heads, head_dim, q_stride)
+        po, so = _row_arg(q_out, "q_out", dtype, T, q_heads, head_dim, q_out_stride)
+    pk, sk = _row_arg(k, "k", dtype, T, kv_heads, head_dim, k_stride)
+    pv, sv = _row_arg(v, "v", dtype, T, kv_heads, head_dim, v_stride)
+    some = T > 0
+    nb = lib.lowbit_kv_cache_bytes(pages, kv_heads, page_tokens, head_dim) if some else 0
+    args = (dtype, pq, sq, po, so, pk, sk, pv, sv, T, q_heads, kv_heads, head_dim, _flat(positions, "positions", T, _I32),
+            _flat(inv_freq, "inv_freq", rotary_dim // 2 if some else 0, _F32T), rotary_dim, style, float(factor),
+            _flat(slots, "slots", T, _I64T), _flat(cache, "cache", nb, None), pages, page_tokens)
+    _call("lowbit_kv_append_rotary", lib.lowbit_kv_append_rotary, stream,
+          (q, q_out, k, v, positions, inv_freq, slots, cache) if q_heads != 0 else (k, v, positions, inv_freq, slots, cache), args)
 
 
 def lowbit_kv_attention_workspace(T, B, q_heads, kv_heads, head_dim, max_q, max_kv, window=0) -> int:

@@ -328,6 +328,24 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
                          const int64_t *slots, void *k, int64_t k_stride, void *v, int64_t v_stride, hipStream_t s);
 
 /*
+ * lowbit_kv_append of keys turned by their positions, and the step's queries turned alike, in one pass.  Row t stands at
+ * positions[t] (int32; lowbit_kv_plan writes them).  Of every head, the first rotary_dim elements (a multiple of 16, at
+ * least 16, at most head_dim) are rotary_dim / 2 pairs (x, y), and the rest stay as they are:
+ *   LB_ROTARY_HALVES  pair i: elements i and i + rotary_dim / 2;    LB_ROTARY_PAIRS  pair i: elements 2i and 2i + 1
+ *   a = positions[t] * inv_freq[i],  (x, y) -> factor * (x cos a - y sin a,  y cos a + x sin a)
+ * inv_freq: device fp32 [rotary_dim / 2]; whatever scaling of long contexts a model has is in them and in factor.
+ * Angles, sines and products are in 64 bits; a turned element is rounded to fp32 and then to dtype.  The cache's bytes are
+ * those of turning first and lowbit_kv_append.  q_out may be q, with the same stride, but not overlap it otherwise;
+ * q_heads may be 0 (q and q_out are not used then).  A row whose slot is negative or past the cache is left out: neither
+ * cache nor q_out change.  T * (q_heads + kv_heads) * head_dim below about 2^35, and at most 65535 heads in all.
+ */
+typedef enum { LB_ROTARY_HALVES = 0, LB_ROTARY_PAIRS = 1 } lb_rotary;
+lb_status lowbit_kv_append_rotary(int dtype, const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, int64_t T, int64_t q_heads, int64_t kv_heads,
+                                  int64_t head_dim, const int32_t *positions, const float *inv_freq, int64_t rotary_dim, int style,
+                                  float factor, const int64_t *slots, void *cache, int64_t pages, int64_t page_tokens, hipStream_t s);
+
+/*
  * Causal attention of a step's new tokens.  Request b's queries are rows cu_q[b] .. cu_q[b+1] - 1 of q and out
  * (at most max_q of them, T rows in all), the last tokens of its kv_lens[b] <= max_kv tokens (new ones included,
  * already appended), found through block_table[b].  Query i of n, at position pos = kv_lens[b] - n + i, sees the

@@ -1,0 +1,205 @@
+"""Queries and keys turned by their positions, keys and values into the 4-bit cache, against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_matvec_q1_amd.lowbit as L
+import serve_ref as R
+from gpu_util import dev, host, say
+
+A = 1 << 20
+TYPES = {"f32": (L.F32, torch.float32), "bf16": (L.BF16, torch.bfloat16), "f16": (L.F16, torch.float16)}
+
+
+def call(dtype=L.F32, q=A, qs=512, qo=A, qos=512, k=A, ks=128, v=A, vs=128, T=4, hq=8, hk=2, D=64, pos=A, freq=A, rd=64, style=0, slots=A,
+         cache=A, pages=4, P=16):
+    return L.lib.lowbit_kv_append_rotary(dtype, q, qs, qo, qos, k, ks, v, vs, T, hq, hk, D, pos, freq, rd, style, 1.0, slots, cache, pages, P, None)
+
+
+def test_refusals():
+    assert call(dtype=3) == L.LB_EINVAL and call(style=2) == L.LB_EINVAL and call(style=-1) == L.LB_EINVAL
+    for rd in (0, 8, 24, 80, -16):
+        assert call(rd=rd) == L.LB_ESHAPE
+    assert call(D=96) == L.LB_ESHAPE and call(P=24) == L.LB_ESHAPE and call(T=-1) == L.LB_ESHAPE and call(hk=0) == L.LB_ESHAPE
+    assert call(hq=-1) == L.LB_ESHAPE and call(hq=65535) == L.LB_ESHAPE and call(T=1 << 30) == L.LB_ESHAPE and call(pages=-1) == L.LB_ESHAPE
+    assert call(qs=511) == L.LB_ESHAPE and call(ks=127) == L.LB_ESHAPE and call(qos=508) == L.LB_ESHAPE
+    assert call(qs=516) == L.LB_ESHAPE  # in place with two strides
+    for name in ("q", "qo", "k", "v", "pos", "freq", "slots", "cache"):
+        assert call(**{name: None}) == L.LB_EINVAL, name
+    assert call(q=A + 8) == L.LB_EALIGN and call(v=A + 8) == L.LB_EALIGN and call(cache=A + 8) == L.LB_EALIGN and call(ks=130) == L.LB_EALIGN
+    assert call(slots=A + 4) == L.LB_EALIGN and call(pos=A + 2) == L.LB_EALIGN and call(freq=A + 1) == L.LB_EALIGN
+    assert call(T=0, q=None, k=None, v=None, slots=None) == L.LB_OK
+
+
+def test_binding_checks_extents():
+    t = dict(q=torch.zeros(4, 8, 64), qo=torch.zeros(4, 8, 64), k=torch.zeros(4, 2, 64), v=torch.zeros(4, 2, 64),
+             pos=torch.zeros(4, dtype=torch.int32), freq=torch.zeros(32), slots=torch.zeros(4, dtype=torch.int64),
+             cache=torch.zeros(L.lowbit_kv_cache_bytes(4, 2, 16, 64), dtype=torch.uint8))
+    bad = dict(q=t["q"][:3], qo=torch.zeros(4, 8, 64, dtype=torch.float16), k=torch.zeros(4, 3, 64), v=t["v"][:, :1], pos=t["pos"].long(),
+               freq=t["freq"][:31], slots=t["slots"][:3], cache=t["cache"][:-1])
+    for name, x in bad.items():
+        a = t | {name: x}
+        with pytest.raises(ValueError):
+            L.lowbit_kv_append_rotary(L.F32, a["q"], a["qo"], a["k"], a["v"], 4, 8, 2, 64, a["pos"], a["freq"], 64, 0, a["slots"], a["cache"], 4, 16)
+
+
+def turn(x, pos, freq, rd, pairs, factor):
+    """Rows [T][heads][D] in 64 bits."""
+    a = pos.astype(np.float64)[:, None] * freq.astype(np.float64)
+    c, s = np.cos(a)[:, None] * factor, np.sin(a)[:, None] * factor
+    y = x.astype(np.float64).copy()
+    p, q = (y[..., 0:rd:2].copy(), y[..., 1:rd:2].copy()) if pairs else (y[..., :rd // 2].copy(), y[..., rd // 2:rd].copy())
+    u, w = p * c - q * s, q * c + p * s
+    if pairs:
+        y[..., 0:rd:2], y[..., 1:rd:2] = u, w
+    else:
+        y[..., :rd // 2], y[..., rd // 2:rd] = u, w
+    return y
+
+
+def as64(t):
+    return t.double().cpu().numpy()
+
+
+def rounded(x, kind):
+    return as64(torch.from_numpy(x).float().to(TYPES[kind][1]))
+
+
+def near(got, want, x, kind, factor=1.0):
+    """Half a step of the type, half a step of fp32 before it (none where they are the same), and what 64 bits may differ by."""
+    fi = torch.finfo(TYPES[kind][1])
+    tol = np.abs(want) * (fi.eps / 2 + (0 if kind == "f32" else 2.0**-24)) * (1 + 2.0**-10) + fi.smallest_normal * fi.eps / 2
+    return (np.abs(got - want) <= tol + 1e-14 * abs(factor) * np.abs(x).max()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("D,P,hq,hk,T,rd,pairs,factor", [
+    (64, 16, 1, 1, 1, 64, False, 1.0), (64, 32, 6, 3, 35, 32, True, 1.0), (128, 16, 5, 5, 33, 128, False, 1.25), (128, 64, 8, 2, 18, 96, False, 1.0),
+    (128, 16, 4, 1, 7, 16, True, -0.5), (256, 16, 3, 1, 21, 256, True, 1.0), (256, 1024, 0, 2, 9, 48, False, 1.0), (64, 16, 40, 8, 3, 16, False, 1.0)])
+def test_rows_and_records(kind, D, P, hq, hk, T, rd, pairs, factor):
+    say(f"case rotary {kind} D={D} P={P} hq={hq} hk={hk} T={T} rd={rd} pairs={pairs}")
+    rng = np.random.default_rng(T + D + rd)
+    pages = -(-T // P) + 2
+    slots = rng.permutation(pages * P)[:T].astype(np.int64)
+    if T > 4:
+        slots[2], slots[4] = -1, pages * P  # left out
+    pos = rng.integers(0, 200000, T).astype(np.int32)
+    pos[0], pos[-1] = 2**31 - 1, 0
+    if T > 1:
+        pos[1] = -77
+    freq = (1e4 ** (-np.arange(rd // 2) * 2 / rd)).astype(np.float32)
+    wide = torch.from_numpy(rng.standard_normal((T, (hq + 2 * hk) * D + 16)) * np.exp(rng.uniform(-3, 3, (T, 1)))).to(TYPES[kind][1])
+    cut = [16, 16 + hq * D, 16 + (hq + hk) * D, 16 + (hq + 2 * hk) * D]
+    q, k, v = (as64(wide[:, a:z]).reshape(T, -1, D) for a, z in zip(cut, cut[1:]))
+    want = rng.integers(0, 256, (pages, hk, R.record_bytes(P, D)), dtype=np.uint8)
+    cache, before = dev(want), want.copy()
+    kt = rounded(turn(k, pos, freq, rd, pairs, factor), kind)
+    live = (slots >= 0) & (slots < pages * P)
+    for t in np.flatnonzero(live):
+        for h in range(hk):
+            R.store(want, P, D, int(slots[t]), h, kt[t, h], v[t, h])
+    w = wide.cuda()
+    out = torch.full((T + 1, hq, D), 7.0, dtype=TYPES[kind][1], device="cuda")
+    parts = [w[:, a:z] for a, z in zip(cut, cut[1:])]
+    args = (T, hq, hk, D, dev(pos), dev(freq), rd, L.ROTARY_PAIRS if pairs else L.ROTARY_HALVES, dev(slots), cache, pages, P)
+    L.lowbit_kv_append_rotary(TYPES[kind][0], parts[0] if hq else None, out if hq else None, parts[1], parts[2], *args, factor=factor)
+    got = host(cache)
+    assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
+    assert torch.equal(w.cpu(), wide)  # the inputs are as they were
+    o = as64(out)
+    assert (o[T] == 7).all() and (o[:T][~live] == 7).all()
+    if not hq:
+        return
+    qt = turn(q, pos, freq, rd, pairs, factor)
+    assert near(o[:T][live], qt[live], q, kind, factor)
+    assert np.array_equal(o[:T][live][..., rd:], q[live][..., rd:])
+    # in place: the same bits, and rows without a slot as they were
+    cache.copy_(dev(before))
+    L.lowbit_kv_append_rotary(TYPES[kind][0], parts[0], parts[0], parts[1], parts[2], *args, factor=factor)
+    here = as64(parts[0]).reshape(T, hq, D)
+    assert np.array_equal(here[live], o[:T][live]) and np.array_equal(here[~live], q[~live])
+    assert np.array_equal(host(cache), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,D,T,hq,hk", [("bf16", 256, 4100, 14, 2), ("f32", 64, 6500, 35, 7), ("f16", 128, 9001, 32, 8)])
+def test_a_long_prompt_equals_turning_and_appending(kind, D, T, hq, hk):
+    """Several heads a workgroup; the keys turned by themselves (as queries of a call) and appended give the same cache."""
+    say(f"case rotary prompt {kind} D={D} T={T}")
+    P, pages = 32, -(-T // 32)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dt = TYPES[kind]
+    q, k, v = (torch.randn(T, h, D, generator=g, device="cuda").to(dt[1]) for h in (hq, hk, hk))
+    slots = torch.randperm(pages * P, generator=g, device="cuda")[:T]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 100000
+    freq = torch.pow(5e5, -torch.arange(D // 2, device="cuda", dtype=torch.float64) * 2 / D).float()
+    a, b, c = (torch.zeros(L.lowbit_kv_cache_bytes(pages, hk, P, D), dtype=torch.uint8, device="cuda") for _ in range(3))
+    out, turned = torch.zeros_like(q), torch.zeros_like(k)
+    L.lowbit_kv_append_rotary(dt[0], q, out, k, v, T, hq, hk, D, pos, freq, D, L.ROTARY_HALVES, slots, a, pages, P)
+    L.lowbit_kv_append_rotary(dt[0], k, turned, k, v, T, hk, hk, D, pos, freq, D, L.ROTARY_HALVES, slots, c, pages, P)
+    L.lowbit_kv_append(dt[0], turned, v, T, hk, D, slots, b, pages, P)
+    assert torch.equal(a, b) and torch.equal(a, c)
+    ang = pos.double()[:, None] * freq.double()
+    cs, sn = ang.cos()[:, None], ang.sin()[:, None]
+    x = q.double()
+    want = torch.cat([x[..., :D // 2] * cs - x[..., D // 2:] * sn, x[..., D // 2:] * cs + x[..., :D // 2] * sn], -1)
+    assert near(as64(out), want.cpu().numpy(), as64(q), kind)
+
+
+@pytest.mark.gpu
+def test_values_that_are_not_finite_stay_in_their_rows():
+    D, P, T = 64, 16, 6
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((3, T, 1, D)).astype(np.float32)
+    x[0, 1, 0, 3], x[1, 2, 0, 40], x[2, 3, 0, 5], x[1, 4, 0, 63] = np.nan, np.inf, np.nan, -np.inf
+    cache = torch.zeros(L.lowbit_kv_cache_bytes(1, 1, P, D), dtype=torch.uint8, device="cuda")
+    q, k, v = (dev(a) for a in x)
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda"), torch.ones(16, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    L.lowbit_kv_append_rotary(L.F32, q, q, k, v, T, 1, 1, D, pos, freq, 32, L.ROTARY_HALVES, slots, cache, 1, P)
+    kk, vv = torch.zeros_like(k), torch.zeros_like(v)
+    L.lowbit_kv_read(L.F32, cache, 1, P, T, 1, D, slots, kk, vv)
+    bad = lambda t: [tuple(i) for i in np.argwhere(~np.isfinite(host(t)[:, 0]))]  # noqa: E731
+    assert bad(q) == [(1, 3), (1, 19)]
+    assert bad(kk) == [(2, i) for i in range(32, 64)] + [(4, i) for i in range(32, 64)]
+    assert bad(vv) == [(3, i) for i in range(32)]
+
+
+@pytest.mark.gpu
+def test_captured_and_on_another_stream():
+    """A captured step replayed with new rows, positions and slots, eager calls between, and a stream of its own."""
+    D, P, T, hq, hk, pages = 128, 16, 20, 4, 2, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, out = (torch.zeros(T, hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros(T, hk, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos, slots = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    freq = torch.pow(1e4, -torch.arange(64, device="cuda").double() / 64).float()
+    cache = torch.zeros(L.lowbit_kv_cache_bytes(pages, hk, P, D), dtype=torch.uint8, device="cuda")
+
+    def step(o, c, stream=None):
+        L.lowbit_kv_append_rotary(L.BF16, q, o, k, v, T, hq, hk, D, pos, freq, D, L.ROTARY_PAIRS, slots, c, pages, P, stream=stream)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out, cache)
+    side = torch.cuda.Stream()
+    for i in range(4):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        pos.copy_(torch.randint(0, 1 << 20, (T,), generator=g, device="cuda"))
+        n = T - 3 * i  # a padded step
+        slots.fill_(-1)
+        slots[:n] = torch.randperm(pages * P, generator=g, device="cuda")[:n]
+        out.fill_(3)
+        mine, mine_out = cache.clone(), torch.full_like(out, 3)
+        torch.cuda.synchronize()
+        graph.replay()
+        step(mine_out, mine, stream=side if i % 2 else None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, mine_out) and torch.equal(cache, mine)
+        assert (out[n:] == 3).all()
+    assert math.isfinite(float(out.float().sum()))
