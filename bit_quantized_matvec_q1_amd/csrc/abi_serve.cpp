@@ -13,6 +13,7 @@ bool is_page(int64_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 bool is_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int64_t kMax = INT32_MAX;
+constexpr int64_t kMaxExperts = 1024;
 constexpr const char *kTiles = "the step has 2^23 tiles, or parts of tiles, or more";
 
 // The cache's shape; LB_OK or the failure.
@@ -285,6 +286,135 @@ lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_
     a.block_table = block_table, a.table_stride = table_stride, a.cache = static_cast<const uint8_t *>(cache), a.pages = pages;
     a.page_tokens = page_tokens, a.scale = scale, a.workspace = workspace;
     return lb::abi_hip(fn, lb::launch_kv_attention(dtype, a, s));
+}
+
+lb_status lowbit_route(int dtype, const void *logits, int64_t stride, int64_t T, int64_t E, int score, const float *bias, int64_t groups,
+                       int64_t groups_kept, int64_t group_best, int64_t top_k, int renormalise, float factor, const int32_t *count,
+                       int32_t *experts, float *weights, hipStream_t s)
+{
+    const char *fn = "lowbit_route";
+    if (!is_dtype(dtype))
+        return lb::abi_fail(LB_EINVAL, fn, "unknown logit type");
+    if (score != LB_SCORE_SOFTMAX && score != LB_SCORE_SIGMOID)
+        return lb::abi_fail(LB_EINVAL, fn, "unknown score");
+    if (T < 0 || T >= (1 << 26) || E < 1 || E > kMaxExperts)
+        return lb::abi_fail(LB_ESHAPE, fn, "T must be from 0 to 2^26 - 1, E from 1 to 1024");
+    if (groups < 1 || groups > 64 || E % groups || groups_kept < 1 || groups_kept > groups || group_best < 1 || group_best > 2)
+        return lb::abi_fail(LB_ESHAPE, fn, "groups must be a divisor of E up to 64, groups_kept from 1 to groups, group_best 1 or 2");
+    if (top_k < 1 || top_k > 64 || top_k > E / groups * groups_kept)
+        return lb::abi_fail(LB_ESHAPE, fn, "top_k must be from 1 to 64, and at most the experts of the groups kept");
+    if (stride < E)
+        return lb::abi_fail(LB_ESHAPE, fn, "a row stride is shorter than the row");
+    if (T == 0)
+        return LB_OK;
+    if (!logits || !experts || !weights)
+        return lb::abi_fail(LB_EINVAL, fn, "null pointer");
+    if (!aligned(logits, lb::dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(count, 4) || !aligned(experts, 4) || !aligned(weights, 4))
+        return lb::abi_fail(LB_EALIGN, fn, "a pointer is not aligned to its elements");
+    lb_status st = lb::abi_check_device(fn);
+    if (st != LB_OK)
+        return st;
+    lb::RouteArgs a = {};
+    a.logits = logits, a.stride = stride, a.T = T, a.E = E, a.groups = groups, a.kept = groups_kept, a.best = group_best, a.top_k = top_k;
+    a.sigmoid = score == LB_SCORE_SIGMOID, a.renormalise = renormalise != 0, a.bias = bias, a.factor = factor, a.count = count;
+    a.experts = experts, a.weights = weights;
+    return lb::abi_hip(fn, lb::launch_route(dtype, a, s));
+}
+
+int64_t lowbit_experts_weight_bytes(int fmt, int64_t E, int64_t N, int64_t K)
+{
+    const int64_t one = lowbit_weight_bytes(fmt, N, K);
+    if (one < 0 || one >= (int64_t)1 << 32 || E < 0 || E > kMaxExperts)
+        return -1;
+    return E * ((one + 15) / 16 * 16);
+}
+
+int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E)
+{
+    if (pairs < 0 || pairs > kMax - 4 || E < 1 || E > kMaxExperts)
+        return -1;
+    return 4 * (lb::experts_tiles_at(pairs) + 4 * lb::experts_max_tiles(pairs, E));
+}
+
+lb_status lowbit_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, void *plan, hipStream_t s)
+{
+    const char *fn = "lowbit_experts_plan";
+    if (pairs < 0 || pairs > kMax - 4 || E < 1 || E > kMaxExperts)
+        return lb::abi_fail(LB_ESHAPE, fn, "pairs must be from 0 to 2^31 - 5, E from 1 to 1024");
+    if (pairs == 0)
+        return LB_OK;
+    if (!experts || !plan)
+        return lb::abi_fail(LB_EINVAL, fn, "null pointer");
+    if (!aligned(experts, 4) || !aligned(plan, 16))
+        return lb::abi_fail(LB_EALIGN, fn, "the plan needs 16-byte alignment, experts 4-byte alignment");
+    lb_status st = lb::abi_check_device(fn);
+    if (st != LB_OK)
+        return st;
+    return lb::abi_hip(fn, lb::launch_experts_plan(experts, pairs, E, static_cast<int32_t *>(plan), s));
+}
+
+lb_status lowbit_experts_matmul(int fmt, const void *W, int64_t E, int64_t N, int64_t K, const int8_t *xq, const void *xscale,
+                                const int32_t *experts, int64_t pairs, int64_t pairs_per_row, const void *plan, float *y, hipStream_t s)
+{
+    const char *fn = "lowbit_experts_matmul";
+    if (fmt < LB_Q1_0 || fmt > LB_Q4_0)
+        return lb::abi_fail(LB_EINVAL, fn, "unknown weight format");
+    if (fmt != LB_Q1_0 && fmt != LB_Q2_0_G64 && fmt != LB_Q4_0)
+        return lb::abi_fail(LB_EUNSUPPORTED, fn, "experts are Q1_0, Q2_0_g64 or Q4_0");
+    if (N < 0 || K < 1 || pairs < 0 || pairs_per_row < 1 || E < 1 || E > kMaxExperts || N > kMax || pairs > kMax - 4 || pairs_per_row > kMax)
+        return lb::abi_fail(LB_ESHAPE, fn, "a size below its least (K, E and pairs_per_row: 1), E over 1024, or another over 2^31 - 1");
+    if (K % (fmt == LB_Q2_0_G64 ? 64 : 128) || K > (fmt == LB_Q4_0 ? 16384 : 32768))
+        return lb::abi_fail(LB_ESHAPE, fn, "K must be a multiple of 128 (64 for Q2_0_g64), at most 32768 (16384 for Q4_0)");
+    if (lowbit_weight_bytes(fmt, N, K) >= (int64_t)1 << 32)
+        return lb::abi_fail(LB_ESHAPE, fn, "an expert's tensor of 4 GiB or more");
+    if (((pairs + pairs_per_row - 1) / pairs_per_row) * K >= (int64_t)1 << 32)
+        return lb::abi_fail(LB_ESHAPE, fn, "activations of 4 GiB or more");
+    if (N == 0 || pairs == 0)
+        return LB_OK;
+    if (!W || !xq || !xscale || !y || (!plan && !experts))
+        return lb::abi_fail(LB_EINVAL, fn, "null pointer");
+    if (!aligned(W, 16) || !aligned(xq, 16) || !aligned(plan, 16) || !aligned(xscale, 4) || !aligned(experts, 4) || !aligned(y, 4))
+        return lb::abi_fail(LB_EALIGN, fn, "W, xq and the plan need 16-byte alignment, everything else 4-byte alignment");
+    lb::ExpertsArgs a = {};
+    a.W = static_cast<const uint8_t *>(W), a.expert_bytes = lowbit_experts_weight_bytes(fmt, 1, N, K);
+    a.E = (int32_t)E, a.N = (int32_t)N, a.K = (int32_t)K, a.pairs = (int32_t)pairs, a.per_row = (int32_t)pairs_per_row;
+    a.xq = xq, a.xs = static_cast<const uint16_t *>(xscale), a.experts = experts, a.plan = static_cast<const int32_t *>(plan);
+    a.max_tiles = plan ? lb::experts_max_tiles(pairs, E) : pairs, a.y = y;
+    const bool gemm = plan && lb::experts_tile_rows(pairs, E) > 4;
+    // a launch's threads are numbered in 32 bits
+    const int64_t blocks = gemm ? a.max_tiles * ((N + 63) / 64) : lb::experts_rows_blocks(fmt, a);
+    if (blocks >= (int64_t)1 << (gemm ? 23 : 24))
+        return lb::abi_fail(LB_ESHAPE, fn, "over 2^32 threads");
+    lb_status st = lb::abi_check_device(fn);
+    if (st != LB_OK)
+        return st;
+    return lb::abi_hip(fn, gemm ? lb::launch_experts_gemm(fmt, a, s) : lb::launch_experts_rows(fmt, a, s));
+}
+
+lb_status lowbit_experts_combine(int dtype, const float *y, const int32_t *experts, const float *weights, int64_t T, int64_t top_k, int64_t E,
+                                 int64_t N, void *out, int64_t out_stride, hipStream_t s)
+{
+    const char *fn = "lowbit_experts_combine";
+    if (!is_dtype(dtype))
+        return lb::abi_fail(LB_EINVAL, fn, "unknown row type");
+    if (T < 0 || T > kMax || top_k < 1 || top_k > 1024 || E < 1 || E > kMaxExperts || N < 0 || N > kMax)
+        return lb::abi_fail(LB_ESHAPE, fn, "negative size, top_k or E not from 1 to 1024, or another size over 2^31 - 1");
+    if (T * ((N + 255) / 256) >= (1 << 24))
+        return lb::abi_fail(LB_ESHAPE, fn, "2^32 outputs or more");
+    if (out_stride < N)
+        return lb::abi_fail(LB_ESHAPE, fn, "a row stride is shorter than the row");
+    if (T == 0 || N == 0)
+        return LB_OK;
+    if (!y || !experts || !weights || !out)
+        return lb::abi_fail(LB_EINVAL, fn, "null pointer");
+    if (!aligned(y, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(out, lb::dtype_bytes(dtype)))
+        return lb::abi_fail(LB_EALIGN, fn, "a pointer is not aligned to its elements");
+    lb_status st = lb::abi_check_device(fn);
+    if (st != LB_OK)
+        return st;
+    lb::CombineArgs a = {};
+    a.y = y, a.experts = experts, a.weights = weights, a.T = T, a.top_k = top_k, a.E = E, a.N = N, a.out = out, a.out_stride = out_stride;
+    return lb::abi_hip(fn, lb::launch_experts_combine(dtype, a, s));
 }
 
 lb_status lowbit_logits_process(int dtype, const void *logits, int64_t in_stride, int64_t B, int64_t V, const int32_t *tokens,

@@ -25,9 +25,11 @@
 //    block's activation scale and -d_x * 1.5 * 2^23 gives round(d_x * isum) without a conversion.  The
 //    weight block scale is then applied with one more FMA (bankml technical report, section III.3: one
 //    multiply-add per q8_0 block, then one per weight block).
+//  * The experts' products (GROUPED) are the same tiles with other rows: a tile is up to TM pairs of one expert, from the
+//    plan of experts.hip, whose activation rows are gathered and whose output rows are scattered by the pairs' numbers.
 //  * Planar weights have no block scales: the MFMA accumulates int32 over the whole row and the two
 //    per-row / per-tensor scales are applied once at the end.
-#include "lowbit_internal.h"
+#include "serve_internal.h"
 
 #include <atomic>
 
@@ -125,8 +127,16 @@ template <int FMT> __device__ __forceinline__ uint32_t step_sbytes(int kk)
     return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 2u : scale32(FMT) ? (uint32_t)(kk / 32) * 2u : (uint32_t)(kk / 64) * 2u;
 }
 
-template <int FMT>
-__device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, int m0, int tid)
+// `pairs`, GROUPED: the tile's pairs (M of them), of which `per_row` share an activation row; `n_pairs` bounds them.
+struct Gather {
+    const int32_t *pairs;
+    uint32_t per_row, n_pairs;
+    __device__ __forceinline__ uint32_t pair(int r) const { return min((uint32_t)pairs[r], n_pairs - 1u); }
+    __device__ __forceinline__ uint32_t row(int r) const { return pair(r) / per_row; }
+};
+
+template <int FMT, bool GROUPED>
+__device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, int m0, int tid, const Gather &g)
 {
     LaneOffs o;
     const int row = min(n0 + (tid >> 3), N - 1), p = tid & 7;
@@ -150,9 +160,10 @@ __device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, in
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         const int slot = 128 * wave + 64 * u + lane, r = slot / XCH;
-        o.x[u] = (uint32_t)min(m0 + r, M - 1) * (uint32_t)K + 16u * (uint32_t)((slot % XCH) ^ ((r >> 1) & 7));
+        const uint32_t xr = GROUPED ? g.row(min(r, M - 1)) : (uint32_t)min(m0 + r, M - 1);
+        o.x[u] = xr * (uint32_t)K + 16u * (uint32_t)((slot % XCH) ^ ((r >> 1) & 7));
     }
-    o.dx = (uint32_t)min(m0 + (tid & (TM - 1)), M - 1) * (uint32_t)(K / QK8) * 2u;
+    o.dx = (GROUPED ? g.row(min(tid & (TM - 1), M - 1)) : (uint32_t)min(m0 + (tid & (TM - 1)), M - 1)) * (uint32_t)(K / QK8) * 2u;
     return o;
 }
 
@@ -161,7 +172,7 @@ __device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, in
 // blocks (only one step of the walk) takes a branch whose lanes of the missing second block re-read the
 // first.  Every thread loads the activation scales of activation row tid mod TM (the first TM threads
 // store them).
-template <int FMT>
+template <int FMT, bool GROUPED>
 __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const uint8_t *__restrict__ W,
                                           const uint8_t *__restrict__ wsc, const uint8_t *__restrict__ xsc, int kk,
                                           bool half_step, int tid, int m0, int M, int K)
@@ -175,9 +186,9 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
     if (FMT != LB_TERNARY_PLANAR && tid < TM) {
         // Q1_0 and Q2_0 rebuild the row offset at every step (an opaque copy of tid stops the compiler from
         // keeping it live across the loop, where it costs a register that their two result tiles need);
-        // Q8_0 keeps it
+        // Q8_0 keeps it, and so do gathered rows
         uint32_t odx = o.dx;
-        if (FMT != LB_Q8_0) {
+        if (FMT != LB_Q8_0 && !GROUPED) {
             int t = tid;
             asm volatile("; activation-scale row %0" : "+v"(t));
             odx = (uint32_t)min(m0 + t, M - 1) * (uint32_t)(K / QK8) * 2u;
@@ -402,12 +413,18 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
 // KSPLIT = 2 (grids of fewer than two workgroups per CU): a workgroup of 16 waves, whose two 8-wave halves
 // walk alternate K-steps of the same output tile with their own LDS buffers and add their partial sums
 // at the end, so a CU holds 16 waves where the tile count alone would give it 8.
-template <int FMT, bool EMIT, int KSPLIT>
+struct GroupArgs { // GROUPED: the experts' tensors and the plan (ExpertsArgs)
+    int64_t expert_bytes, tiles_at;
+    const int32_t *plan;
+    int32_t E, pairs, per_row;
+};
+
+template <int FMT, bool EMIT, int KSPLIT, bool GROUPED = false>
 __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kernel(const uint8_t *__restrict__ W, int N, int K,
                                                                        float w_scale, const int8_t *__restrict__ X,
                                                                        const void *__restrict__ Xscale, int M,
                                                                        float *__restrict__ Y, int32_t *__restrict__ sums,
-                                                                       int ntn)
+                                                                       int ntn, GroupArgs ga)
 {
     __shared__ Lds lds[KSPLIT];
     __shared__ uint32_t xt0[KSPLIT][XTILE], xt1[KSPLIT][XTILE];
@@ -421,7 +438,18 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     // this wave's 32 x 32 output tile inside the 64 x 128 workgroup tile
     const int wn = wave & 1, wm = wave >> 1;
     const int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
-    const int n0 = bn * TN, m0 = bm * TM;
+    const int n0 = bn * TN, m0 = GROUPED ? 0 : bm * TM;
+    Gather g = {};
+    if constexpr (GROUPED) {
+        if (bm >= ga.plan[0])
+            return;
+        const int4 t = reinterpret_cast<const int4 *>(ga.plan + ga.tiles_at)[bm];
+        if ((unsigned)t.x >= (unsigned)ga.E || t.y < 0 || t.z < 1 || t.z > TM || t.y > ga.pairs - t.z)
+            return; // no plan of these pairs
+        W += t.x * ga.expert_bytes;
+        M = t.z;
+        g = {ga.plan + experts_order_at() + t.y, (uint32_t)ga.per_row, (uint32_t)ga.pairs};
+    }
     const int64_t rowcode = FMT == LB_Q1_0 ? K / 8 : FMT == LB_Q8_0 ? K : FMT == LB_Q4_0 ? K / 2 : K / 4; // code bytes per weight row
     const int nab = K / QK8;                                                  // activation blocks per row
     const uint8_t *wsc = W + (int64_t)N * rowcode;
@@ -457,7 +485,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     const int kend = nsteps * KS;                   // the walk's K offsets are taken modulo this
     const int kfirst = ((bn % nsteps + half) % nsteps) * KS;
 
-    const LaneOffs lo = lane_offsets<FMT>(N, K, M, n0, m0, tid);
+    const LaneOffs lo = lane_offsets<FMT, GROUPED>(N, K, M, n0, m0, tid, g);
     uint32_t xb[4]; // dword offsets in a tile of chunk 2 j + h of activation row 32 wm + l32
 #pragma unroll
     for (int j = 0; j < 4; j++)
@@ -469,7 +497,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     // LDS tiles of every step are fixed objects.
     StepRegs ring;
     int kk = kfirst;
-    load_step<FMT>(ring, lo, W, wsc, xsc, kk, K - kk < KS, tid, m0, M, K);
+    load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kk, K - kk < KS, tid, m0, M, K);
     issue_x(xt0[half], X, lo, kk, K - kk < KS, wave, lane);
 
     for (int j0 = 0; j0 < nsh; j0 += 2)
@@ -489,7 +517,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         int kn = kk + KSPLIT * KS;
         kn = kn >= kend ? kn - kend : kn;
         kn = kn >= kend ? kn - kend : kn;
-        load_step<FMT>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
+        load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
         issue_x(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
         if (active)
             step_compute<FMT, EMIT, 4>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
@@ -559,7 +587,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         const int r = 2 * k + (lane >> 5), mm = m0 + 32 * wm + r;
         const float v = __uint_as_float(t[32 * r + (nc ^ r)]);
         if (mm < M && n < N)
-            Y[(int64_t)mm * N + n] = v;
+            Y[(GROUPED ? (int64_t)g.pair(mm) : (int64_t)mm) * N + n] = v;
     }
 }
 
@@ -592,15 +620,31 @@ hipError_t launch_fmt(const uint8_t *W, int64_t N, int64_t K, float w_scale, con
     if constexpr (!EMIT) {
         if (ntn * ntm < 2 * (int64_t)device_cus()) {
             hipLaunchKernelGGL((gemm_kernel<FMT, EMIT, 2>), grid, dim3(2 * GT), 0, s, W, (int)N, (int)K, w_scale, Xq,
-                               Xscale, (int)M, Y, sums, (int)ntn);
+                               Xscale, (int)M, Y, sums, (int)ntn, GroupArgs{});
             return hipGetLastError();
         }
     }
     hipLaunchKernelGGL((gemm_kernel<FMT, EMIT, 1>), grid, dim3(GT), 0, s, W, (int)N, (int)K, w_scale, Xq, Xscale,
-                       (int)M, Y, sums, (int)ntn);
+                       (int)M, Y, sums, (int)ntn, GroupArgs{});
+    return hipGetLastError();
+}
+
+template <int FMT> hipError_t launch_experts_fmt(const ExpertsArgs &a, hipStream_t s)
+{
+    const int64_t ntn = (a.N + TN - 1) / TN;
+    const GroupArgs ga = {a.expert_bytes, experts_tiles_at(a.pairs), a.plan, a.E, a.pairs, a.per_row};
+    hipLaunchKernelGGL((gemm_kernel<FMT, false, 1, true>), dim3((unsigned)(ntn * a.max_tiles)), dim3(GT), 0, s, a.W, a.N, a.K, 1.0f, a.xq, a.xs,
+                       0, a.y, nullptr, (int)ntn, ga);
     return hipGetLastError();
 }
 } // namespace
+
+hipError_t launch_experts_gemm(int fmt, const ExpertsArgs &a, hipStream_t s)
+{
+    return fmt == LB_Q1_0       ? launch_experts_fmt<LB_Q1_0>(a, s)
+           : fmt == LB_Q2_0_G64 ? launch_experts_fmt<LB_Q2_0_G64>(a, s)
+                                : launch_experts_fmt<LB_Q4_0>(a, s);
+}
 
 hipError_t launch_gemm(int fmt, const uint8_t *W, int64_t N, int64_t K, float w_scale, const int8_t *Xq,
                        const void *Xscale, int64_t M, float *Y, int32_t *sums, hipStream_t s)

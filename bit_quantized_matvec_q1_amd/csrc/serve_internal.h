@@ -110,6 +110,50 @@ int64_t kv_attention_workspace(const AttnArgs &a);
 bool kv_attention_fits(int dtype, const AttnArgs &a);
 hipError_t launch_kv_attention(int dtype, const AttnArgs &a, hipStream_t s);
 
+struct RouteArgs {
+    const void *logits;
+    int64_t stride, T, E, groups, kept, best, top_k;
+    bool sigmoid, renormalise;
+    const float *bias;
+    float factor;
+    const int32_t *count;
+    int32_t *experts;
+    float *weights;
+};
+hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
+
+// The routed pairs by expert (include/lowbit.h, lowbit_experts_plan): int32 words
+//   [0] tiles, [1] routed pairs, [2], [3] unused; order [pairs, rounded up to 4]; tiles {expert, first place in order, rows, 0}
+// A tile is at most experts_tile_rows() pairs of one expert.
+inline __host__ __device__ int64_t experts_order_at() { return 4; }
+inline __host__ __device__ int64_t experts_tiles_at(int64_t pairs) { return 4 + (pairs + 3) / 4 * 4; }
+int64_t experts_tile_rows(int64_t pairs, int64_t E);
+int64_t experts_max_tiles(int64_t pairs, int64_t E);
+
+struct ExpertsArgs {
+    const uint8_t *W;
+    int64_t expert_bytes; // from one expert's tensor to the next
+    int32_t E, N, K, pairs, per_row;
+    const int8_t *xq;
+    const uint16_t *xs;
+    const int32_t *experts, *plan; // plan null: a tile a pair
+    int64_t max_tiles;
+    float *y;
+};
+hipError_t launch_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, int32_t *plan, hipStream_t s);
+// 0: no kernel for these sizes
+int64_t experts_rows_blocks(int fmt, const ExpertsArgs &a);
+hipError_t launch_experts_rows(int fmt, const ExpertsArgs &a, hipStream_t s);
+hipError_t launch_experts_gemm(int fmt, const ExpertsArgs &a, hipStream_t s);
+struct CombineArgs {
+    const float *y;
+    const int32_t *experts;
+    const float *weights;
+    int64_t T, top_k, E, N, out_stride;
+    void *out;
+};
+hipError_t launch_experts_combine(int dtype, const CombineArgs &a, hipStream_t s);
+
 struct LogitsArgs {
     const void *logits;
     void *out;

@@ -16,6 +16,7 @@ Q1_0, Q2_0_G64, TERNARY_PLANAR, Q8_0, TERNARY_B3, Q4_0 = 1, 2, 3, 4, 5, 6
 ACT_Q8_0, ACT_I8_ROW, ACT_F32_Q8_0 = 1, 2, 3
 F32, BF16, F16 = 0, 1, 2
 ROTARY_HALVES, ROTARY_PAIRS = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 LB_OK, LB_EINVAL, LB_ESHAPE, LB_EALIGN, LB_EUNSUPPORTED, LB_EDEVICE, LB_ENOMEM = range(7)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblowbit.so")
@@ -56,6 +57,12 @@ SIGNATURES = {
     "lowbit_kv_attention_workspace": (_I64, [_I64] * 8),
     "lowbit_kv_attention": (_I, [_I, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _F, _I64,
                                  _P, _I64, _P, _I64, _P]),
+    "lowbit_route": (_I, [_I, _P, _I64, _I64, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, _F, _P, _P, _P, _P]),
+    "lowbit_experts_weight_bytes": (_I64, [_I, _I64, _I64, _I64]),
+    "lowbit_experts_plan_bytes": (_I64, [_I64, _I64]),
+    "lowbit_experts_plan": (_I, [_P, _I64, _I64, _P, _P]),
+    "lowbit_experts_matmul": (_I, [_I, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P]),
+    "lowbit_experts_combine": (_I, [_I, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _P]),
     "lowbit_logits_process": (_I, [_I, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P]),
     "lowbit_read_probe": (_I, [_P, _I64, _P, _P]),
 }
@@ -494,6 +501,53 @@ def lowbit_logits_process(dtype, logits, B, V, out, tokens=None, prompt_lens=Non
             pbt, pbv, sbt, _flat(bias_lens, "bias_lens", b, _I32), pm, sm, po, so)
     _call("lowbit_logits_process", lib.lowbit_logits_process, stream, (logits, out, tokens, prompt_lens, total_lens, repetition, presence,
                                                                        frequency, bias_tokens, bias_values, bias_lens, mask), args)
+
+
+def lowbit_route(dtype, logits, T, E, top_k, experts, weights, score=SCORE_SOFTMAX, bias=None, groups=1, groups_kept=1, group_best=1,
+                 renormalise=True, factor=1.0, count=None, stream=None):
+    """logits [T][>= E] (any row stride); experts int32 and weights fp32 [T][top_k]; bias fp32 [E]; count int32 [1]."""
+    t, e = max(T, 0), max(E, 0)
+    pl, sl = _matrix(logits, "logits", t, e, _DTYPES.get(dtype, _F32T))
+    n = t * max(top_k, 0)
+    some = 1 if t else 0
+    args = (dtype, pl, sl, T, E, score, _flat(bias, "bias", e * some, _F32T), groups, groups_kept, group_best, top_k, 1 if renormalise else 0,
+            float(factor), _flat(count, "count", some, _I32), _flat(experts, "experts", n, _I32), _flat(weights, "weights", n, _F32T))
+    _call("lowbit_route", lib.lowbit_route, stream, (logits, bias, count, experts, weights), args)
+
+
+def lowbit_experts_weight_bytes(fmt: int, E: int, N: int, K: int) -> int:
+    return lib.lowbit_experts_weight_bytes(fmt, E, N, K)
+
+
+def lowbit_experts_plan_bytes(pairs: int, E: int) -> int:
+    return lib.lowbit_experts_plan_bytes(pairs, E)
+
+
+def lowbit_experts_plan(experts, pairs, E, plan, stream=None):
+    n = max(pairs, 0)
+    args = (_flat(experts, "experts", n, _I32), pairs, E, _flat(plan, "plan", lib.lowbit_experts_plan_bytes(pairs, E) if n else 0, None))
+    _call("lowbit_experts_plan", lib.lowbit_experts_plan, stream, (experts, plan), args)
+
+
+def lowbit_experts_matmul(fmt, W, E, N, K, xq, xscale, experts, pairs, pairs_per_row, y, plan=None, stream=None):
+    """W: lowbit_experts_weight_bytes(fmt, E, N, K) bytes; xq int8, xscale binary16 (their bits too), y fp32, dense.
+    plan: lowbit_experts_plan's of these pairs; without one, every pair by itself."""
+    n = pairs if N > 0 and pairs > 0 else 0
+    rows = -(-n // pairs_per_row) if pairs_per_row > 0 else 0
+    if isinstance(xscale, _Tensor) and xscale.dtype not in _F16_BITS:
+        raise ValueError(f"xscale: dtype {xscale.dtype} not accepted (expected one of {[str(d) for d in _F16_BITS]})")
+    args = (fmt, _flat(W, "W", lib.lowbit_experts_weight_bytes(fmt, E, N, K) if n else 0, None), E, N, K, _flat(xq, "xq", rows * K, torch.int8),
+            _flat(xscale, "xscale", rows * (K // 32) * 2, None), _flat(experts, "experts", n, _I32), pairs,
+            pairs_per_row, _flat(plan, "plan", lib.lowbit_experts_plan_bytes(pairs, E) if n else 0, None), _flat(y, "y", n * N, _F32T))
+    _call("lowbit_experts_matmul", lib.lowbit_experts_matmul, stream, (W, xq, xscale, experts, plan, y), args)
+
+
+def lowbit_experts_combine(dtype, y, experts, weights, T, top_k, E, N, out, out_stride=None, stream=None):
+    """out: [T][N] tensor (any row stride), or an address with out_stride."""
+    po, so = _row_arg(out, "out", dtype, T, 1, N, out_stride)
+    n = T * top_k if T > 0 and N > 0 and top_k > 0 else 0
+    args = (dtype, _flat(y, "y", n * N, _F32T), _flat(experts, "experts", n, _I32), _flat(weights, "weights", n, _F32T), T, top_k, E, N, po, so)
+    _call("lowbit_experts_combine", lib.lowbit_experts_combine, stream, (y, experts, weights, out), args)
 
 
 class Batch:

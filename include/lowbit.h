@@ -382,6 +382,57 @@ lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_
                               int64_t workspace_bytes, hipStream_t s);
 
 /*
+ * Routing of T tokens to E experts (1 to 1024).  logits [T][E] of type dtype, row stride `stride` elements.  Per token:
+ *   scores   p = softmax over the E logits (LB_SCORE_SOFTMAX), or 1 / (1 + exp(-logit)) (LB_SCORE_SIGMOID)
+ *   order    experts by p + bias[e] (bias: device fp32 [E], NULL for none), the largest first, equal ones by index
+ *   groups   of E / groups experts each (1 to 64 of them): only the groups_kept groups with the largest sums of their
+ *            group_best (1 or 2) largest values p + bias are looked at; equal ones by index
+ *   chosen   the first top_k (1 to 64): experts[t][j], in order; their weights are p, without the bias, over the sum of the
+ *            top_k where renormalise is not 0 (0 where that is 0), times factor: weights[t][j]
+ * Scores, sums and comparisons are in 64 bits, weights rounded to fp32 once.  A NaN logit counts as -inf, and a softmax of
+ * logits of -inf alone is that of equal ones; of infinite ones, those share it; a p + bias that is NaN or -inf comes last.
+ * count: device int32, NULL for T; tokens from count[0] on (a padded step's; the last of lowbit_kv_plan's cu_q is that
+ * number) get experts -1 and weights 0.  T below 2^26.
+ */
+typedef enum { LB_SCORE_SOFTMAX = 0, LB_SCORE_SIGMOID = 1 } lb_score;
+lb_status lowbit_route(int dtype, const void *logits, int64_t stride, int64_t T, int64_t E, int score, const float *bias, int64_t groups,
+                       int64_t groups_kept, int64_t group_best, int64_t top_k, int renormalise, float factor, const int32_t *count,
+                       int32_t *experts, float *weights, hipStream_t s);
+
+/*
+ * The products of the routed pairs.  The experts' N x K tensors lie one after another, each lowbit_pack_weights' layout
+ * padded to a multiple of 16 bytes: lowbit_experts_weight_bytes(fmt, 1, N, K) from one to the next (-1 for a bad shape, or
+ * a tensor of 4 GiB or more).
+ *
+ * lowbit_experts_plan sorts `pairs` pairs by expert (experts: device int32 [pairs]; a number outside 0 .. E-1 is a pair
+ * that is left out, as a padded token's -1) into `plan` (device, lowbit_experts_plan_bytes(pairs, E) bytes, 16-byte
+ * aligned), for any number of products of the same pairs and E.  The order does not depend on how anything runs.
+ */
+int64_t lowbit_experts_weight_bytes(int fmt, int64_t E, int64_t N, int64_t K);
+int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E);
+lb_status lowbit_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, void *plan, hipStream_t s);
+
+/*
+ * y[p] = W[experts[p]] . dequant(x[p / pairs_per_row]) for every pair p that is not left out (y's other rows are not
+ * written): pairs_per_row is top_k where a token's pairs share its activations (an expert's first products), 1 where each
+ * pair has its own (its last).  fmt LB_Q1_0, LB_Q2_0_G64 or LB_Q4_0 (others LB_EUNSUPPORTED); xq int8
+ * [ceil(pairs / pairs_per_row)][K] and xscale binary16 [..][K/32] are q8_0 rows (lowbit_quantize_act); y fp32 [pairs][N].
+ * With a plan, weights are read once for the rows of a tile, and `experts` is not read; without (NULL), each pair is
+ * computed by itself, which is best for a single token.  Integer block sums are exact and scaled as lowbit_matvec does.
+ * Limits: K a multiple of 128 (64 for LB_Q2_0_G64), at most 32768 (16384 for LB_Q4_0); xq below 4 GiB.
+ */
+lb_status lowbit_experts_matmul(int fmt, const void *W, int64_t E, int64_t N, int64_t K, const int8_t *xq, const void *xscale,
+                                const int32_t *experts, int64_t pairs, int64_t pairs_per_row, const void *plan, float *y, hipStream_t s);
+
+/*
+ * out[t] = sum over j of weights[t][j] * y[t * top_k + j], for the pairs with an expert in 0 .. E-1 (the others' rows are not
+ * read; a token without any gives zeros).  y fp32 [T * top_k][N], out [T][N] of type dtype with a stride in elements.
+ * Summed in fp32 in the order of j, rounded once.  T * N below about 2^32.
+ */
+lb_status lowbit_experts_combine(int dtype, const float *y, const int32_t *experts, const float *weights, int64_t T, int64_t top_k, int64_t E,
+                                 int64_t N, void *out, int64_t out_stride, hipStream_t s);
+
+/*
  * Logits before sampling: logits [B][V] of type `dtype`, row stride in_stride elements; out alike (it may be
  * logits itself, with the same stride, but not overlap it otherwise).  In fp32, for every token t of row b, in
  * this order, rounded to dtype once at the end:

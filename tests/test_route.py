@@ -1,0 +1,193 @@
+"""Routing of tokens to experts, against its definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_matvec_q1_amd.lowbit as L
+from gpu_util import dev, host, say
+
+A = 1 << 20
+TYPES = {"f32": (L.F32, torch.float32), "bf16": (L.BF16, torch.bfloat16), "f16": (L.F16, torch.float16)}
+
+
+def reference(x, k, sigmoid=False, bias=None, groups=1, kept=1, best=1, renorm=True, factor=1.0):
+    """experts [T][k] and weights [T][k] (64 bits) of logits x [T][E] (64 bits)."""
+    with np.errstate(all="ignore"):
+        x = np.where(np.isnan(x), -np.inf, x)
+        if sigmoid:
+            p = 1 / (1 + np.exp(-x))
+        else:
+            top = x.max(1, keepdims=True)
+            p = np.where(x == top, 1.0, np.exp(x - top))
+            p /= p.sum(1, keepdims=True)
+        least = -np.finfo(np.float64).max
+        floor = lambda v: np.where(v >= least, v, least)  # noqa: E731
+        sel = floor(p if bias is None else p + bias.astype(np.float64))
+        T, E = x.shape
+        if groups > 1:
+            per = -np.sort(-sel.reshape(T, groups, -1), axis=-1)
+            score = floor(per[..., 0] + per[..., 1] if best == 2 and per.shape[-1] > 1 else per[..., 0])
+            keep = np.argsort(-score, axis=1, kind="stable")[:, :kept]
+            ok = np.zeros((T, groups), bool)
+            np.put_along_axis(ok, keep, True, 1)
+            sel = np.where(np.repeat(ok, E // groups, 1), sel, -np.inf)
+        at = np.argsort(-sel, axis=1, kind="stable")[:, :k]
+        w = np.take_along_axis(p, at, 1)
+        if renorm:
+            z = w.sum(1, keepdims=True)
+            w = np.where(z > 0, w / np.where(z > 0, z, 1), 0)
+        return at, w * factor
+
+
+def run(logits, kind, k, T=None, E=None, **a):
+    T, E = logits.shape[0] if T is None else T, logits.shape[1] if E is None else E
+    experts = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
+    weights = torch.full((T + 1, k), -7.0, device="cuda")
+    L.lowbit_route(TYPES[kind][0], logits, T, E, k, experts, weights, **a)
+    e, w = host(experts), host(weights)
+    assert (e[T] == -7).all() and (w[T] == -7).all()
+    return e[:T], w[:T]
+
+
+def check(x, kind, k, sigmoid=False, bias=None, groups=1, kept=1, best=1, renorm=True, factor=1.0):
+    e, w = run(x.cuda(), kind, k, score=L.SCORE_SIGMOID if sigmoid else L.SCORE_SOFTMAX, bias=None if bias is None else dev(bias), groups=groups,
+               groups_kept=kept, group_best=best, renormalise=renorm, factor=factor)
+    we, ww = reference(x.double().numpy(), k, sigmoid, bias, groups, kept, best, renorm, factor)
+    assert np.array_equal(e, we)
+    # rounded to fp32 once (half a step, 2^-24; below the normal range half a step of that), from 64 bits
+    assert (np.abs(w - ww) <= np.abs(ww) * 2.0**-24 * (1 + 1e-6) + 2.0**-149).all()
+
+
+def test_refusals():
+    def call(dtype=0, x=A, stride=64, T=4, E=64, score=0, bias=A, groups=8, kept=4, best=2, k=8, count=None, experts=A, weights=A):
+        return L.lib.lowbit_route(dtype, x, stride, T, E, score, bias, groups, kept, best, k, 1, 1.0, count, experts, weights, None)
+
+    assert call(dtype=3) == L.LB_EINVAL and call(score=2) == L.LB_EINVAL
+    for bad in (dict(T=-1), dict(T=1 << 26), dict(E=0), dict(E=1025, groups=1, kept=1, stride=1025), dict(groups=0), dict(groups=7), dict(kept=0), dict(kept=9),
+                dict(best=0), dict(best=3), dict(k=0), dict(k=33), dict(E=128, groups=1, kept=1, k=65, stride=128), dict(stride=63)):
+        assert call(**bad) == L.LB_ESHAPE, bad
+    assert call(E=130, groups=65, kept=65, stride=130) == L.LB_ESHAPE
+    for name in ("x", "experts", "weights"):
+        assert call(**{name: None}) == L.LB_EINVAL
+    for name in ("x", "experts", "weights", "bias", "count"):
+        assert call(**{name: A + 2}) == L.LB_EALIGN
+    assert call(T=0, x=None) == L.LB_OK
+
+
+def test_binding_checks_extents():
+    t = dict(x=torch.zeros(4, 64), e=torch.zeros(4, 8, dtype=torch.int32), w=torch.zeros(4, 8))
+    for name, bad in dict(x=t["x"][:3], e=t["e"][:3], w=t["w"].double()).items():
+        a = t | {name: bad}
+        with pytest.raises(ValueError):
+            L.lowbit_route(L.F32, a["x"], 4, 64, 8, a["e"], a["w"])
+    with pytest.raises(ValueError):
+        L.lowbit_route(L.F32, t["x"], 4, 64, 8, t["e"], t["w"], bias=torch.zeros(63))
+    with pytest.raises(ValueError):
+        L.lowbit_route(L.F32, t["x"][:, :63], 4, 64, 8, t["e"], t["w"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T,E,k,sigmoid,bias,groups,kept,best,renorm", [
+    (1, 1, 1, False, False, 1, 1, 1, True), (1, 64, 8, False, False, 1, 1, 1, True), (5, 8, 8, True, False, 1, 1, 1, False),
+    (33, 60, 4, False, True, 4, 2, 1, True), (130, 256, 8, True, True, 8, 4, 2, True), (7, 384, 10, True, True, 1, 1, 1, True),
+    (9, 160, 6, False, False, 8, 3, 1, False), (6, 1024, 64, False, True, 64, 40, 2, True), (4, 1000, 33, True, False, 5, 5, 2, True),
+    (11, 128, 2, True, True, 64, 1, 2, True), (12, 96, 3, False, False, 32, 1, 2, True), (3, 65, 65 - 1, True, True, 1, 1, 1, True),
+    (2049, 512, 8, False, False, 1, 1, 1, True)])
+def test_choices_and_weights(kind, T, E, k, sigmoid, bias, groups, kept, best, renorm):
+    say(f"case route {kind} T={T} E={E} k={k} sigmoid={sigmoid} groups={groups}/{kept}")
+    rng = np.random.default_rng(E + k)
+    x = torch.from_numpy(2 * rng.standard_normal((T, E))).to(TYPES[kind][1])
+    b = (0.1 * rng.standard_normal(E)).astype(np.float32) if bias else None
+    check(x, kind, k, sigmoid, b, groups, kept, best, renorm, factor=2.5 if T % 2 else 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups,kept,best", [(1, 1, 1), (4, 2, 1), (4, 3, 2)])
+def test_ties_go_to_the_lowest_index(sigmoid, groups, kept, best):
+    say(f"case route ties sigmoid={sigmoid} groups={groups}")
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.integers(-1, 2, (40, 200)).astype(np.float32))
+    x[0] = 0
+    x[1, 100:] = 5
+    check(x, "f32", 12, sigmoid, None, groups, kept, best)
+    check(x, "f32", 12, sigmoid, np.tile(np.float32([0.25, 0.5]), 100), groups, kept, best)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_masked_and_infinite_logits(sigmoid):
+    rng = np.random.default_rng(9)
+    x = torch.from_numpy(rng.standard_normal((12, 70)).astype(np.float32))
+    x[0] = -np.inf  # nothing is allowed
+    x[1] = np.nan
+    x[2, 3:] = -np.inf  # fewer than are chosen
+    x[3, 5], x[3, 66] = np.inf, np.inf
+    x[4, 7] = np.nan
+    x[5] = torch.finfo(torch.float32).min
+    x[6, :69] = torch.finfo(torch.float32).min
+    x[7] = torch.finfo(torch.float32).max
+    x[8, 10], x[8, 11] = np.inf, np.nan
+    x[9] *= 1e5  # far apart: most weights are 0 also in 64 bits
+    x[10] *= 1e-30
+    for renorm in (True, False):
+        check(x, "f32", 6, sigmoid, None, renorm=renorm)
+        check(x, "f32", 6, sigmoid, None, 7, 2, 2, renorm=renorm)
+        b = np.zeros(70, np.float32)
+        b[3], b[9], b[20] = np.nan, -np.inf, np.inf
+        check(x, "f32", 6, sigmoid, b, renorm=renorm)
+        check(x, "f32", 6, sigmoid, b, 7, 3, 2, renorm=renorm)
+
+
+@pytest.mark.gpu
+def test_near_ties_are_decided_in_64_bits():
+    """Sums of score and bias that fp32 cannot tell apart."""
+    x = torch.zeros(1, 64)
+    b = np.zeros(64, np.float32)
+    x[0, 10], x[0, 20], x[0, 30] = 1e-7, 2e-7, 1.5e-7
+    check(x, "f32", 3, True, b)
+    check(x, "f32", 3, False, b)
+    assert reference(x.double().numpy(), 3)[0].tolist() == [[20, 30, 10]]
+
+
+@pytest.mark.gpu
+def test_strides_counts_and_other_streams():
+    rng = np.random.default_rng(4)
+    T, E, k = 37, 64, 6
+    wide = dev(rng.standard_normal((T, E + 9)).astype(np.float32))
+    x = wide[:, 3:3 + E]
+    we, ww = reference(host(x).astype(np.float64), k)
+    e, w = run(x, "f32", k)
+    assert np.array_equal(e, we)
+    for n in (0, 1, 20, T, T + 5):
+        side = torch.cuda.Stream() if n % 2 else None
+        count = torch.tensor([n], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        e, w = run(x, "f32", k, count=count, stream=side)
+        assert np.array_equal(e[:n], we[:n]) and (e[n:] == -1).all() and (w[n:] == 0).all()
+
+
+@pytest.mark.gpu
+def test_captured():
+    T, E, k = 50, 256, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, b = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda"), torch.zeros(E, device="cuda")
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = [torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")]
+    args = dict(score=L.SCORE_SIGMOID, bias=b, groups=8, groups_kept=4, group_best=2, count=count)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.lowbit_route(L.BF16, x, T, E, k, *out, **args)
+    for i in range(4):
+        x.copy_(torch.randn(T, E, generator=g, device="cuda"))
+        b.copy_(torch.randn(E, generator=g, device="cuda") * 0.1)
+        count.fill_(T - 9 * i)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = [torch.zeros_like(t) for t in out]
+        L.lowbit_route(L.BF16, x, T, E, k, *mine, **args)
+        assert torch.equal(out[0], mine[0]) and torch.equal(out[1], mine[1])
+        n = T - 9 * i
+        assert np.array_equal(host(out[0])[:n], reference(x[:n].double().cpu().numpy(), k, True, host(b), 8, 4, 2)[0])
