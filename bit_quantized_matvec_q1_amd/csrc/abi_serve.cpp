@@ -379,16 +379,16 @@ lb_status lowbit_experts_matmul(int fmt, const void *W, int64_t E, int64_t N, in
     a.W = static_cast<const uint8_t *>(W), a.expert_bytes = lowbit_experts_weight_bytes(fmt, 1, N, K);
     a.E = (int32_t)E, a.N = (int32_t)N, a.K = (int32_t)K, a.pairs = (int32_t)pairs, a.per_row = (int32_t)pairs_per_row;
     a.xq = xq, a.xs = static_cast<const uint16_t *>(xscale), a.experts = experts, a.plan = static_cast<const int32_t *>(plan);
-    a.max_tiles = plan ? lb::experts_max_tiles(pairs, E) : pairs, a.y = y;
-    const bool gemm = plan && lb::experts_tile_rows(pairs, E) > 4;
+    a.max_tiles = lb::experts_max_tiles(pairs, E), a.y = y;
+    const int64_t rows = plan ? lb::experts_tile_rows(pairs, E) : 1;
     // a launch's threads are numbered in 32 bits
-    const int64_t blocks = gemm ? a.max_tiles * ((N + 63) / 64) : lb::experts_rows_blocks(fmt, a);
-    if (blocks >= (int64_t)1 << (gemm ? 23 : 24))
+    const int64_t blocks = plan ? a.max_tiles * ((N + 63) / 64) + 7 : lb::experts_pair_blocks(fmt, a);
+    if (blocks >= (int64_t)1 << (rows > 16 ? 23 : 24))
         return lb::abi_fail(LB_ESHAPE, fn, "over 2^32 threads");
     lb_status st = lb::abi_check_device(fn);
     if (st != LB_OK)
         return st;
-    return lb::abi_hip(fn, gemm ? lb::launch_experts_gemm(fmt, a, s) : lb::launch_experts_rows(fmt, a, s));
+    return lb::abi_hip(fn, rows > 16 ? lb::launch_experts_gemm(fmt, a, s) : rows > 1 ? lb::launch_experts_tile(fmt, a, s) : lb::launch_experts_pairs(fmt, a, s));
 }
 
 lb_status lowbit_experts_combine(int dtype, const float *y, const int32_t *experts, const float *weights, int64_t T, int64_t top_k, int64_t E,

@@ -1,0 +1,341 @@
+// The experts' products with up to 16 rows of activations a tile, on the int8 matrix cores.
+//
+// Between a decode step's one or two rows an expert, where nibble dot products on the vector unit keep up with HBM
+// (experts.hip), and a prompt's hundreds (gemm.hip) a product of 16 x 16 tiles reads the weights once for 16 rows: the rows
+// are the A operand (from LDS), 16 weight rows the B operand, unpacked in registers as they come from HBM.
+//  * Lane (n, q) = (lane mod 16, lane / 16) loads whole 16-byte records, record 4 s + q of weight row n.  The matrix product
+//    wants a q8_0 block's weights spread over the four q, so four records are transposed between the lanes' quarters, dword
+//    by dword (v_permlane32_swap, v_permlane16_swap: four instructions for four records).
+//  * The order of weights within a block is free, as long as the activations have the same: they are staged in the order in
+//    which shifts and masks isolate the weights' bytes, which needs no further arrangement.  Q4_0: nibbles in the upper
+//    halves of bytes, 16 w (the factor is in the activation scale); Q2_0_g64: codes w + 1; Q1_0: 2 bit = w + 1.  The sum of
+//    the activations that codes carry too much is subtracted by the accumulator's start.
+//  * A Q2_0_g64 dword belongs to one of its record's two q8_0 blocks: the 64-deep product is taken twice, with the other
+//    block's activations read as zeros.
+//  * Results are read as fp32 through the bias 1.5 * 2^23 as in gemm.hip: round(d_x * isum), then one multiply-add with the
+//    weight scale (one value a lane).
+// A wave has G groups of 16 weight rows, so that what it reads from LDS (activations, scales, accumulator starts) is read
+// once for all of them.
+#include "matvec_tile.h"
+#include "serve_internal.h"
+
+namespace lb {
+
+namespace {
+
+constexpr int TR = 16;   // activation rows a tile
+constexpr int G = 2;     // groups of 16 weight rows a wave
+constexpr int KC = 1024; // columns staged at a time: 20 KiB of LDS, and 2 to 9 of weight scales
+constexpr uint32_t BIAS = 0x4B400000u; // 1.5 * 2^23 as fp32 bits
+constexpr float BIASF = 12582912.0f;
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef unsigned v2u_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef __attribute__((address_space(1))) const v2u_a2 gv2u_a2;
+
+template <int FMT> struct __attribute__((aligned(16))) TileLds {
+    static constexpr int BLOCKS = KC / QK8, RECORDS = KC / F<FMT>::SW, WROWS = 64 * G;
+    // a weight row's scales of the chunk, 8 bytes apart from the next row's (16 rows' reads of 8 bytes meet 16 pairs of banks)
+    static constexpr int SCALES = RECORDS + 4;
+    uint32_t x[KC * TR / 4]; // Q4_0, Q1_0: [block][q][row] 8 bytes; Q2_0_g64: [record][q][row] 16 bytes
+    float dx[BLOCKS * TR];   // [block][row]
+    int start[FMT == LB_Q4_0 ? 4 : BLOCKS * TR]; // accumulator starts, [block][row]
+    uint16_t dw[WROWS * SCALES];
+    uint4 zero;
+};
+
+__device__ __forceinline__ uint32_t bperm(uint32_t s0, uint32_t s1, uint32_t sel) { return __builtin_amdgcn_perm(s0, s1, sel); }
+
+// A workgroup barrier after this thread's LDS accesses, which leaves its loads from memory in flight (__syncthreads() would
+// wait for them); the empty asm statements keep the compiler from moving LDS accesses across it.
+__device__ __forceinline__ void chunk_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// d[i] of lane quarter q becomes d[q] of quarter i
+__device__ __forceinline__ void transpose_quarters(uint32_t (&d)[4])
+{
+    auto p = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+    d[0] = p[0], d[2] = p[1];
+    p = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    d[1] = p[0], d[3] = p[1];
+    p = __builtin_amdgcn_permlane16_swap(d[0], d[1], false, false);
+    d[0] = p[0], d[1] = p[1];
+    p = __builtin_amdgcn_permlane16_swap(d[2], d[3], false, false);
+    d[2] = p[0], d[3] = p[1];
+}
+
+// Block b (32 columns from column 32 b of the chunk) of activation row r: 32 bytes and their scale.
+template <int FMT> __device__ __forceinline__ void stage_block(TileLds<FMT> &lds, int b, int r, uint4 lo, uint4 hi, float dx)
+{
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (FMT == LB_Q2_0_G64) { // weights 16 q + 4 t + s at byte t of dword s
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint32_t *e = w + 4 * h;
+            const uint32_t lo01 = bperm(e[1], e[0], 0x05010400u), hi01 = bperm(e[1], e[0], 0x07030602u);
+            const uint32_t lo23 = bperm(e[3], e[2], 0x05010400u), hi23 = bperm(e[3], e[2], 0x07030602u);
+            *reinterpret_cast<uint4 *>(lds.x + (b >> 1) * 256 + ((2 * (b & 1) + h) * TR + r) * 4) =
+                make_uint4(bperm(lo23, lo01, 0x05040100u), bperm(lo23, lo01, 0x07060302u), bperm(hi23, hi01, 0x05040100u), bperm(hi23, hi01, 0x07060302u));
+        }
+    } else { // weights 8 q + 0, 2, 4, 6, then 8 q + 1, 3, 5, 7
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            *reinterpret_cast<uint2 *>(lds.x + b * 128 + (q * TR + r) * 2) =
+                make_uint2(bperm(w[2 * q + 1], w[2 * q], 0x06040200u), bperm(w[2 * q + 1], w[2 * q], 0x07050301u));
+    }
+    int sq = 0;
+    if (FMT != LB_Q4_0) {
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            sq = __builtin_amdgcn_sdot4((int)w[k], 0x01010101, sq, false);
+    }
+    lds.dx[b * TR + r] = FMT == LB_Q4_0 ? dx * 0.0625f : dx;
+    if (FMT != LB_Q4_0)
+        lds.start[b * TR + r] = (int)BIAS - sq;
+}
+
+// (Two waves a SIMD at the least: with 256 registers the matrix products' results are in vector registers; with more the
+// compiler has them in accumulator registers, which costs a move each.)
+template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_tile_kernel(ExpertsArgs a, int chunks)
+{
+    using Lds = TileLds<FMT>;
+    __shared__ Lds lds;
+    constexpr int BPR = F<FMT>::SW / QK8; // q8_0 blocks a record
+    const int64_t at = experts_block(a.plan[0], chunks);
+    if (at < 0)
+        return;
+    const int chunk = (int)(at % chunks), tile = (int)(at / chunks);
+    if (tile >= a.max_tiles)
+        return; // no plan of these pairs
+    const int4 t = reinterpret_cast<const int4 *>(a.plan + experts_tiles_at(a.pairs))[tile];
+    if ((unsigned)t.x >= (unsigned)a.E || t.y < 0 || t.z < 1 || t.z > TR || t.y > a.pairs - t.z)
+        return; // no tile, or no plan of these pairs
+    const uint8_t *W = a.W + t.x * a.expert_bytes;
+    const int32_t *order = a.plan + experts_order_at() + t.y;
+    const int rows = t.z, ns = a.K / F<FMT>::SW;
+    const uint8_t *scales = W + (int64_t)a.N * ns * CODE_BYTES;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
+    const int n0 = (chunk * (WG / 64) + wave) * G * 16 + (lane & 15); // this lane's weight row in group 0
+    if (threadIdx.x == 0)
+        lds.zero = make_uint4(0, 0, 0, 0);
+
+    uint32_t rec0[G]; // first record of the lane's rows
+#pragma unroll
+    for (int g = 0; g < G; g++)
+        rec0[g] = (uint32_t)min(n0 + 16 * g, a.N - 1) * (uint32_t)ns;
+    // A step is H times four records of a row.  Q4_0, whose records are soonest computed, takes 128 bytes, whole lines, at
+    // once; for the others the registers of a second half cost more than the lines' second visit.
+    constexpr int H = FMT == LB_Q4_0 ? 2 : 1;
+    struct Regs {
+        uint4 code[H][G];
+    };
+    auto issue = [&](Regs &r, int s) {
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int h = 0; h < H; h++) {
+                const v4u c = *(gv4u *)((gu8 *)W + (rec0[g] + (uint32_t)min(4 * (H * s + h) + q, ns - 1)) * (uint32_t)CODE_BYTES);
+                r.code[h][g] = make_uint4(c.x, c.y, c.z, c.w);
+            }
+    };
+    float acc[G][4] = {};
+    auto compute = [&](const uint4 (&code)[G], int s, int first) { // records 4 s .. 4 s + 3; first: the chunk's first
+        uint32_t d[G][4];
+        uint2 sc[G];
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            sc[g] = *reinterpret_cast<const uint2 *>(lds.dw + (wave * G * 16 + g * 16 + (lane & 15)) * Lds::SCALES + (4 * s - first));
+            d[g][0] = code[g].x, d[g][1] = code[g].y, d[g][2] = code[g].z, d[g][3] = code[g].w;
+            transpose_quarters(d[g]);
+        }
+        auto record = [&](int j) {
+            const int rec = 4 * s + j;
+            // the record's weights as bytes: Q2_0_g64 16 of them, the others 8 for each of its blocks
+            constexpr int WB = FMT == LB_Q1_0 ? 4 : 1, WD = FMT == LB_Q2_0_G64 ? 4 : 2;
+            uint32_t w[G][WB][WD];
+            float dw[G];
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const uint32_t v = d[g][j], h = j < 2 ? sc[g].x : sc[g].y;
+                dw[g] = half_bits_to_float((uint16_t)(j & 1 ? h >> 16 : h));
+                if (FMT == LB_Q2_0_G64) {
+#pragma unroll
+                    for (int i = 0; i < WD; i++)
+                        w[g][0][i] = (v >> (2 * i)) & 0x03030303u;
+                } else if (FMT == LB_Q4_0) {
+                    w[g][0][0] = (v << 4) & 0xF0F0F0F0u, w[g][0][1] = v & 0xF0F0F0F0u;
+                } else { // the sign of block b, at bit b of each nibble, moved to bit 1
+#pragma unroll
+                    for (int b = 0; b < WB; b++)
+                        w[g][b][0] = (b ? v >> (b - 1) : v << 1) & 0x02020202u, w[g][b][1] = (v >> (b + 3)) & 0x02020202u;
+                }
+            }
+            const int r0 = rec - first;
+            float tg[G][4];
+#pragma unroll
+            for (int b = 0; b < BPR; b++) {
+                const int at = (r0 * BPR + b) * TR + 4 * q;
+                const float4 dx = *reinterpret_cast<const float4 *>(lds.dx + at);
+                v4i start = {(int)BIAS, (int)BIAS, (int)BIAS, (int)BIAS};
+                if (FMT != LB_Q4_0)
+                    start = *reinterpret_cast<const v4i *>(lds.start + at);
+                const float dxv[4] = {dx.x, dx.y, dx.z, dx.w};
+                float c[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    c[i] = -dxv[i] * BIASF; // exact: an 11-bit significand times 3 * 2^22
+                v4i xw = {};
+                long xb = 0;
+                if (FMT == LB_Q2_0_G64) {
+                    const uint32_t *p = (q >> 1) == b ? lds.x + r0 * 256 + lane * 4 : reinterpret_cast<const uint32_t *>(&lds.zero);
+                    xw = *reinterpret_cast<const v4i *>(p);
+                } else {
+                    xb = *reinterpret_cast<const long *>(lds.x + (r0 * BPR + b) * 128 + lane * 2);
+                }
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    v4i D;
+                    if (FMT == LB_Q2_0_G64) {
+                        const v4i wv = {(int)w[g][0][0], (int)w[g][0][1], (int)w[g][0][WD - 2], (int)w[g][0][WD - 1]};
+                        D = __builtin_amdgcn_mfma_i32_16x16x64_i8(xw, wv, start, 0, 0, 0);
+                    } else {
+                        const int wb = FMT == LB_Q1_0 ? b : 0;
+                        D = __builtin_amdgcn_mfma_i32_16x16x32_i8(xb, (long)((uint64_t)w[g][wb][1] << 32 | w[g][wb][0]), start, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float f = fmaf(dxv[i], __int_as_float(D[i]), c[i]); // round(d_x * isum)
+                        tg[g][i] = b ? tg[g][i] + f : f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < G; g++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    acc[g][i] = fmaf(dw[g], tg[g][i], acc[g][i]);
+        };
+        if (4 * s + 4 <= ns) { // uniform: in one piece, so that one record's loads from LDS go out in another's arithmetic
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                record(j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; j++)
+                if (4 * s + j < ns)
+                    record(j);
+        }
+    };
+
+    // staging: a thread has blocks tid / TR, and so on by 256 / TR, of activation row tid mod TR (a row past the tile's
+    // repeats its last and is not stored)
+    constexpr int BSTEP = WG / TR, U = Lds::BLOCKS / BSTEP;
+    const int sr = threadIdx.x % TR, sb = threadIdx.x / TR;
+    const int64_t row = min((uint32_t)order[min(sr, rows - 1)], (uint32_t)(a.pairs - 1)) / (uint32_t)a.per_row;
+    const int8_t *xq = a.xq + row * a.K;
+    const uint16_t *xs = a.xs + row * (a.K / QK8);
+
+    // and eight scales of a weight row (their lines would be read again for every four records otherwise)
+    constexpr int PARTS = Lds::RECORDS / 8, PIECES = Lds::WROWS * PARTS, P = (PIECES + WG - 1) / WG;
+    // A chunk's activations and scales are loaded into registers a chunk ahead, the weights a step ahead: what is waited for
+    // was asked for long before.
+    uint4 lo[U], hi[U], dws[P];
+    uint32_t sc[U];
+    auto load_chunk = [&](int k0) {
+        const int nblk = min(Lds::BLOCKS, (a.K - k0) / QK8);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int b = min(sb + BSTEP * u, nblk - 1);
+            lo[u] = *reinterpret_cast<const uint4 *>(xq + k0 + 32 * b);
+            hi[u] = *reinterpret_cast<const uint4 *>(xq + k0 + 32 * b + 16);
+            sc[u] = xs[k0 / QK8 + b];
+        }
+#pragma unroll
+        for (int u = 0; u < P; u++) {
+            const int p = threadIdx.x + u * WG, rec = k0 / F<FMT>::SW + p % PARTS * 8;
+            const uint32_t at = (uint32_t)min(chunk * Lds::WROWS + p / PARTS, a.N - 1) * (uint32_t)ns;
+            if (WHOLE) { // the eight lie in the row, and on 16 bytes
+                const v4u d = *(gv4u *)((gu8 *)scales + (at + (uint32_t)min(rec, ns - 8)) * 2u);
+                dws[u] = make_uint4(d.x, d.y, d.z, d.w);
+            } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    h[j] = *(gu16 *)((gu8 *)scales + (at + (uint32_t)min(rec + j, ns - 1)) * 2u);
+                dws[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+            }
+        }
+    };
+    const int steps = (ns + 4 * H - 1) / (4 * H);
+    constexpr int SPC = Lds::RECORDS / (4 * H); // steps a chunk
+    Regs buf[2];
+    load_chunk(0);
+    issue(buf[0], 0);
+    for (int s = 0; s < steps; s += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            if (s + u >= steps) // uniform
+                break;
+            if (u % SPC == 0 && (s + u) % SPC == 0) { // uniform: the next chunk
+                const int k0 = (s + u) * 4 * H * F<FMT>::SW, nblk = min(Lds::BLOCKS, (a.K - k0) / QK8);
+                if (s + u)
+                    chunk_barrier(); // every wave has read the chunk before
+#pragma unroll
+                for (int v = 0; v < U; v++)
+                    if (sb + BSTEP * v < nblk)
+                        stage_block<FMT>(lds, sb + BSTEP * v, sr, lo[v], hi[v], half_bits_to_float((uint16_t)sc[v]));
+#pragma unroll
+                for (int v = 0; v < P; v++) {
+                    const int p = threadIdx.x + v * WG;
+                    if (PIECES % WG == 0 || p < PIECES) {
+                        uint2 *to = reinterpret_cast<uint2 *>(lds.dw + p / PARTS * Lds::SCALES + p % PARTS * 8);
+                        to[0] = make_uint2(dws[v].x, dws[v].y), to[1] = make_uint2(dws[v].z, dws[v].w);
+                    }
+                }
+                if (k0 + KC < a.K) // uniform
+                    load_chunk(k0 + KC);
+                chunk_barrier();
+            }
+            issue(buf[1 - u], min(s + u + 1, steps - 1));
+            __builtin_amdgcn_sched_barrier(0); // these loads go out before this step's arithmetic
+#pragma unroll
+            for (int h = 0; h < H; h++)
+                if (h == 0 || 4 * (H * (s + u) + h) < ns) // uniform
+                    compute(buf[u].code[h], H * (s + u) + h, (s + u) / SPC * SPC * 4 * H);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = 4 * q + i;
+        const int64_t pair = min((uint32_t)order[min(r, rows - 1)], (uint32_t)(a.pairs - 1));
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            if (r < rows && n0 + 16 * g < a.N)
+                a.y[pair * a.N + n0 + 16 * g] = acc[g][i];
+    }
+}
+
+template <int FMT> hipError_t tile_fmt(const ExpertsArgs &a, hipStream_t s)
+{
+    const int chunks = (a.N + TileLds<FMT>::WROWS - 1) / TileLds<FMT>::WROWS;
+    const dim3 grid((unsigned)((a.max_tiles * chunks + 7) / 8 * 8));
+    if (a.K / F<FMT>::SW % 8 == 0)
+        hipLaunchKernelGGL((experts_tile_kernel<FMT, true>), grid, dim3(WG), 0, s, a, chunks);
+    else
+        hipLaunchKernelGGL((experts_tile_kernel<FMT, false>), grid, dim3(WG), 0, s, a, chunks);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_experts_tile(int fmt, const ExpertsArgs &a, hipStream_t s)
+{
+    return fmt == LB_Q1_0 ? tile_fmt<LB_Q1_0>(a, s) : fmt == LB_Q2_0_G64 ? tile_fmt<LB_Q2_0_G64>(a, s) : tile_fmt<LB_Q4_0>(a, s);
+}
+
+} // namespace lb

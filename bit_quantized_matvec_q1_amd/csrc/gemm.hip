@@ -414,7 +414,7 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
 // walk alternate K-steps of the same output tile with their own LDS buffers and add their partial sums
 // at the end, so a CU holds 16 waves where the tile count alone would give it 8.
 struct GroupArgs { // GROUPED: the experts' tensors and the plan (ExpertsArgs)
-    int64_t expert_bytes, tiles_at;
+    int64_t expert_bytes, tiles_at, max_tiles;
     const int32_t *plan;
     int32_t E, pairs, per_row;
 };
@@ -437,12 +437,16 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     const int h = lane >> 5, l32 = lane & 31;
     // this wave's 32 x 32 output tile inside the 64 x 128 workgroup tile
     const int wn = wave & 1, wm = wave >> 1;
-    const int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
+    int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
+    if constexpr (GROUPED) {
+        const int64_t at = experts_block(ga.plan[0], ntn);
+        if (at < 0 || at / ntn >= ga.max_tiles)
+            return;
+        bn = (int)(at % ntn), bm = (int)(at / ntn);
+    }
     const int n0 = bn * TN, m0 = GROUPED ? 0 : bm * TM;
     Gather g = {};
     if constexpr (GROUPED) {
-        if (bm >= ga.plan[0])
-            return;
         const int4 t = reinterpret_cast<const int4 *>(ga.plan + ga.tiles_at)[bm];
         if ((unsigned)t.x >= (unsigned)ga.E || t.y < 0 || t.z < 1 || t.z > TM || t.y > ga.pairs - t.z)
             return; // no plan of these pairs
@@ -508,6 +512,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
             break;
         // the second half of a split workgroup may run one step short: it still meets every barrier
         const bool active = KSPLIT == 1 || j * KSPLIT + half < nsteps; // uniform per half
+        const bool some = !GROUPED || 32 * wm < M; // uniform: a wave without rows of the tile computes nothing
         __builtin_amdgcn_s_waitcnt(wait_vmcnt(0)); // this thread's loads of step j have landed
         if (active)
             store_step<FMT>(lds[half], q, ring, K, kk, tid);
@@ -519,7 +524,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         kn = kn >= kend ? kn - kend : kn;
         load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
         issue_x(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
-        if (active)
+        if (active && some)
             step_compute<FMT, EMIT, 4>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
                                        kk, acc, iacc, cbias, sums);
         kk = kn;
@@ -632,8 +637,8 @@ hipError_t launch_fmt(const uint8_t *W, int64_t N, int64_t K, float w_scale, con
 template <int FMT> hipError_t launch_experts_fmt(const ExpertsArgs &a, hipStream_t s)
 {
     const int64_t ntn = (a.N + TN - 1) / TN;
-    const GroupArgs ga = {a.expert_bytes, experts_tiles_at(a.pairs), a.plan, a.E, a.pairs, a.per_row};
-    hipLaunchKernelGGL((gemm_kernel<FMT, false, 1, true>), dim3((unsigned)(ntn * a.max_tiles)), dim3(GT), 0, s, a.W, a.N, a.K, 1.0f, a.xq, a.xs,
+    const GroupArgs ga = {a.expert_bytes, experts_tiles_at(a.pairs), a.max_tiles, a.plan, a.E, a.pairs, a.per_row};
+    hipLaunchKernelGGL((gemm_kernel<FMT, false, 1, true>), dim3((unsigned)((ntn * a.max_tiles + 7) / 8 * 8)), dim3(GT), 0, s, a.W, a.N, a.K, 1.0f, a.xq, a.xs,
                        0, a.y, nullptr, (int)ntn, ga);
     return hipGetLastError();
 }

@@ -124,9 +124,18 @@ hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
 
 // The routed pairs by expert (include/lowbit.h, lowbit_experts_plan): int32 words
 //   [0] tiles, [1] routed pairs, [2], [3] unused; order [pairs, rounded up to 4]; tiles {expert, first place in order, rows, 0}
-// A tile is at most experts_tile_rows() pairs of one expert.
+// A tile is at most experts_tile_rows() pairs of one expert, and may be empty (rows 0).
 inline __host__ __device__ int64_t experts_order_at() { return 4; }
 inline __host__ __device__ int64_t experts_tiles_at(int64_t pairs) { return 4 + (pairs + 3) / 4 * 4; }
+// The workgroup's place in a grid of tiles x chunks of weight rows, -1 for none.  Workgroups go to the eight XCDs in turn:
+// each XCD takes one eighth of the places, one after another, so that the tiles of an expert, which read the same weights,
+// meet in one L2.
+inline __device__ int64_t experts_block(int tiles, int chunks)
+{
+    const int64_t all = (int64_t)max(tiles, 0) * chunks, share = (all + 7) / 8;
+    const int64_t i = blockIdx.x / 8, at = (blockIdx.x % 8) * share + i;
+    return i < share && at < all ? at : -1;
+}
 int64_t experts_tile_rows(int64_t pairs, int64_t E);
 int64_t experts_max_tiles(int64_t pairs, int64_t E);
 
@@ -136,14 +145,14 @@ struct ExpertsArgs {
     int32_t E, N, K, pairs, per_row;
     const int8_t *xq;
     const uint16_t *xs;
-    const int32_t *experts, *plan; // plan null: a tile a pair
-    int64_t max_tiles;
+    const int32_t *experts, *plan; // plan null: every pair by itself
+    int64_t max_tiles;             // of the plan
     float *y;
 };
 hipError_t launch_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, int32_t *plan, hipStream_t s);
-// 0: no kernel for these sizes
-int64_t experts_rows_blocks(int fmt, const ExpertsArgs &a);
-hipError_t launch_experts_rows(int fmt, const ExpertsArgs &a, hipStream_t s);
+int64_t experts_pair_blocks(int fmt, const ExpertsArgs &a); // workgroups of launch_experts_pairs
+hipError_t launch_experts_pairs(int fmt, const ExpertsArgs &a, hipStream_t s);
+hipError_t launch_experts_tile(int fmt, const ExpertsArgs &a, hipStream_t s);
 hipError_t launch_experts_gemm(int fmt, const ExpertsArgs &a, hipStream_t s);
 struct CombineArgs {
     const float *y;
