@@ -333,7 +333,8 @@ int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E)
 {
     if (pairs < 0 || pairs > kMax - 4 || E < 1 || E > kMaxExperts)
         return -1;
-    return 4 * (lb::experts_tiles_at(pairs) + 4 * lb::experts_max_tiles(pairs, E));
+    const int64_t tiles = lb::experts_max_tiles(pairs, E);
+    return (4 * lb::experts_pairs_at(tiles, tiles, lb::experts_tile_rows(pairs, E)) + 15) / 16 * 16;
 }
 
 lb_status lowbit_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, void *plan, hipStream_t s)

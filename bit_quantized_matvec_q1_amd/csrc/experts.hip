@@ -24,7 +24,7 @@ constexpr int PLAN_WG = 1024, PLAN_WAVES = PLAN_WG / 64, MAX_E = 1024, FEW_PAIRS
 
 template <bool FEW>
 __global__ __launch_bounds__(PLAN_WG) void plan_kernel(const int32_t *__restrict__ experts, int pairs, int E, int32_t *__restrict__ plan,
-                                                       int tile_rows, int64_t tiles_at)
+                                                       int tile_rows, int max_tiles)
 {
     __shared__ int hist[FEW ? MAX_E : 1];
     __shared__ int mine[PLAN_WAVES], before[PLAN_WAVES], tiles[PLAN_WAVES];
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(PLAN_WG) void plan_kernel(const int32_t *__restrict
             before[wave] = n, tiles[wave] = nt;
         __syncthreads();
     }
-    int first = 0, tile = 0, at = 0, rows = 0;
+    int first = 0, tile = 0, at = 0, rows = 0; // `first`: pairs of the experts before
     for (int w = 0; w < PLAN_WAVES; w++) {
         first += before[w], tile += tiles[w], rows += mine[w];
         at += w < wave ? mine[w] : 0;
@@ -83,12 +83,17 @@ __global__ __launch_bounds__(PLAN_WG) void plan_kernel(const int32_t *__restrict
         tile = first / tile_rows + e;
         entries = (first + rows) / tile_rows + e + 1 - tile;
     }
-    if (e == E - 1 && threadIdx.x == 0)
-        plan[0] = tile + entries, plan[1] = first + rows, plan[2] = plan[3] = 0;
-    int4 *table = reinterpret_cast<int4 *>(plan + tiles_at);
+    if (e == E - 1) { // the rest of the table too
+        if (threadIdx.x == 0)
+            plan[0] = tile + entries, plan[1] = first + rows, plan[2] = plan[3] = 0;
+        entries = max_tiles - tile;
+    }
+    int2 *table = reinterpret_cast<int2 *>(plan + experts_tile_at(tile));
     for (int i = threadIdx.x; i < entries; i += PLAN_WG)
-        table[tile + i] = make_int4(e, first + min(i * tile_rows, rows), max(0, min(tile_rows, rows - i * tile_rows)), 0);
-    int32_t *order = plan + experts_order_at() + first;
+        table[i] = make_int2(e, max(0, min(tile_rows, rows - i * tile_rows)));
+    int32_t *places = plan + experts_pairs_at(max_tiles, tile, tile_rows);
+    for (int i = rows + threadIdx.x; i < own_tiles * tile_rows; i += PLAN_WG)
+        places[i] = -1;
     for (int64_t p = p0; p < p1; p += 64 * U) {
         int x[U];
         load(p, x);
@@ -96,7 +101,7 @@ __global__ __launch_bounds__(PLAN_WG) void plan_kernel(const int32_t *__restrict
         for (int u = 0; u < U; u++) {
             const uint64_t m = __ballot(x[u] == e);
             if (x[u] == e)
-                order[at + __popcll(m & (((uint64_t)1 << lane) - 1))] = (int32_t)(p + 64 * u + lane);
+                places[at + __popcll(m & (((uint64_t)1 << lane) - 1))] = (int32_t)(p + 64 * u + lane);
             at += __popcll(m);
         }
     }
@@ -206,10 +211,10 @@ hipError_t launch_experts_plan(const int32_t *experts, int64_t pairs, int64_t E,
     const int rows = (int)experts_tile_rows(pairs, E);
     if (pairs <= FEW_PAIRS)
         hipLaunchKernelGGL(plan_kernel<true>, dim3((unsigned)E), dim3(PLAN_WG), 0, s, experts, (int)pairs, (int)E, plan, rows,
-                           experts_tiles_at(pairs));
+                           (int)experts_max_tiles(pairs, E));
     else
         hipLaunchKernelGGL(plan_kernel<false>, dim3((unsigned)E), dim3(PLAN_WG), 0, s, experts, (int)pairs, (int)E, plan, rows,
-                           experts_tiles_at(pairs));
+                           (int)experts_max_tiles(pairs, E));
     return hipGetLastError();
 }
 

@@ -106,18 +106,19 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
     using Lds = TileLds<FMT>;
     __shared__ Lds lds;
     constexpr int BPR = F<FMT>::SW / QK8; // q8_0 blocks a record
-    const int64_t at = experts_block(a.plan[0], chunks);
-    if (at < 0)
-        return;
-    const int chunk = (int)(at % chunks), tile = (int)(at / chunks);
-    if (tile >= a.max_tiles)
-        return; // no plan of these pairs
-    const int4 t = reinterpret_cast<const int4 *>(a.plan + experts_tiles_at(a.pairs))[tile];
-    if ((unsigned)t.x >= (unsigned)a.E || t.y < 0 || t.z < 1 || t.z > TR || t.y > a.pairs - t.z)
+    const int chunk = blockIdx.x % chunks, tile = blockIdx.x / chunks;
+    const int2 t = *reinterpret_cast<const int2 *>(a.plan + experts_tile_at(tile));
+    const int32_t *pairs = a.plan + experts_pairs_at(a.max_tiles, tile, TR);
+    // staging: a thread has blocks tid / TR, and so on by 256 / TR, of activation row tid mod TR (a place without a pair reads
+    // some row, and is not stored)
+    constexpr int BSTEP = WG / TR, U = Lds::BLOCKS / BSTEP;
+    const int sr = threadIdx.x % TR, sb = threadIdx.x / TR;
+    const int64_t row = min((uint32_t)pairs[sr], (uint32_t)(a.pairs - 1)) / (uint32_t)a.per_row;
+    const int rows = min(t.y, TR);
+    if ((unsigned)t.x >= (unsigned)a.E || rows < 1)
         return; // no tile, or no plan of these pairs
     const uint8_t *W = a.W + t.x * a.expert_bytes;
-    const int32_t *order = a.plan + experts_order_at() + t.y;
-    const int rows = t.z, ns = a.K / F<FMT>::SW;
+    const int ns = a.K / F<FMT>::SW;
     const uint8_t *scales = W + (int64_t)a.N * ns * CODE_BYTES;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
     const int n0 = (chunk * (WG / 64) + wave) * G * 16 + (lane & 15); // this lane's weight row in group 0
@@ -232,11 +233,6 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
         }
     };
 
-    // staging: a thread has blocks tid / TR, and so on by 256 / TR, of activation row tid mod TR (a row past the tile's
-    // repeats its last and is not stored)
-    constexpr int BSTEP = WG / TR, U = Lds::BLOCKS / BSTEP;
-    const int sr = threadIdx.x % TR, sb = threadIdx.x / TR;
-    const int64_t row = min((uint32_t)order[min(sr, rows - 1)], (uint32_t)(a.pairs - 1)) / (uint32_t)a.per_row;
     const int8_t *xq = a.xq + row * a.K;
     const uint16_t *xs = a.xs + row * (a.K / QK8);
 
@@ -312,7 +308,7 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int r = 4 * q + i;
-        const int64_t pair = min((uint32_t)order[min(r, rows - 1)], (uint32_t)(a.pairs - 1));
+        const int64_t pair = min((uint32_t)pairs[r], (uint32_t)(a.pairs - 1));
 #pragma unroll
         for (int g = 0; g < G; g++)
             if (r < rows && n0 + 16 * g < a.N)
@@ -323,7 +319,7 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
 template <int FMT> hipError_t tile_fmt(const ExpertsArgs &a, hipStream_t s)
 {
     const int chunks = (a.N + TileLds<FMT>::WROWS - 1) / TileLds<FMT>::WROWS;
-    const dim3 grid((unsigned)((a.max_tiles * chunks + 7) / 8 * 8));
+    const dim3 grid((unsigned)(a.max_tiles * chunks));
     if (a.K / F<FMT>::SW % 8 == 0)
         hipLaunchKernelGGL((experts_tile_kernel<FMT, true>), grid, dim3(WG), 0, s, a, chunks);
     else

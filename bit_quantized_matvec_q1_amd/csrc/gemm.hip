@@ -127,7 +127,8 @@ template <int FMT> __device__ __forceinline__ uint32_t step_sbytes(int kk)
     return FMT == LB_Q1_0 ? (uint32_t)(kk / 128) * 2u : scale32(FMT) ? (uint32_t)(kk / 32) * 2u : (uint32_t)(kk / 64) * 2u;
 }
 
-// `pairs`, GROUPED: the tile's pairs (M of them), of which `per_row` share an activation row; `n_pairs` bounds them.
+// GROUPED: the tile's TM places, of which M have a pair (the others read some row and are not stored); `per_row` pairs share
+// an activation row, and `n_pairs` bounds them.
 struct Gather {
     const int32_t *pairs;
     uint32_t per_row, n_pairs;
@@ -160,10 +161,10 @@ __device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, in
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         const int slot = 128 * wave + 64 * u + lane, r = slot / XCH;
-        const uint32_t xr = GROUPED ? g.row(min(r, M - 1)) : (uint32_t)min(m0 + r, M - 1);
+        const uint32_t xr = GROUPED ? g.row(r) : (uint32_t)min(m0 + r, M - 1);
         o.x[u] = xr * (uint32_t)K + 16u * (uint32_t)((slot % XCH) ^ ((r >> 1) & 7));
     }
-    o.dx = (GROUPED ? g.row(min(tid & (TM - 1), M - 1)) : (uint32_t)min(m0 + (tid & (TM - 1)), M - 1)) * (uint32_t)(K / QK8) * 2u;
+    o.dx = (GROUPED ? g.row(tid & (TM - 1)) : (uint32_t)min(m0 + (tid & (TM - 1)), M - 1)) * (uint32_t)(K / QK8) * 2u;
     return o;
 }
 
@@ -414,7 +415,7 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
 // walk alternate K-steps of the same output tile with their own LDS buffers and add their partial sums
 // at the end, so a CU holds 16 waves where the tile count alone would give it 8.
 struct GroupArgs { // GROUPED: the experts' tensors and the plan (ExpertsArgs)
-    int64_t expert_bytes, tiles_at, max_tiles;
+    int64_t expert_bytes, max_tiles;
     const int32_t *plan;
     int32_t E, pairs, per_row;
 };
@@ -437,22 +438,16 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     const int h = lane >> 5, l32 = lane & 31;
     // this wave's 32 x 32 output tile inside the 64 x 128 workgroup tile
     const int wn = wave & 1, wm = wave >> 1;
-    int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
-    if constexpr (GROUPED) {
-        const int64_t at = experts_block(ga.plan[0], ntn);
-        if (at < 0 || at / ntn >= ga.max_tiles)
-            return;
-        bn = (int)(at % ntn), bm = (int)(at / ntn);
-    }
+    const int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
     const int n0 = bn * TN, m0 = GROUPED ? 0 : bm * TM;
     Gather g = {};
     if constexpr (GROUPED) {
-        const int4 t = reinterpret_cast<const int4 *>(ga.plan + ga.tiles_at)[bm];
-        if ((unsigned)t.x >= (unsigned)ga.E || t.y < 0 || t.z < 1 || t.z > TM || t.y > ga.pairs - t.z)
-            return; // no plan of these pairs
+        const int2 t = *reinterpret_cast<const int2 *>(ga.plan + experts_tile_at(bm));
+        g = {ga.plan + experts_pairs_at(ga.max_tiles, bm, TM), (uint32_t)ga.per_row, (uint32_t)ga.pairs};
+        M = min(t.y, TM);
+        if ((unsigned)t.x >= (unsigned)ga.E || M < 1)
+            return; // no tile, or no plan of these pairs
         W += t.x * ga.expert_bytes;
-        M = t.z;
-        g = {ga.plan + experts_order_at() + t.y, (uint32_t)ga.per_row, (uint32_t)ga.pairs};
     }
     const int64_t rowcode = FMT == LB_Q1_0 ? K / 8 : FMT == LB_Q8_0 ? K : FMT == LB_Q4_0 ? K / 2 : K / 4; // code bytes per weight row
     const int nab = K / QK8;                                                  // activation blocks per row
@@ -637,8 +632,8 @@ hipError_t launch_fmt(const uint8_t *W, int64_t N, int64_t K, float w_scale, con
 template <int FMT> hipError_t launch_experts_fmt(const ExpertsArgs &a, hipStream_t s)
 {
     const int64_t ntn = (a.N + TN - 1) / TN;
-    const GroupArgs ga = {a.expert_bytes, experts_tiles_at(a.pairs), a.max_tiles, a.plan, a.E, a.pairs, a.per_row};
-    hipLaunchKernelGGL((gemm_kernel<FMT, false, 1, true>), dim3((unsigned)((ntn * a.max_tiles + 7) / 8 * 8)), dim3(GT), 0, s, a.W, a.N, a.K, 1.0f, a.xq, a.xs,
+    const GroupArgs ga = {a.expert_bytes, a.max_tiles, a.plan, a.E, a.pairs, a.per_row};
+    hipLaunchKernelGGL((gemm_kernel<FMT, false, 1, true>), dim3((unsigned)(ntn * a.max_tiles)), dim3(GT), 0, s, a.W, a.N, a.K, 1.0f, a.xq, a.xs,
                        0, a.y, nullptr, (int)ntn, ga);
     return hipGetLastError();
 }

@@ -122,20 +122,13 @@ struct RouteArgs {
 };
 hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
 
-// The routed pairs by expert (include/lowbit.h, lowbit_experts_plan): int32 words
-//   [0] tiles, [1] routed pairs, [2], [3] unused; order [pairs, rounded up to 4]; tiles {expert, first place in order, rows, 0}
-// A tile is at most experts_tile_rows() pairs of one expert, and may be empty (rows 0).
-inline __host__ __device__ int64_t experts_order_at() { return 4; }
-inline __host__ __device__ int64_t experts_tiles_at(int64_t pairs) { return 4 + (pairs + 3) / 4 * 4; }
-// The workgroup's place in a grid of tiles x chunks of weight rows, -1 for none.  Workgroups go to the eight XCDs in turn:
-// each XCD takes one eighth of the places, one after another, so that the tiles of an expert, which read the same weights,
-// meet in one L2.
-inline __device__ int64_t experts_block(int tiles, int chunks)
-{
-    const int64_t all = (int64_t)max(tiles, 0) * chunks, share = (all + 7) / 8;
-    const int64_t i = blockIdx.x / 8, at = (blockIdx.x % 8) * share + i;
-    return i < share && at < all ? at : -1;
-}
+// The routed pairs by expert (include/lowbit.h, lowbit_experts_plan), in tiles of R = experts_tile_rows() places, of one
+// expert each.  int32 words, for `tiles` = experts_max_tiles():
+//   [0] tiles in use, [1] routed pairs, [2], [3] unused; {expert, rows} [tiles]; pairs [tiles][R]
+// A tile may have no rows (those past the last in use, and others); places behind a tile's rows hold -1.  A tile's entry and
+// its pairs are at addresses of the tile's number alone, so that neither waits for the other.
+inline __host__ __device__ int64_t experts_tile_at(int64_t tile) { return 4 + 2 * tile; }
+inline __host__ __device__ int64_t experts_pairs_at(int64_t tiles, int64_t tile, int64_t rows) { return 4 + (2 * tiles + 3) / 4 * 4 + tile * rows; }
 int64_t experts_tile_rows(int64_t pairs, int64_t E);
 int64_t experts_max_tiles(int64_t pairs, int64_t E);
 

@@ -94,17 +94,19 @@ def test_plan(pairs, E):
         ok = (which >= 0) & (which < E)
         want = np.argsort(np.where(ok, which, E), kind="stable")[:ok.sum()]
         assert p[1] == ok.sum()
-        assert np.array_equal(p[4:4 + p[1]], want)
-        tiles = p[4 + (pairs + 3) // 4 * 4:].reshape(-1, 4)[:p[0]]
-        tiles = tiles[tiles[:, 2] != 0]  # some may be empty
+        size = 128 if pairs >= 96 * E else 16
+        n = pairs // size + min(pairs, E)
+        tiles, places = p[4:4 + 2 * n].reshape(-1, 2), p[4 + (2 * n + 3) // 4 * 4:][:n * size].reshape(n, size)
+        assert (tiles[p[0]:, 1] == 0).all() and (tiles[:, 1] >= 0).all()
         at = 0
-        for x, first, rows, _ in tiles:  # they cover the order one after another
-            assert first == at and rows > 0 and (which[want[at:at + rows]] == x).all()
-            at += rows
+        for (x, rows), pair in zip(tiles, places):
+            if rows:  # they cover the order one after another
+                assert np.array_equal(pair[:rows], want[at:at + rows]) and (which[pair[:rows]] == x).all() and (pair[rows:] == -1).all()
+                at += rows
         assert at == p[1]
-        size = tiles[:, 2].max() if len(tiles) else 0
-        for a, b in zip(tiles, tiles[1:]):  # and are full but for each expert's last
-            assert a[0] != b[0] or a[2] == size
+        used = tiles[tiles[:, 1] != 0]
+        for a, b in zip(used, used[1:]):  # and are full but for each expert's last
+            assert a[0] != b[0] or a[1] == size
 
 
 class Layer:
