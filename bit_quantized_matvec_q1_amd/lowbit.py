@@ -24,6 +24,10 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built (python -m bit_quantized_matvec_q1_amd.build); "
                       "the HIP library is the only implementation of this package")
 
+_Tensor = torch.Tensor
+# the current stream's handle without a stream object about it, where this torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
 _P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
 lib = ctypes.CDLL(LIB_PATH)
@@ -132,6 +136,15 @@ def _check_arg(t, name, count, dtypes=None):
 def _args(*specs):
     """Addresses of the arguments (t, name, count[, dtypes]) after checking every one of them: all sizes and
     dtypes first, then the device and layout checks of _ptr."""
+    ptrs = []
+    for spec in specs:  # all in order, as nearly always: one look at each
+        t = spec[0]
+        if not (isinstance(t, _Tensor) and (t.numel() >= spec[2] and t.dtype in spec[3] if len(spec) == 4 else t.nbytes >= spec[2])
+                and t.is_cuda and t.is_contiguous()):
+            break
+        ptrs.append(t.data_ptr())
+    else:
+        return ptrs
     for spec in specs:
         _check_arg(*spec)
     return [_ptr(spec[0]) for spec in specs]
@@ -163,7 +176,7 @@ def _stream(stream, *tensors):
         return stream if isinstance(stream, int) else stream.cuda_stream
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return _raw_stream(t.get_device())
     return None
 
 
@@ -254,20 +267,18 @@ def lowbit_read_probe(buf, nbytes, sink, stream=None):
 
 _DTYPES = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
 _I32, _I64T, _F32T = torch.int32, torch.int64, torch.float32
-_Tensor = torch.Tensor
-# the current stream's handle without a stream object about it, where this torch has the call
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # (only asked with a tensor on one)
 
 
 def _call(name, fn, stream, tensors, args):
     """fn(*args, stream) on the device of `tensors`, which all of them have to share, whatever the current one is."""
-    dev = -1
+    dev = -2  # none yet; a host tensor's is -1
     for t in tensors:
         if isinstance(t, _Tensor):
-            if not t.is_cuda:
-                raise ValueError(f"device tensor required, got one on {t.device}")
             i = t.get_device()
             if i != dev:
+                if not t.is_cuda:
+                    raise ValueError(f"device tensor required, got one on {t.device}")
                 if dev >= 0:
                     raise ValueError(f"tensors on cuda:{dev} and cuda:{i}: one device required")
                 dev = i
@@ -275,7 +286,7 @@ def _call(name, fn, stream, tensors, args):
         stream = _raw_stream(dev) if dev >= 0 else None
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev < 0 or dev == _current_device():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -287,9 +298,12 @@ def _call(name, fn, stream, tensors, args):
 def _flat(t, name, count, dtype):
     """The address of a dense argument of at least `count` elements (its device is checked by _call); None and
     addresses pass through.  dtype None: `count` bytes of any type."""
-    if t is None or isinstance(t, int):
+    if isinstance(t, _Tensor):
+        if (t.dtype is dtype and t.numel() >= count if dtype is not None else t.nbytes >= count) and t.is_contiguous():
+            return t.data_ptr()
+    elif t is None or isinstance(t, int):
         return t
-    if not isinstance(t, _Tensor):
+    else:
         raise ValueError(f"{name}: a torch tensor, an int address or None is required")
     if dtype is None:
         have = t.numel() * t.element_size()
