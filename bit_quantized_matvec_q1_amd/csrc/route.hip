@@ -6,62 +6,127 @@
 // sums and comparisons are in 64 bits (the hardware's fp64 rate is its fp32 rate without packing), and equal values go to
 // the lowest index.
 //
-// A wave takes one token, lane l the experts l, l + 64, ... .  A choice is one maximum over the wave by DPP (an instruction
-// and two moves a step), found again by comparing: the first element number with a lane that has it, and of those the
-// lowest lane, is the lowest index.
+// A token has LT lanes, 32 or a whole wave, lane l the experts l, l + LT, ... .  A choice is one maximum over the lanes
+// (DPP within rows of 16, row swaps across them: an instruction and two moves a step), and a minimum of the indexes of
+// those that have it.  What it takes is instructions, and nearly as many for 32 lanes as for 64: so long batches put two
+// tokens in a wave, and short ones, where a single token's time counts, one.
 #include "serve_internal.h"
 
 namespace lb {
 
 namespace {
 
-constexpr int WAVES = 4; // tokens a workgroup
+constexpr int WAVES = 4; // a workgroup
 
-template <int CTRL, int ROWS> __device__ __forceinline__ double dpp(double v, double fill)
-{
-    const uint64_t b = __double_as_longlong(v), f = __double_as_longlong(fill);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)f, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(f >> 32), (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
-    return __longlong_as_double((uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double lane_of(double v, int l) // l uniform
+template <int CTRL> __device__ __forceinline__ double dpp(double v)
 {
     const uint64_t b = __double_as_longlong(v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
     return __longlong_as_double((uint64_t)hi << 32 | lo);
 }
-// over the wave, in every lane; no NaN among them
-__device__ __forceinline__ double wave_max(double v)
+struct Both {
+    double a, b;
+};
+// v of the even and of the odd row of 16 of each two (ROW), or of the lower and upper 32 lanes, in both of them
+template <bool ROW> __device__ __forceinline__ Both halves(double v)
 {
-    v = fmax(v, dpp<0xB1, 0xF>(v, v));  // quad_perm [1,0,3,2]
-    v = fmax(v, dpp<0x4E, 0xF>(v, v));  // quad_perm [2,3,0,1]
-    v = fmax(v, dpp<0x141, 0xF>(v, v)); // row_half_mirror
-    v = fmax(v, dpp<0x140, 0xF>(v, v)); // row_mirror
-    v = fmax(v, dpp<0x142, 0xA>(v, v)); // row_bcast:15 into rows 1, 3
-    v = fmax(v, dpp<0x143, 0xC>(v, v)); // row_bcast:31 into rows 2, 3
-    return lane_of(v, 63);
+    const uint64_t x = __double_as_longlong(v);
+    const uint32_t lo = (uint32_t)x, hi = (uint32_t)(x >> 32);
+    const auto p = ROW ? __builtin_amdgcn_permlane16_swap(lo, lo, false, false) : __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto q = ROW ? __builtin_amdgcn_permlane16_swap(hi, hi, false, false) : __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    return {__longlong_as_double((uint64_t)(uint32_t)q[0] << 32 | (uint32_t)p[0]), __longlong_as_double((uint64_t)(uint32_t)q[1] << 32 | (uint32_t)p[1])};
 }
-__device__ __forceinline__ double wave_sum(double v)
+// The maximum, as one instruction (fmax makes its operands canonical first, an instruction each; there is no NaN here).
+__device__ __forceinline__ double dmax(double a, double b)
 {
-    v += dpp<0xB1, 0xF>(v, 0.0);
-    v += dpp<0x4E, 0xF>(v, 0.0);
-    v += dpp<0x141, 0xF>(v, 0.0);
-    v += dpp<0x140, 0xF>(v, 0.0);
-    v += dpp<0x142, 0xA>(v, 0.0);
-    v += dpp<0x143, 0xC>(v, 0.0);
-    return lane_of(v, 63);
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// e^a for a <= 0: a = n ln 2 + r, |r| <= ln 2 / 2, with ln 2 as a sum of two, and the Taylor series of e^r, whose next term
+// is below 2^-57; 0 below the smallest number.
+__device__ __forceinline__ double exp_down(double a)
+{
+    a = dmax(a, -800.0);
+    const double n = rint(a * 0x1.71547652b82fep0);                             // 1 / ln 2
+    const double r = fma(-n, 0x1.abc9e3b39803fp-56, fma(-n, 0x1.62e42fefa39efp-1, a)); // ln 2
+    double e = 1.0 / 6227020800.0; // 13!
+    e = fma(e, r, 1.0 / 479001600.0);
+    e = fma(e, r, 1.0 / 39916800.0);
+    e = fma(e, r, 1.0 / 3628800.0);
+    e = fma(e, r, 1.0 / 362880.0);
+    e = fma(e, r, 1.0 / 40320.0);
+    e = fma(e, r, 1.0 / 5040.0);
+    e = fma(e, r, 1.0 / 720.0);
+    e = fma(e, r, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return ldexp(e, (int)n);
+}
+// 1 / (1 + e^-x): with e = e^-|x| <= 1, 1 / (1 + e) or e / (1 + e), the reciprocal by Newton's steps
+__device__ __forceinline__ double sigmoid(double x)
+{
+    const double e = exp_down(-fabs(x)), d = 1.0 + e;
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.0), r, r);
+    r = fma(fma(-d, r, 1.0), r, r);
+    return x >= 0.0 ? r : e * r;
+}
+
+// f over a token's LT lanes, in all of them
+template <int LT, typename Op> __device__ __forceinline__ double over_lanes(double v, Op &&f)
+{
+    v = f(v, dpp<0xB1>(v));  // quad_perm [1,0,3,2]
+    v = f(v, dpp<0x4E>(v));  // quad_perm [2,3,0,1]
+    v = f(v, dpp<0x141>(v)); // row_half_mirror
+    v = f(v, dpp<0x140>(v)); // row_mirror
+    Both o = halves<true>(v);
+    v = f(o.a, o.b);
+    if (LT == 64) {
+        o = halves<false>(v);
+        v = f(o.a, o.b);
+    }
+    return v;
+}
+template <int LT> __device__ __forceinline__ double lanes_max(double v) // no NaN among them
+{
+    return over_lanes<LT>(v, [](double a, double b) { return dmax(a, b); });
+}
+template <int LT> __device__ __forceinline__ double lanes_sum(double v)
+{
+    return over_lanes<LT>(v, [](double a, double b) { return a + b; });
+}
+template <int LT> __device__ __forceinline__ uint32_t lanes_min(uint32_t v)
+{
+    v = min(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+    v = min(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+    v = min(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+    v = min(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+    auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = min((uint32_t)p[0], (uint32_t)p[1]);
+    if (LT == 64) {
+        p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = min((uint32_t)p[0], (uint32_t)p[1]);
+    }
+    return v;
 }
 
 // An allowed expert's value is at least LEAST, one that is taken or not allowed -inf.
 constexpr double LEAST = -1.7976931348623157e308;
 __device__ __forceinline__ double value_of(double v) { return v >= LEAST ? v : LEAST; } // a NaN and -inf count least
 
-template <int DT, int NE> __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
+template <int DT, int LT, int NE> __global__ __launch_bounds__(64 * WAVES) void route_kernel(RouteArgs a)
 {
     using R = RowType<DT>;
-    extern __shared__ double shared[]; // [WAVES][E], where there are groups
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = (int)a.E, k = (int)a.top_k;
-    const int64_t t = (int64_t)blockIdx.x * WAVES + wave;
+    extern __shared__ double shared[]; // [tokens][E] scores, then the values they are ordered by, where there are groups
+    constexpr int TOKENS = 64 / LT * WAVES;
+    const int lane = threadIdx.x % LT, local = threadIdx.x / LT, E = (int)a.E, k = (int)a.top_k;
+    const int64_t t = (int64_t)blockIdx.x * TOKENS + local;
     const bool grouped = a.groups > 1; // uniform
     const bool live = t < a.T && (!a.count || t < (int64_t)a.count[0]);
     const double NONE = -__builtin_inf();
@@ -70,7 +135,7 @@ template <int DT, int NE> __global__ __launch_bounds__(64 * WAVES) void route_ke
     float x[NE];
 #pragma unroll
     for (int i = 0; i < NE; i++) {
-        const int e = i * 64 + lane;
+        const int e = i * LT + lane;
         x[i] = -__builtin_inff();
         if (live && e < E) {
             const float v = R::get(static_cast<const typename R::T *>(a.logits)[t * a.stride + e]);
@@ -80,41 +145,44 @@ template <int DT, int NE> __global__ __launch_bounds__(64 * WAVES) void route_ke
     if (a.sigmoid) { // uniform
 #pragma unroll
         for (int i = 0; i < NE; i++)
-            p[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+            p[i] = sigmoid((double)x[i]);
     } else {
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < NE; i++)
             m = fmaxf(m, x[i]);
-        const double top = wave_max((double)m);
+        const double top = lanes_max<LT>((double)m);
         double z = 0.0;
 #pragma unroll
         for (int i = 0; i < NE; i++) { // (the largest is 1 also where it is infinite)
-            p[i] = i * 64 + lane < E ? ((double)x[i] == top ? 1.0 : exp((double)x[i] - top)) : 0.0;
+            p[i] = i * LT + lane < E ? ((double)x[i] == top ? 1.0 : exp_down((double)x[i] - top)) : 0.0;
             z += p[i];
         }
-        z = wave_sum(z);
+        z = 1.0 / lanes_sum<LT>(z);
 #pragma unroll
         for (int i = 0; i < NE; i++)
-            p[i] /= z;
+            p[i] *= z;
     }
+    double *scores = shared + local * E;
 #pragma unroll
     for (int i = 0; i < NE; i++) {
-        const int e = i * 64 + lane;
+        const int e = i * LT + lane;
         sel[i] = e < E ? value_of(a.bias ? p[i] + (double)a.bias[e] : p[i]) : NONE;
+        if (e < E)
+            scores[e] = p[i];
     }
 
     if (grouped) {
-        double *mine = shared + wave * E;
+        double *mine = shared + (TOKENS + local) * E;
 #pragma unroll
         for (int i = 0; i < NE; i++)
-            if (i * 64 + lane < E)
-                mine[i * 64 + lane] = sel[i];
+            if (i * LT + lane < E)
+                mine[i * LT + lane] = sel[i];
         __syncthreads();
         // `each` lanes a group (a power of two), which look through its experts in turn
         const int groups = (int)a.groups, size = E / groups;
         int each = 1;
-        while (2 * each * groups <= 64)
+        while (2 * each * groups <= LT)
             each *= 2;
         const int g = lane / each;
         double m1 = LEAST, m2 = LEAST; // the best two
@@ -130,71 +198,82 @@ template <int DT, int NE> __global__ __launch_bounds__(64 * WAVES) void route_ke
             m1 = fmax(m1, o1);
         }
         double gs = value_of(a.best == 2 && size > 1 ? m1 + m2 : m1);
-        gs = __shfl(gs, min(lane * each, 63)); // group l in lane l
+        gs = __shfl(gs, min(lane * each, LT - 1), LT); // group l in lane l
         gs = lane < groups ? gs : NONE;
         uint64_t kept = 0;
         for (int r = 0; r < (int)a.kept; r++) {
-            const uint64_t at = __ballot(gs == wave_max(gs)) & (groups < 64 ? ((uint64_t)1 << groups) - 1 : ~(uint64_t)0);
-            const int best = __ffsll((unsigned long long)at) - 1;
+            const double m = lanes_max<LT>(gs);
+            const int best = (int)lanes_min<LT>(lane < groups && gs == m ? (uint32_t)lane : 63u);
             kept |= (uint64_t)1 << best;
             gs = lane == best ? NONE : gs;
         }
+        // e / size: (e + 1/2) / size is 2^-11 or more from a whole number, and the quotient below 64 off by less than 2^-16
+        const float part = 1.0f / (float)size;
 #pragma unroll
         for (int i = 0; i < NE; i++) {
-            const int e = i * 64 + lane;
-            if (e < E && !(kept >> (e / size) & 1))
+            const int e = i * LT + lane, in = (int)(((float)e + 0.5f) * part);
+            if (e < E && !(kept >> in & 1))
                 sel[i] = NONE;
         }
     }
 
-    double weight = 0.0; // choice j in lane j
-    int chosen = -1;
+    uint32_t mine[2] = {0, 0}; // choices `lane` and LT + `lane`
     for (int j = 0; j < k; j++) {
         double m = sel[0];
 #pragma unroll
         for (int i = 1; i < NE; i++)
-            m = fmax(m, sel[i]);
-        m = wave_max(m);
-        bool found = false;
+            m = dmax(m, sel[i]);
+        m = lanes_max<LT>(m);
+        uint32_t at = ~0u;
 #pragma unroll
-        for (int i = 0; i < NE; i++) {
-            const uint64_t at = found ? 0 : __ballot(sel[i] == m);
-            if (at) { // uniform
-                found = true;
-                const int l = __ffsll((unsigned long long)at) - 1;
-                const double w = lane_of(p[i], l);
-                weight = lane == j ? w : weight;
-                chosen = lane == j ? i * 64 + l : chosen;
-                sel[i] = lane == l ? NONE : sel[i];
-            }
+        for (int i = NE - 1; i >= 0; i--)
+            at = sel[i] == m ? (uint32_t)(i * LT + lane) : at;
+        at = lanes_min<LT>(at);
+#pragma unroll
+        for (int i = 0; i < NE; i++)
+            sel[i] = at == (uint32_t)(i * LT + lane) ? NONE : sel[i];
+        mine[0] = j == lane ? at : mine[0];
+        if (LT == 32)
+            mine[1] = j == LT + lane ? at : mine[1];
+    }
+    __syncthreads(); // the scores are in place
+    double w[2] = {0.0, 0.0};
+#pragma unroll
+    for (int h = 0; h < 64 / LT; h++)
+        if (h * LT + lane < k)
+            w[h] = scores[min(mine[h], (uint32_t)(E - 1))];
+    if (a.renormalise) {
+        const double z = lanes_sum<LT>(w[0] + w[1]);
+        w[0] = z > 0.0 ? w[0] / z : 0.0, w[1] = z > 0.0 ? w[1] / z : 0.0;
+    }
+#pragma unroll
+    for (int h = 0; h < 64 / LT; h++) {
+        const int j = h * LT + lane;
+        if (t < a.T && j < k) {
+            a.experts[t * k + j] = live ? (int32_t)mine[h] : -1;
+            a.weights[t * k + j] = live ? (float)(w[h] * (double)a.factor) : 0.0f;
         }
     }
-    if (a.renormalise) {
-        const double z = wave_sum(lane < k ? weight : 0.0);
-        weight = z > 0.0 ? weight / z : 0.0;
-    }
-    if (t < a.T && lane < k) {
-        a.experts[t * k + lane] = live ? chosen : -1;
-        a.weights[t * k + lane] = live ? (float)(weight * (double)a.factor) : 0.0f;
-    }
+}
+
+template <int DT, int LT, int NE> hipError_t route_n(const RouteArgs &a, hipStream_t s)
+{
+    constexpr int TOKENS = 64 / LT * WAVES;
+    const size_t lds = (size_t)a.E * TOKENS * sizeof(double) * (a.groups > 1 ? 2 : 1);
+    hipLaunchKernelGGL((route_kernel<DT, LT, NE>), dim3((unsigned)((a.T + TOKENS - 1) / TOKENS)), dim3(64 * WAVES), lds, s, a);
+    return hipGetLastError();
 }
 
 template <int DT> hipError_t route_d(const RouteArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.T + WAVES - 1) / WAVES)), block(64 * WAVES);
-    const size_t lds = a.groups > 1 ? (size_t)a.E * WAVES * sizeof(double) : 0;
-    const int n = (int)((a.E + 63) / 64);
-    if (n <= 1)
-        hipLaunchKernelGGL((route_kernel<DT, 1>), grid, block, lds, s, a);
-    else if (n <= 2)
-        hipLaunchKernelGGL((route_kernel<DT, 2>), grid, block, lds, s, a);
-    else if (n <= 4)
-        hipLaunchKernelGGL((route_kernel<DT, 4>), grid, block, lds, s, a);
-    else if (n <= 8)
-        hipLaunchKernelGGL((route_kernel<DT, 8>), grid, block, lds, s, a);
-    else
-        hipLaunchKernelGGL((route_kernel<DT, 16>), grid, block, lds, s, a);
-    return hipGetLastError();
+    // two tokens a wave from 1024 tokens on, where their experts are at most eight a lane
+    if (a.T >= 1024 && a.E <= 256 && a.groups <= 32)
+        return a.E <= 32 ? route_n<DT, 32, 1>(a, s) : a.E <= 64 ? route_n<DT, 32, 2>(a, s) : a.E <= 128 ? route_n<DT, 32, 4>(a, s) : route_n<DT, 32, 8>(a, s);
+    return a.E <= 64    ? route_n<DT, 64, 1>(a, s)
+           : a.E <= 128 ? route_n<DT, 64, 2>(a, s)
+           : a.E <= 256 ? route_n<DT, 64, 4>(a, s)
+           : a.E <= 512 ? route_n<DT, 64, 8>(a, s)
+                        : route_n<DT, 64, 16>(a, s);
 }
 
 } // namespace

@@ -93,7 +93,8 @@ def test_binding_checks_extents():
     (33, 60, 4, False, True, 4, 2, 1, True), (130, 256, 8, True, True, 8, 4, 2, True), (7, 384, 10, True, True, 1, 1, 1, True),
     (9, 160, 6, False, False, 8, 3, 1, False), (6, 1024, 64, False, True, 64, 40, 2, True), (4, 1000, 33, True, False, 5, 5, 2, True),
     (11, 128, 2, True, True, 64, 1, 2, True), (12, 96, 3, False, False, 32, 1, 2, True), (3, 65, 65 - 1, True, True, 1, 1, 1, True),
-    (2049, 512, 8, False, False, 1, 1, 1, True)])
+    (2049, 512, 8, False, False, 1, 1, 1, True), (1025, 64, 8, False, True, 1, 1, 1, True), (1500, 256, 8, True, True, 8, 4, 2, True),
+    (1027, 20, 5, True, False, 5, 2, 1, False), (1024, 128, 40, False, False, 32, 16, 2, True), (1100, 256, 64, True, True, 1, 1, 1, True)])
 def test_choices_and_weights(kind, T, E, k, sigmoid, bias, groups, kept, best, renorm):
     say(f"case route {kind} T={T} E={E} k={k} sigmoid={sigmoid} groups={groups}/{kept}")
     rng = np.random.default_rng(E + k)
@@ -108,7 +109,7 @@ def test_choices_and_weights(kind, T, E, k, sigmoid, bias, groups, kept, best, r
 def test_ties_go_to_the_lowest_index(sigmoid, groups, kept, best):
     say(f"case route ties sigmoid={sigmoid} groups={groups}")
     rng = np.random.default_rng(8)
-    x = torch.from_numpy(rng.integers(-1, 2, (40, 200)).astype(np.float32))
+    x = torch.from_numpy(rng.integers(-1, 2, (1040 if groups == 4 else 40, 200)).astype(np.float32))
     x[0] = 0
     x[1, 100:] = 5
     check(x, "f32", 12, sigmoid, None, groups, kept, best)
