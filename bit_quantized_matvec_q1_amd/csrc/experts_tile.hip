@@ -15,7 +15,12 @@
 //  * Results are read as fp32 through the bias 1.5 * 2^23 as in gemm.hip: round(d_x * isum), then one multiply-add with the
 //    weight scale (one value a lane).
 // A wave has G groups of 16 weight rows, so that what it reads from LDS (activations, scales, accumulator starts) is read
-// once for all of them.
+// once for all of them.  lowbit_gemm takes the same kernel for Q4_0 products of few rows, whose tiles need no plan.
+//
+// What bounds it: HBM, or the cache, while experts have few rows (512 pairs of 128 Q4_0 experts of 2048 x 768, 113 MB: 28 us,
+// 4.1 TB/s), the vector unit with many (12 to 14 instructions for eight weights of a lane and 16 rows, eight of them the
+// rescale).  Two things made it: each row's scales staged through LDS by whole lines (read four at a time from memory, their
+// lines came through the caches again for every step, Q4_0 875 -> 577 us for 32768 pairs), and results in vector registers.
 #include "matvec_tile.h"
 #include "serve_internal.h"
 
@@ -24,7 +29,6 @@ namespace lb {
 namespace {
 
 constexpr int TR = 16;   // activation rows a tile
-constexpr int G = 2;     // groups of 16 weight rows a wave
 constexpr int KC = 1024; // columns staged at a time: 20 KiB of LDS, and 2 to 9 of weight scales
 constexpr uint32_t BIAS = 0x4B400000u; // 1.5 * 2^23 as fp32 bits
 constexpr float BIASF = 12582912.0f;
@@ -33,8 +37,8 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef unsigned v2u_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef __attribute__((address_space(1))) const v2u_a2 gv2u_a2;
 
-template <int FMT> struct __attribute__((aligned(16))) TileLds {
-    static constexpr int BLOCKS = KC / QK8, RECORDS = KC / F<FMT>::SW, WROWS = 64 * G;
+template <int FMT, int G, bool KS> struct __attribute__((aligned(16))) TileLds {
+    static constexpr int BLOCKS = KC / QK8, RECORDS = KC / F<FMT>::SW, WROWS = (KS ? 16 : 64) * G;
     // a weight row's scales of the chunk, 8 bytes apart from the next row's (16 rows' reads of 8 bytes meet 16 pairs of banks)
     static constexpr int SCALES = RECORDS + 4;
     uint32_t x[KC * TR / 4]; // Q4_0, Q1_0: [block][q][row] 8 bytes; Q2_0_g64: [record][q][row] 16 bytes
@@ -70,7 +74,7 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&d)[4])
 }
 
 // Block b (32 columns from column 32 b of the chunk) of activation row r: 32 bytes and their scale.
-template <int FMT> __device__ __forceinline__ void stage_block(TileLds<FMT> &lds, int b, int r, uint4 lo, uint4 hi, float dx)
+template <int FMT, typename Lds> __device__ __forceinline__ void stage_block(Lds &lds, int b, int r, uint4 lo, uint4 hi, float dx)
 {
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     if (FMT == LB_Q2_0_G64) { // weights 16 q + 4 t + s at byte t of dword s
@@ -101,19 +105,21 @@ template <int FMT> __device__ __forceinline__ void stage_block(TileLds<FMT> &lds
 
 // (Two waves a SIMD at the least: with 256 registers the matrix products' results are in vector registers; with more the
 // compiler has them in accumulator registers, which costs a move each.)
-template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_tile_kernel(ExpertsArgs a, int chunks)
+template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 2) void experts_tile_kernel(ExpertsArgs a, int chunks)
 {
-    using Lds = TileLds<FMT>;
+    using Lds = TileLds<FMT, G, KS>;
     __shared__ Lds lds;
     constexpr int BPR = F<FMT>::SW / QK8; // q8_0 blocks a record
     const int chunk = blockIdx.x % chunks, tile = blockIdx.x / chunks;
-    const int2 t = *reinterpret_cast<const int2 *>(a.plan + experts_tile_at(tile));
-    const int32_t *pairs = a.plan + experts_pairs_at(a.max_tiles, tile, TR);
+    // without a plan the rows are those of one matrix product, one after another
+    const int2 t = a.plan ? *reinterpret_cast<const int2 *>(a.plan + experts_tile_at(tile)) : make_int2(0, a.pairs - TR * tile);
+    const int32_t *pairs = a.plan ? a.plan + experts_pairs_at(a.max_tiles, tile, TR) : nullptr;
+    auto pair_at = [&](int r) { return min(pairs ? (uint32_t)pairs[r] : (uint32_t)(TR * tile + r), (uint32_t)(a.pairs - 1)); };
     // staging: a thread has blocks tid / TR, and so on by 256 / TR, of activation row tid mod TR (a place without a pair reads
     // some row, and is not stored)
     constexpr int BSTEP = WG / TR, U = Lds::BLOCKS / BSTEP;
     const int sr = threadIdx.x % TR, sb = threadIdx.x / TR;
-    const int64_t row = min((uint32_t)pairs[sr], (uint32_t)(a.pairs - 1)) / (uint32_t)a.per_row;
+    const int64_t row = pair_at(sr) / (uint32_t)a.per_row;
     const int rows = min(t.y, TR);
     if ((unsigned)t.x >= (unsigned)a.E || rows < 1)
         return; // no tile, or no plan of these pairs
@@ -121,7 +127,8 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
     const int ns = a.K / F<FMT>::SW;
     const uint8_t *scales = W + (int64_t)a.N * ns * CODE_BYTES;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-    const int n0 = (chunk * (WG / 64) + wave) * G * 16 + (lane & 15); // this lane's weight row in group 0
+    const int wrow = (KS ? 0 : wave * G * 16) + (lane & 15); // this lane's weight row of the workgroup's, in group 0
+    const int n0 = chunk * Lds::WROWS + wrow;
     if (threadIdx.x == 0)
         lds.zero = make_uint4(0, 0, 0, 0);
 
@@ -150,7 +157,7 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
         uint2 sc[G];
 #pragma unroll
         for (int g = 0; g < G; g++) {
-            sc[g] = *reinterpret_cast<const uint2 *>(lds.dw + (wave * G * 16 + g * 16 + (lane & 15)) * Lds::SCALES + (4 * s - first));
+            sc[g] = *reinterpret_cast<const uint2 *>(lds.dw + (wrow + g * 16) * Lds::SCALES + (4 * s - first));
             d[g][0] = code[g].x, d[g][1] = code[g].y, d[g][2] = code[g].z, d[g][3] = code[g].w;
             transpose_quarters(d[g]);
         }
@@ -269,46 +276,86 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
     };
     const int steps = (ns + 4 * H - 1) / (4 * H);
     constexpr int SPC = Lds::RECORDS / (4 * H); // steps a chunk
+    auto stage_chunk = [&](int k0) { // the loaded one, from column k0; then the next one's loads go out
+        const int nblk = min(Lds::BLOCKS, (a.K - k0) / QK8);
+        if (k0)
+            chunk_barrier(); // every wave has read the chunk before
+#pragma unroll
+        for (int v = 0; v < U; v++)
+            if (sb + BSTEP * v < nblk)
+                stage_block<FMT>(lds, sb + BSTEP * v, sr, lo[v], hi[v], half_bits_to_float((uint16_t)sc[v]));
+#pragma unroll
+        for (int v = 0; v < P; v++) {
+            const int p = threadIdx.x + v * WG;
+            if (PIECES % WG == 0 || p < PIECES) {
+                uint2 *to = reinterpret_cast<uint2 *>(lds.dw + p / PARTS * Lds::SCALES + p % PARTS * 8);
+                to[0] = make_uint2(dws[v].x, dws[v].y), to[1] = make_uint2(dws[v].z, dws[v].w);
+            }
+        }
+        if (k0 + KC < a.K) // uniform
+            load_chunk(k0 + KC);
+        chunk_barrier();
+    };
+    auto step = [&](const Regs &r, int s, int first) {
+#pragma unroll
+        for (int h = 0; h < H; h++)
+            if (h == 0 || 4 * (H * s + h) < ns) // uniform
+                compute(r.code[h], H * s + h, first);
+    };
     Regs buf[2];
     load_chunk(0);
-    issue(buf[0], 0);
-    for (int s = 0; s < steps; s += 2) {
+    if constexpr (KS) {
+        // the waves have the same weight rows and a step of every chunk each, and add up what they have at the end
+        const int mine = min(wave, SPC - 1), chunks_k = (steps + SPC - 1) / SPC;
+        issue(buf[0], min(mine, steps - 1));
+        for (int c = 0; c < chunks_k; c += 2) {
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            if (s + u >= steps) // uniform
-                break;
-            if (u % SPC == 0 && (s + u) % SPC == 0) { // uniform: the next chunk
-                const int k0 = (s + u) * 4 * H * F<FMT>::SW, nblk = min(Lds::BLOCKS, (a.K - k0) / QK8);
-                if (s + u)
-                    chunk_barrier(); // every wave has read the chunk before
-#pragma unroll
-                for (int v = 0; v < U; v++)
-                    if (sb + BSTEP * v < nblk)
-                        stage_block<FMT>(lds, sb + BSTEP * v, sr, lo[v], hi[v], half_bits_to_float((uint16_t)sc[v]));
-#pragma unroll
-                for (int v = 0; v < P; v++) {
-                    const int p = threadIdx.x + v * WG;
-                    if (PIECES % WG == 0 || p < PIECES) {
-                        uint2 *to = reinterpret_cast<uint2 *>(lds.dw + p / PARTS * Lds::SCALES + p % PARTS * 8);
-                        to[0] = make_uint2(dws[v].x, dws[v].y), to[1] = make_uint2(dws[v].z, dws[v].w);
-                    }
-                }
-                if (k0 + KC < a.K) // uniform
-                    load_chunk(k0 + KC);
-                chunk_barrier();
+            for (int u = 0; u < 2; u++) {
+                if (c + u >= chunks_k) // uniform
+                    break;
+                stage_chunk((c + u) * KC);
+                issue(buf[1 - u], min((c + u + 1) * SPC + mine, steps - 1));
+                __builtin_amdgcn_sched_barrier(0); // these loads go out before this step's arithmetic
+                if (wave < SPC && (c + u) * SPC + wave < steps) // uniform in the wave
+                    step(buf[u], (c + u) * SPC + wave, (c + u) * Lds::RECORDS);
             }
-            issue(buf[1 - u], min(s + u + 1, steps - 1));
-            __builtin_amdgcn_sched_barrier(0); // these loads go out before this step's arithmetic
+        }
+        chunk_barrier();
+        float *sums = reinterpret_cast<float *>(lds.x); // [wave][group][4][lane]
+        static_assert(sizeof(lds.x) >= 4 * (WG / 64) * G * 4 * 64, "the waves' sums");
 #pragma unroll
-            for (int h = 0; h < H; h++)
-                if (h == 0 || 4 * (H * (s + u) + h) < ns) // uniform
-                    compute(buf[u].code[h], H * (s + u) + h, (s + u) / SPC * SPC * 4 * H);
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                sums[((wave * G + g) * 4 + i) * 64 + lane] = acc[g][i];
+        __syncthreads();
+        if (wave)
+            return;
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                for (int w = 1; w < WG / 64; w++)
+                    acc[g][i] += sums[((w * G + g) * 4 + i) * 64 + lane];
+    } else {
+        issue(buf[0], 0);
+        for (int s = 0; s < steps; s += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                if (s + u >= steps) // uniform
+                    break;
+                if (u % SPC == 0 && (s + u) % SPC == 0) // uniform: the next chunk
+                    stage_chunk((s + u) / SPC * KC);
+                issue(buf[1 - u], min(s + u + 1, steps - 1));
+                __builtin_amdgcn_sched_barrier(0); // these loads go out before this step's arithmetic
+                step(buf[u], s + u, (s + u) / SPC * Lds::RECORDS);
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int r = 4 * q + i;
-        const int64_t pair = min((uint32_t)pairs[r], (uint32_t)(a.pairs - 1));
+        const int64_t pair = pair_at(r);
 #pragma unroll
         for (int g = 0; g < G; g++)
             if (r < rows && n0 + 16 * g < a.N)
@@ -316,15 +363,32 @@ template <int FMT, bool WHOLE> __global__ __launch_bounds__(WG, 2) void experts_
     }
 }
 
-template <int FMT> hipError_t tile_fmt(const ExpertsArgs &a, hipStream_t s)
+template <int FMT, int G, bool KS> hipError_t tile_g(const ExpertsArgs &a, hipStream_t s)
 {
-    const int chunks = (a.N + TileLds<FMT>::WROWS - 1) / TileLds<FMT>::WROWS;
+    constexpr int WROWS = TileLds<FMT, G, KS>::WROWS;
+    const int chunks = (a.N + WROWS - 1) / WROWS;
     const dim3 grid((unsigned)(a.max_tiles * chunks));
     if (a.K / F<FMT>::SW % 8 == 0)
-        hipLaunchKernelGGL((experts_tile_kernel<FMT, true>), grid, dim3(WG), 0, s, a, chunks);
+        hipLaunchKernelGGL((experts_tile_kernel<FMT, G, true, KS>), grid, dim3(WG), 0, s, a, chunks);
     else
-        hipLaunchKernelGGL((experts_tile_kernel<FMT, false>), grid, dim3(WG), 0, s, a, chunks);
+        hipLaunchKernelGGL((experts_tile_kernel<FMT, G, false, KS>), grid, dim3(WG), 0, s, a, chunks);
     return hipGetLastError();
+}
+// By the workgroups that 64 weight rows each would make.  Many: two groups of 16 rows a wave, which share what is read from
+// LDS.  Under three a CU, one; under one and a half, the waves of a workgroup share its rows instead and divide K, so that
+// all CUs have work.  Measured with Q4_0, 16 rows: 4096 x 12288 (64 workgroups) 24 us so with one group, 28 with two, 44
+// with K whole; 12288 x 4096 (192) 17, 15, 16; 64 rows of 12288 x 4096 (768) 28 us with one group and K whole, 30 with two
+// (Q1_0's chunk of K has work for two waves only, and nothing is gained.)
+template <int FMT> hipError_t tile_fmt(const ExpertsArgs &a, hipStream_t s)
+{
+    const int64_t w = a.max_tiles * ((a.N + 63) / 64);
+    if constexpr (FMT != LB_Q1_0) {
+        if (w <= 64)
+            return tile_g<FMT, 1, true>(a, s);
+        if (w <= 384)
+            return tile_g<FMT, 2, true>(a, s);
+    }
+    return w <= 768 ? tile_g<FMT, 1, false>(a, s) : tile_g<FMT, 2, false>(a, s);
 }
 
 } // namespace

@@ -12,7 +12,7 @@
 //    double-buffered LDS -- the weights unpacked to int8 in natural column order (shift and mask, a 4x4
 //    byte transpose with v_perm_b32, and a v_perm_b32 lookup from code to weight byte: Q2_0 c -> c - 1,
 //    Q1_0 bit -> +/-1, planar (pos, neg) -> pos - neg; Q8_0 weights are int8 already and copied as they
-//    are; a Q4_0 nibble w, moved to its byte's upper half, is the int8 16 w, whose factor the weight scale takes back) -- and one barrier per step separates the writes from the reads.  Every thread loads and
+//    are; a Q4_0 nibble w, moved to its byte's upper half, is the int8 16 w, whose factor the activation scale takes back) -- and one barrier per step separates the writes from the reads.  Every thread loads and
 //    unpacks an equal share of the weight tile and issues an equal share of the activation tile.
 //  * A workgroup is 8 waves (512 threads), two per SIMD, and two workgroups fit a CU.  Wave w computes
 //    the 32 x 32 output tile (weight rows 32 (w mod 2), activation rows 32 (w / 2)) over every step's
@@ -114,6 +114,11 @@ struct LaneOffs {
 
 // Whether every 32 weights have a scale of their own: Q4_0, Q8_0
 constexpr bool scale32(int fmt) { return fmt == LB_Q8_0 || fmt == LB_Q4_0; }
+
+// Q4_0's weight scales stay binary16 in LDS where a workgroup has all 16 waves of a CU (KSPLIT = 2): there their reads, half
+// of the step's bytes from LDS as fp32, are what a step takes (512 x 4096 x 12288: 102 us as fp32, 93 as binary16, converted by
+// the multiply-add).  Two workgroups a CU hide more of them, and the conversions show (2048 x 4096 x 4096: 111 us, 116).
+constexpr bool half_scales(int fmt, int ksplit) { return fmt == LB_Q4_0 && ksplit == 2; }
 
 // Bytes a step advances each base by: weight records (16 bytes per 64 Q2_0 / planar, 128 Q1_0 or 32 Q4_0 weights, 32
 // per 32 Q8_0 weights), their binary16 scales, the activation scales (binary16 per 32) and the activation
@@ -270,7 +275,7 @@ struct __attribute__((aligned(16))) Lds {
 };
 constexpr int XTILE = TM * KS / 4; // dwords of an activation tile, swizzled 16-byte chunks (x_slot)
 
-template <int FMT>
+template <int FMT, int KSPLIT>
 __device__ __forceinline__ void store_step(Lds &lds, int buf, const StepRegs &r, int K, int kk, int tid)
 {
     // On the half step that ends a row of an odd number of 64-column blocks, blocks 2 and 3 of the step get
@@ -279,10 +284,12 @@ __device__ __forceinline__ void store_step(Lds &lds, int buf, const StepRegs &r,
     const int kab = min(KS, K - kk) / QK8;
     if (FMT != LB_TERNARY_PLANAR && tid < TM) {
         const uint32_t hi = kab == 4 ? r.c.y : 0u;
-        lds.dx[buf][0 * TM + tid] = half_bits_to_float((uint16_t)(r.c.x & 0xffffu));
-        lds.dx[buf][1 * TM + tid] = half_bits_to_float((uint16_t)(r.c.x >> 16));
-        lds.dx[buf][2 * TM + tid] = half_bits_to_float((uint16_t)(hi & 0xffffu));
-        lds.dx[buf][3 * TM + tid] = half_bits_to_float((uint16_t)(hi >> 16));
+        // Q4_0's products are 16 isum (|16 isum| <= 16 * 32 * 8 * 128 < 2^22): an exact power of two in the scale
+        constexpr float by = FMT == LB_Q4_0 ? 0.0625f : 1.0f;
+        lds.dx[buf][0 * TM + tid] = by * half_bits_to_float((uint16_t)(r.c.x & 0xffffu));
+        lds.dx[buf][1 * TM + tid] = by * half_bits_to_float((uint16_t)(r.c.x >> 16));
+        lds.dx[buf][2 * TM + tid] = by * half_bits_to_float((uint16_t)(hi & 0xffffu));
+        lds.dx[buf][3 * TM + tid] = by * half_bits_to_float((uint16_t)(hi >> 16));
     }
     const int rr = tid >> 3, p = tid & 7;
     uint32_t *wrow = lds.w[buf] + rr * WROW;
@@ -313,8 +320,13 @@ __device__ __forceinline__ void store_step(Lds &lds, int buf, const StepRegs &r,
         const uint32_t e1 = (r.a.y << 4) & 0xF0F0F0F0u, o1 = r.a.y & 0xF0F0F0F0u;
         *reinterpret_cast<uint4 *>(wrow + 8 * j + 4 * (p & 1)) =
             make_uint4(perm(o0, e0, 0x05010400u), perm(o0, e0, 0x07030602u), perm(o1, e1, 0x05010400u), perm(o1, e1, 0x07030602u));
-        if ((p & 1) == 0) // the products are 16 isum: exact powers of two, |16 isum| <= 16 * 32 * 8 * 128 < 2^22
-            lds.dw[buf][j * TN + rr] = half_bits_to_float((uint16_t)(r.sc >> r.sh)) * 0.0625f;
+        if ((p & 1) == 0) {
+            const uint16_t d = (uint16_t)(r.sc >> r.sh);
+            if (half_scales(FMT, KSPLIT))
+                reinterpret_cast<uint16_t *>(lds.dw[buf])[j * TN + rr] = d;
+            else
+                lds.dw[buf][j * TN + rr] = half_bits_to_float(d);
+        }
     } else if (FMT == LB_Q2_0_G64) {
         const int bb = p >> 2, d = p & 3;
         const bool live = 2 * bb < kab;
@@ -347,7 +359,7 @@ __device__ __forceinline__ void store_step(Lds &lds, int buf, const StepRegs &r,
 // One wave's share of a K-step: its 32 x 32 output tile over the step's KAB = 4 q8_0 blocks (on a half step
 // the last two carry zero weights and scales).  Each block's result is scaled as soon as it is ready; the
 // next block's MFMA runs meanwhile (Q1_0, Q2_0), and the other waves of the SIMD fill the rest.
-template <int FMT, bool EMIT, int KAB>
+template <int FMT, bool EMIT, int KAB, int KSPLIT>
 __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint32_t *xt, const uint32_t (&xb)[4], int h,
                                              int l32, int wn, int wm, int m0, int n0, int M, int N, int nab, int kk,
                                              float (&acc)[16], v16i &iacc, const v16i &cbias,
@@ -377,7 +389,7 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
     // every result is read as fp32 through the bias: 1.5 * 2^23 + isum exactly (|isum| < 2^22).  Q1_0 and
     // Q2_0 issue each block's MFMA before the previous block's rescale, so the wave's own rescale covers the
     // MFMA latency (Q8_0, whose weight scales change with every block, measured slower that way).
-    constexpr bool AHEAD = FMT != LB_Q8_0;
+    constexpr bool AHEAD = FMT != LB_Q8_0 && !half_scales(FMT, KSPLIT);
     v16i Dn;
     if (AHEAD)
         Dn = mfma(0, cbias);
@@ -390,8 +402,15 @@ __device__ __forceinline__ void step_compute(const Lds &lds, int buf, const uint
         float dwv[16];
 #pragma unroll
         for (int g = 0; g < 4; g++) {
-            const float4 dw = *reinterpret_cast<const float4 *>(lds.dw[buf] + (j / JW) * TN + 32 * wn + 8 * g + 4 * h);
-            dwv[4 * g] = dw.x, dwv[4 * g + 1] = dw.y, dwv[4 * g + 2] = dw.z, dwv[4 * g + 3] = dw.w;
+            const int at = (j / JW) * TN + 32 * wn + 8 * g + 4 * h;
+            if (half_scales(FMT, KSPLIT)) {
+                const uint2 dw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(lds.dw[buf]) + at);
+                dwv[4 * g] = half_bits_to_float((uint16_t)dw.x), dwv[4 * g + 1] = half_bits_to_float((uint16_t)(dw.x >> 16));
+                dwv[4 * g + 2] = half_bits_to_float((uint16_t)dw.y), dwv[4 * g + 3] = half_bits_to_float((uint16_t)(dw.y >> 16));
+            } else {
+                const float4 dw = *reinterpret_cast<const float4 *>(lds.dw[buf] + at);
+                dwv[4 * g] = dw.x, dwv[4 * g + 1] = dw.y, dwv[4 * g + 2] = dw.z, dwv[4 * g + 3] = dw.w;
+            }
         }
         const float c = -dx[j] * BIASF; // exact: an 11-bit significand times 3 * 2^22
 #pragma unroll
@@ -510,7 +529,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         const bool some = !GROUPED || 32 * wm < M; // uniform: a wave without rows of the tile computes nothing
         __builtin_amdgcn_s_waitcnt(wait_vmcnt(0)); // this thread's loads of step j have landed
         if (active)
-            store_step<FMT>(lds[half], q, ring, K, kk, tid);
+            store_step<FMT, KSPLIT>(lds[half], q, ring, K, kk, tid);
         step_barrier();
         // the next step's loads (past the last step the walk wraps: valid addresses, unused).  With one
         // step in all and two halves, the stride is twice the walk, so the offset may need two wraps.
@@ -520,7 +539,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
         issue_x(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
         if (active && some)
-            step_compute<FMT, EMIT, 4>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
+            step_compute<FMT, EMIT, 4, KSPLIT>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
                                        kk, acc, iacc, cbias, sums);
         kk = kn;
     }
@@ -650,6 +669,14 @@ hipError_t launch_gemm(int fmt, const uint8_t *W, int64_t N, int64_t K, float w_
                        const void *Xscale, int64_t M, float *Y, int32_t *sums, hipStream_t s)
 {
     const bool emit = sums != nullptr;
+    // Few rows, or few weight rows: tiles of 16 rows (experts_tile.hip), as one expert's.  Measured: 2 rows of 4096 x 4096
+    // 9 us so and 29 here, 128 22 and 31; 64 of 12288 x 4096 28 and 30, 96 41 and 31; 192 of 4096 x 12288 75 and 84.
+    if (fmt == LB_Q4_0 && !emit && (M + 15) / 16 * ((N + 63) / 64) <= 768) {
+        ExpertsArgs a = {};
+        a.W = W, a.E = 1, a.N = (int32_t)N, a.K = (int32_t)K, a.pairs = (int32_t)M, a.per_row = 1, a.max_tiles = (M + 15) / 16;
+        a.xq = Xq, a.xs = static_cast<const uint16_t *>(Xscale), a.y = Y;
+        return launch_experts_tile(fmt, a, s);
+    }
     switch (fmt) {
     case LB_Q1_0:
         return emit ? launch_fmt<LB_Q1_0, true>(W, N, K, w_scale, Xq, Xscale, M, Y, sums, s)

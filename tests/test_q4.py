@@ -89,7 +89,9 @@ def test_one_row(N, K):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(2, 1, 128), (3, 65, 256), (70, 130, 384), (128, 64, 4096), (129, 300, 640), (260, 1000, 1408)])
+@pytest.mark.parametrize("M,N,K", [(2, 1, 128), (3, 65, 256), (70, 130, 384), (128, 64, 4096), (129, 300, 640), (260, 1000, 1408),
+                                   (16, 4100, 2048), (33, 8200, 1152), (17, 1030, 16384), (5, 20, 896), (193, 4100, 256), (300, 2500, 128),
+                                   (1, 77, 512), (4100, 70, 384)])
 def test_many_rows(M, N, K):
     say(f"case many rows M={M} N={N} K={K}")
     w, d, q, s = case(N, K, M)
