@@ -13,7 +13,7 @@ bool is_page(int64_t p) { return p >= 16 && p <= 1024 && (p & (p - 1)) == 0; }
 bool is_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
 constexpr int64_t kMax = INT32_MAX;
-constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxExperts = 1024, kMaxPairs = (int64_t)1 << 30; // (places of tiles are numbered in 32 bits)
 constexpr const char *kTiles = "the step has 2^23 tiles, or parts of tiles, or more";
 
 // The cache's shape; LB_OK or the failure.
@@ -331,7 +331,7 @@ int64_t lowbit_experts_weight_bytes(int fmt, int64_t E, int64_t N, int64_t K)
 
 int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E)
 {
-    if (pairs < 0 || pairs > kMax - 4 || E < 1 || E > kMaxExperts)
+    if (pairs < 0 || pairs > kMaxPairs || E < 1 || E > kMaxExperts)
         return -1;
     const int64_t tiles = lb::experts_max_tiles(pairs, E);
     return (4 * lb::experts_pairs_at(tiles, tiles, lb::experts_tile_rows(pairs, E)) + 15) / 16 * 16;
@@ -340,8 +340,8 @@ int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E)
 lb_status lowbit_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, void *plan, hipStream_t s)
 {
     const char *fn = "lowbit_experts_plan";
-    if (pairs < 0 || pairs > kMax - 4 || E < 1 || E > kMaxExperts)
-        return lb::abi_fail(LB_ESHAPE, fn, "pairs must be from 0 to 2^31 - 5, E from 1 to 1024");
+    if (pairs < 0 || pairs > kMaxPairs || E < 1 || E > kMaxExperts)
+        return lb::abi_fail(LB_ESHAPE, fn, "pairs must be from 0 to 2^30, E from 1 to 1024");
     if (pairs == 0)
         return LB_OK;
     if (!experts || !plan)
@@ -362,8 +362,8 @@ lb_status lowbit_experts_matmul(int fmt, const void *W, int64_t E, int64_t N, in
         return lb::abi_fail(LB_EINVAL, fn, "unknown weight format");
     if (fmt != LB_Q1_0 && fmt != LB_Q2_0_G64 && fmt != LB_Q4_0)
         return lb::abi_fail(LB_EUNSUPPORTED, fn, "experts are Q1_0, Q2_0_g64 or Q4_0");
-    if (N < 0 || K < 1 || pairs < 0 || pairs_per_row < 1 || E < 1 || E > kMaxExperts || N > kMax || pairs > kMax - 4 || pairs_per_row > kMax)
-        return lb::abi_fail(LB_ESHAPE, fn, "a size below its least (K, E and pairs_per_row: 1), E over 1024, or another over 2^31 - 1");
+    if (N < 0 || K < 1 || pairs < 0 || pairs_per_row < 1 || E < 1 || E > kMaxExperts || N > kMax || pairs > kMaxPairs || pairs_per_row > kMax)
+        return lb::abi_fail(LB_ESHAPE, fn, "a size below its least (K, E and pairs_per_row: 1), E over 1024, pairs over 2^30, or another over 2^31 - 1");
     if (K % (fmt == LB_Q2_0_G64 ? 64 : 128) || K > (fmt == LB_Q4_0 ? 16384 : 32768))
         return lb::abi_fail(LB_ESHAPE, fn, "K must be a multiple of 128 (64 for Q2_0_g64), at most 32768 (16384 for Q4_0)");
     if (lowbit_weight_bytes(fmt, N, K) >= (int64_t)1 << 32)

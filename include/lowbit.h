@@ -406,7 +406,8 @@ lb_status lowbit_route(int dtype, const void *logits, int64_t stride, int64_t T,
  *
  * lowbit_experts_plan sorts `pairs` pairs by expert (experts: device int32 [pairs]; a number outside 0 .. E-1 is a pair
  * that is left out, as a padded token's -1) into `plan` (device, lowbit_experts_plan_bytes(pairs, E) bytes, 16-byte
- * aligned), for any number of products of the same pairs and E.  The order does not depend on how anything runs.
+ * aligned), for any number of products of the same pairs and E.  The order does not depend on how anything runs.  At most
+ * 2^30 pairs and 1024 experts.
  */
 int64_t lowbit_experts_weight_bytes(int fmt, int64_t E, int64_t N, int64_t K);
 int64_t lowbit_experts_plan_bytes(int64_t pairs, int64_t E);
@@ -428,7 +429,7 @@ lb_status lowbit_experts_matmul(int fmt, const void *W, int64_t E, int64_t N, in
 /*
  * out[t] = sum over j of weights[t][j] * y[t * top_k + j], for the pairs with an expert in 0 .. E-1 (the others' rows are not
  * read; a token without any gives zeros).  y fp32 [T * top_k][N], out [T][N] of type dtype with a stride in elements.
- * Summed in fp32 in the order of j, rounded once.  T * N below about 2^32.
+ * Summed in fp32 in the order of j, rounded once.  out must not overlap y.  T * N below about 2^32.
  */
 lb_status lowbit_experts_combine(int dtype, const float *y, const int32_t *experts, const float *weights, int64_t T, int64_t top_k, int64_t E,
                                  int64_t N, void *out, int64_t out_stride, hipStream_t s);

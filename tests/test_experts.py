@@ -19,9 +19,9 @@ def test_sizes():
     assert L.lowbit_experts_weight_bytes(L.Q2_0_G64, 0, 5, 128) == 0
     assert L.lowbit_experts_weight_bytes(L.Q4_0, 1, 1 << 22, 16384) == -1 and L.lowbit_experts_weight_bytes(9, 1, 1, 128) == -1
     assert L.lowbit_experts_weight_bytes(L.Q1_0, 1, 1, 64) == -1 and L.lowbit_experts_weight_bytes(L.Q1_0, 1025, 1, 128) == -1
-    for pairs, E in ((0, 1), (1, 1), (7, 1024), (2**31 - 5, 1024)):
+    for pairs, E in ((0, 1), (1, 1), (7, 1024), (2**30, 1024)):
         assert L.lowbit_experts_plan_bytes(pairs, E) >= 4 * pairs
-    for pairs, E in ((-1, 4), (2**31 - 4, 4), (4, 0), (4, 1025)):
+    for pairs, E in ((-1, 4), (2**30 + 1, 4), (4, 0), (4, 1025)):
         assert L.lowbit_experts_plan_bytes(pairs, E) == -1
 
 
@@ -173,7 +173,7 @@ def test_few_rows(fmt, E, N, K, n, per):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
-@pytest.mark.parametrize("E,N,K,n,per", [(1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4)])
+@pytest.mark.parametrize("E,N,K,n,per", [(1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4), (40, 1000, 1152, 500, 1), (20, 1000, 1408, 150, 2)])
 def test_many_rows(fmt, E, N, K, n, per):
     say(f"case many rows {W.NAMES[fmt]} E={E} N={N} K={K} pairs={n} per={per}")
     layer = Layer(fmt, E, N, K)
@@ -333,3 +333,89 @@ def test_a_layer_of_experts(T, fmts):
             # largest / 127 times the weight; of all k * H of them hardly more than a few do (fp32 is right to 2^-20 of a
             # step's 2^-7), and 1 % of the result's size is over 10 of the largest such steps
             assert np.abs(got - want).max() <= 0.01 * np.abs(want).max(), (t, np.abs(got - want).max(), np.abs(want).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pairs,N", [(150, 16_000_000), (3000, 800_000)])
+def test_outputs_past_32_bits(pairs, N):
+    """Rows of 16 and of 128 a tile, and every pair by itself, at sampled places; then the sum over pairs of rows."""
+    say(f"case outputs past 32 bits {pairs} x {N}")
+    fmt, E, K = L.Q1_0, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    step = L.lowbit_experts_weight_bytes(fmt, 1, N, K)
+    w = torch.randint(0, 256, (E, step), dtype=torch.uint8, generator=g, device="cuda")
+    w[:, 16 * N:18 * N] = (torch.rand(E, N, generator=g, device="cuda") * 0.02 + 0.005).half().view(torch.uint8)
+    q, s = W.random_rows(np.random.default_rng(0), pairs, K)
+    e = (np.arange(pairs) % 3 == 0).astype(np.int32)
+    y = torch.zeros(pairs * N, device="cuda")
+    at_p, at_n = [0, pairs // 2, pairs - 2, pairs - 1], [0, 5, N // 3, N - 1]
+    want, mags = np.zeros((4, 4)), np.zeros((4, 4))
+    for i, p in enumerate(at_p):
+        for j, n in enumerate(at_n):
+            rec = w[e[p], 16 * n:16 * n + 16].cpu().numpy()
+            bits = np.array([rec[(32 * (k % 32 // 8) + 4 * (k % 8) + k // 32) // 8] >> ((4 * (k % 8) + k // 32) % 8) & 1 for k in range(128)])
+            d = w[e[p], 16 * N + 2 * n:16 * N + 2 * n + 2].cpu().numpy().view(np.float16)
+            a, b = W.product(fmt, (2 * bits.astype(np.int64) - 1)[None], d[None], q[p:p + 1], s[p:p + 1])
+            want[i, j], mags[i, j] = a[0, 0], b[0, 0]
+
+    def check():
+        got = y.view(pairs, N)[at_p][:, at_n].cpu().numpy()
+        assert (np.abs(got - want) <= W.allowance(mags, K)).all()
+        y.zero_()
+
+    xq, xs, ed = dev(q), dev(s), dev(e)
+    L.lowbit_experts_matmul(fmt, w.view(-1), E, N, K, xq, xs, ed, pairs, 1, y)
+    check()
+    L.lowbit_experts_matmul(fmt, w.view(-1), E, N, K, xq, xs, ed, pairs, 1, y, plan=planned(e, E))
+    got = y.view(pairs, N)[at_p][:, at_n].cpu().numpy()
+    assert (np.abs(got - want) <= W.allowance(mags, K)).all()
+    out = torch.zeros(pairs // 2, N, dtype=torch.bfloat16, device="cuda")
+    ones = torch.ones(pairs, device="cuda")
+    L.lowbit_experts_combine(L.BF16, y, ed, ones, pairs // 2, 2, E, N, out)
+    both = y.view(pairs, N)
+    assert torch.equal(out[-1], (both[pairs - 2 - pairs % 2] + both[pairs - 1 - pairs % 2]).bfloat16()) and torch.equal(out[0], (both[0] + both[1]).bfloat16())
+
+
+@pytest.mark.gpu
+def test_experts_past_32_bits():
+    """The last expert of tensors that together pass 4 GiB."""
+    fmt, E, N, K = L.Q4_0, 1000, 2048, 4096
+    step = L.lowbit_experts_weight_bytes(fmt, 1, N, K)
+    assert E * step > 2**32
+    packed = torch.zeros(E * step, dtype=torch.uint8, device="cuda")
+    layer = Layer(fmt, 1, N, K)
+    packed[(E - 1) * step:] = layer.packed
+    e = np.full(5, E - 1, np.int32)
+    q, s = W.random_rows(np.random.default_rng(2), 5, K)
+    want, mags = W.product(fmt, layer.w[0], layer.d[0], q, s)
+    for plan in (None, planned(e, E)):
+        y = torch.zeros(5, N, device="cuda")
+        L.lowbit_experts_matmul(fmt, packed, E, N, K, dev(q), dev(s), dev(e), 5, 1, y, plan=plan)
+        assert (np.abs(host(y) - want) <= W.allowance(mags, K)).all()
+
+
+@pytest.mark.gpu
+def test_on_another_stream_and_two_at_once():
+    """Two products with plans of their own on two streams at once, against one after another."""
+    layer = Layer(L.Q2_0_G64, 6, 300, 512)
+    rng = np.random.default_rng(3)
+    runs = []
+    for i in range(2):
+        n = 60 + 700 * i
+        e = some_pairs(rng, n, 6)
+        q, s = W.random_rows(rng, n, 512)
+        runs.append((n, dev(e), dev(q), dev(s), torch.zeros(L.lowbit_experts_plan_bytes(n, 6), dtype=torch.uint8, device="cuda"),
+                     torch.zeros(n, 300, device="cuda"), torch.zeros(n, 300, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def go(n, e, q, s, plan, y, stream):
+        L.lowbit_experts_plan(e, n, 6, plan, stream=stream)
+        L.lowbit_experts_matmul(L.Q2_0_G64, layer.packed, 6, 300, 512, q, s, e, n, 1, y, plan=plan, stream=stream)
+
+    for n, e, q, s, plan, y, _, stream in runs:
+        go(n, e, q, s, plan, y, stream)
+    torch.cuda.synchronize()
+    for n, e, q, s, plan, y, z, _ in runs:
+        go(n, e, q, s, plan, z, None)
+        torch.cuda.synchronize()
+        assert torch.equal(y, z)

@@ -7,6 +7,8 @@ import torch
 
 import bit_quantized_matvec_q1_amd.lowbit as L
 import serve_ref as R
+import synth
+import test_serve_together as together
 from gpu_util import dev, host, say
 
 A = 1 << 20
@@ -203,3 +205,80 @@ def test_captured_and_on_another_stream():
         assert torch.equal(out, mine_out) and torch.equal(cache, mine)
         assert (out[n:] == 3).all()
     assert math.isfinite(float(out.float().sum()))
+
+
+@pytest.mark.gpu
+def test_slots_past_32_bits():
+    """The last page of a cache of more than 4 GiB."""
+    D, P, hk = 256, 1024, 4
+    pages = (2**32 + 2**30) // (hk * R.record_bytes(P, D))
+    cache = torch.zeros(L.lowbit_kv_cache_bytes(pages, hk, P, D), dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(0)
+    q, k, v = (dev(rng.standard_normal((2, h, D)).astype(np.float32)) for h in (3, hk, hk))
+    slots = dev(np.array([pages * P - 1, 7]))
+    pos, freq = dev(np.int32([5, 6])), dev((1e4 ** (-np.arange(64) / 64)).astype(np.float32))
+    L.lowbit_kv_append_rotary(L.F32, q, q, k, v, 2, 3, hk, D, pos, freq, 128, L.ROTARY_HALVES, slots, cache, pages, P)
+    kk, vv = torch.zeros_like(k), torch.zeros_like(v)
+    L.lowbit_kv_read(L.F32, cache, pages, P, 2, hk, D, slots, kk, vv)
+    turned = turn(host(k), host(pos), host(freq), 128, False, 1.0).astype(np.float32)
+    for t in range(2):
+        for h in range(hk):
+            assert np.array_equal(host(kk)[t, h], R.values(*R.quantise(turned[t, h].astype(np.float64))).astype(np.float32))
+            assert np.array_equal(host(vv)[t, h], R.values(*R.quantise(host(v)[t, h].astype(np.float64))).astype(np.float32))
+
+
+class RotaryServer(together.Server):
+    """A step whose queries and keys are turned by the plan's positions on their way."""
+
+    def __init__(self, *a):
+        super().__init__(*a)
+        self.freq = torch.pow(1e4, -torch.arange(together.D // 2, device="cuda").double() * 2 / together.D).float()
+        self.q = torch.zeros(self.max_tokens, together.HQ, together.D, device="cuda")
+
+    def step(self):
+        n, hq, hk, D, P = self.max_tokens, together.HQ, together.HK, together.D, together.P
+        L.lowbit_kv_plan(self.new, self.B, P, self.lens, self.lens, self.table, self.stride, self.free, self.count, self.count, self.cu, self.cup,
+                         self.slots, self.positions, n, self.status)
+        q, k, v = (self.qkv[:, a * D:z * D] for a, z in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+        L.lowbit_kv_append_rotary(L.F32, q, self.q, k, v, n, hq, hk, D, self.positions, self.freq, D, L.ROTARY_HALVES, self.slots, self.cache,
+                                  self.pages, P)
+        L.lowbit_kv_attention(L.F32, self.q, n, self.B, hq, hk, D, self.cu, self.lens, self.table, self.stride, self.cache, self.pages, P, self.max_q,
+                              self.stride * P, 1 / math.sqrt(D), self.out, workspace=self.ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_of_a_batch(captured):
+    """Plan, rotation with the append, and attention over several steps of a padded batch, against 64 bits."""
+    hq, hk, D = together.HQ, together.HK, together.D
+    s, follower = RotaryServer(3, 8, 30, 40, 20), together.Follower(3)
+    rng = synth.rng(7)
+    freq = host(s.freq)
+    step = s.step
+    if captured:
+        s.new.zero_()
+        s.step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s.step()
+        step = graph.replay
+    held = [0, 0, 0]
+    for news in ([5, 0, 20], [1, 1, 1], [0, 17, 1], [1, 1, 1]):
+        T = sum(news)
+        qkv = rng.standard_normal((T, hq + 2 * hk, D)).astype(np.float32)
+        s.qkv.fill_(float("nan"))
+        s.qkv[:T] = dev(qkv.reshape(T, -1))
+        s.new.copy_(dev(np.int32(news)))
+        s.out.fill_(3)
+        torch.cuda.synchronize()
+        step()
+        torch.cuda.synchronize()
+        pos = np.concatenate([np.arange(h, h + n) for h, n in zip(held, news)]).astype(np.int32)
+        held = [h + n for h, n in zip(held, news)]
+        turned = qkv.astype(np.float64)
+        turned[:, :hq + hk] = turn(qkv[:, :hq + hk], pos, freq, D, False, 1.0)
+        want = follower.step(news, turned.astype(np.float32).reshape(T, -1))
+        got = host(s.out)
+        assert np.abs(got[:T] - np.asarray(want).reshape(T, hq, D)).max() < together.TOL  # as without rotation
+        assert (got[T:] == 3).all()
