@@ -49,6 +49,7 @@ constexpr float BIASF = 12582912.0f;
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef float v4f_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ uint32_t perm(uint32_t s0, uint32_t s1, uint32_t sel)
 {
@@ -571,9 +572,9 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     }
 
     // The wave's 32 x 32 tile of Y.  Lane (h, l32) holds weight rows n = 32 wn + 8 (i / 4) + 4 h + i % 4 of
-    // activation row m = 32 wm + l32; the tile goes through LDS (a 32 x 32 fp32 area per wave, element
-    // [m][n] at m * 32 + (n ^ m): the XOR keeps the column writes and the row reads free of bank conflicts)
-    // so that every store writes two whole 128-byte row segments of Y.
+    // activation row m = 32 wm + l32: four consecutive ones four times.  The tile goes through LDS (a 32 x 32 fp32 area per
+    // wave, the 16 bytes of chunk c of row m at chunk c ^ (m % 8): writes and reads meet different banks) so that a store
+    // writes eight 128-byte row segments of Y, 16 bytes a lane.
     const int m = m0 + 32 * wm + l32;
     float out[16];
     if (PLANAR) {
@@ -596,17 +597,27 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         __syncthreads(); // every wave is done with the activation tiles
     uint32_t *t = (wave < 4 ? xt0[0] : xt1[0]) + 1024 * (wave & 3);
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int nl = 8 * (i >> 2) + 4 * h + (i & 3);
-        t[32 * l32 + (nl ^ l32)] = __float_as_uint(out[i]);
-    }
-    const int nc = lane & 31, n = n0 + 32 * wn + nc;
+    for (int q = 0; q < 4; q++)
+        *reinterpret_cast<float4 *>(t + 32 * l32 + 4 * ((2 * q + h) ^ (l32 & 7))) =
+            make_float4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
+    const int nc = lane & 7, n = n0 + 32 * wn + 4 * nc;
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-        const int r = 2 * k + (lane >> 5), mm = m0 + 32 * wm + r;
-        const float v = __uint_as_float(t[32 * r + (nc ^ r)]);
-        if (mm < M && n < N)
-            Y[(GROUPED ? (int64_t)g.pair(mm) : (int64_t)mm) * N + n] = v;
+    for (int k = 0; k < 4; k++) {
+        const int r = 8 * k + (lane >> 3), mm = m0 + 32 * wm + r;
+        const float4 v = *reinterpret_cast<const float4 *>(t + 32 * r + 4 * (nc ^ (r & 7)));
+        if (mm < M && n < N) {
+            float *y = Y + (GROUPED ? (int64_t)g.pair(mm) : (int64_t)mm) * N + n;
+            if (n + 3 < N) {
+                const v4f_a4 f = {v.x, v.y, v.z, v.w};
+                *reinterpret_cast<v4f_a4 *>(y) = f;
+            } else { // a row's last one to three
+                y[0] = v.x;
+                if (n + 1 < N)
+                    y[1] = v.y;
+                if (n + 2 < N)
+                    y[2] = v.z;
+            }
+        }
     }
 }
 
