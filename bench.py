@@ -33,7 +33,7 @@ MFMA_I8_PEAK_TOPS = 5000.0  # MI355X dense int8, published
 METRIC = "effective weight GB/s & % HBM peak, 8B-shape batch-1 ternary matvec; prefill TOPS"
 PROFILE_PMC = os.path.join(ROOT, "profiles", "matvec_batched_q2_8b_token.pmc.txt")
 # the decode kernel and the batch tile planner: both decide the batched launch's traffic
-KERNEL_SRCS = [os.path.join(ROOT, "bit_quantized_matvec_q1_amd", "csrc", f) for f in ("matvec.hip", "abi.cpp")]
+KERNEL_SRCS = [os.path.join(ROOT, "bit_quantized_matvec_q1_amd", "csrc", f) for f in ("matvec_tile.h", "matvec.hip", "abi.cpp")]
 
 
 def log(*a):
@@ -354,7 +354,7 @@ def time_token(tok, steps, warmup):
 
 def stored_traffic(kernel_name, algorithmic_bytes):
     """HBM bytes per launch from the committed rocprofv3 --pmc summary, if it was taken on the current
-    kernel and tile-planner sources (sha256 over matvec.hip then abi.cpp); otherwise None."""
+    kernel and tile-planner sources (sha256 over matvec_tile.h, matvec.hip, abi.cpp); otherwise None."""
     if not os.path.exists(PROFILE_PMC):
         return None
     text = open(PROFILE_PMC).read()

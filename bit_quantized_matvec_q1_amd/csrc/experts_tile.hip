@@ -17,8 +17,8 @@
 // A wave has G groups of 16 weight rows, so that what it reads from LDS (activations, scales, accumulator starts) is read
 // once for all of them.  lowbit_gemm takes the same kernel for Q4_0 products of few rows, whose tiles need no plan.
 //
-// What bounds it: HBM, or the cache, while experts have few rows (512 pairs of 128 Q4_0 experts of 2048 x 768, 113 MB: 28 us,
-// 4.1 TB/s), the vector unit with many (12 to 14 instructions for eight weights of a lane and 16 rows, eight of them the
+// What bounds it: loads while experts have few rows (360 pairs of 128 Q4_0 experts of 2048 x 768, 107 MB: 22 to 24 us, 4.5 to
+// 4.9 TB/s; a workgroup's start, plan to rows to LDS, beside its three steps of K), the vector unit with many (12 to 14 instructions for eight weights of a lane and 16 rows, eight of them the
 // rescale).  Two things made it: each row's scales staged through LDS by whole lines (read four at a time from memory, their
 // lines came through the caches again for every step, Q4_0 875 -> 577 us for 32768 pairs), and results in vector registers.
 #include "matvec_tile.h"

@@ -27,6 +27,8 @@
 //    multiply-add per q8_0 block, then one per weight block).
 //  * The experts' products (GROUPED) are the same tiles with other rows: a tile is up to TM pairs of one expert, from the
 //    plan of experts.hip, whose activation rows are gathered and whose output rows are scattered by the pairs' numbers.
+//    24576 pairs of 64 Q1_0 experts of 2816 x 2048: 500 to 560 us, 506 to 567 TOPS (places without a pair not counted), the vector
+//    unit some three quarters busy, two thirds of it the rescale.
 //  * Planar weights have no block scales: the MFMA accumulates int32 over the whole row and the two
 //    per-row / per-tensor scales are applied once at the end.
 #include "serve_internal.h"

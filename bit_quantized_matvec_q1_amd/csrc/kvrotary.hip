@@ -12,6 +12,9 @@
 // and values), and computes the tokens' sines and cosines once, spread over its threads, through LDS.  A lane of a query has
 // four whole pairs, four elements of either half of the turned part, and keeps their sines over the heads; the next head's
 // elements are loaded ahead.  (Keys are written by lanes of eight consecutive elements, which read the other half's again.)
+//
+// Measured: 16384 bf16 rows of 32 query and 2 x 8 key and value heads of 128: 84 to 93 us, 355 MB, 3.8 to 4.2 TB/s of the 5.1
+// that a large copy reaches (120 us with sines by head and the library's functions); 32 fp32 rows 6 us.
 #include "kvcache_device.h"
 
 namespace lb {

@@ -2,6 +2,9 @@
 // matvec_tile.h's kernels for this format, in a translation unit of their own so that they compile beside the others.
 // A Q4_0 block is one 16-byte code record, as a Q2_0_g64 or Q1_0 block is, so configurations, tiles and the work lists
 // are theirs.
+//
+// Bound by HBM as they are: 151669 x 4096 (349 MB) takes 51.5 us, 6.8 TB/s of the 7.1 that a plain read reaches; 12288 x
+// 4096 (28 MB) 6.7 us and 640 x 2560 3.1 us, of which some 3 us are a launch's.
 #include "matvec_tile.h"
 
 namespace lb {
