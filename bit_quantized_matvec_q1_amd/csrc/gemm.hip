@@ -27,7 +27,7 @@
 //    multiply-add per q8_0 block, then one per weight block).
 //  * The experts' products (GROUPED) are the same tiles with other rows: a tile is up to TM pairs of one expert, from the
 //    plan of experts.hip, whose activation rows are gathered and whose output rows are scattered by the pairs' numbers.
-//    24576 pairs of 64 Q1_0 experts of 2816 x 2048: 500 to 560 us, 506 to 567 TOPS (places without a pair not counted), the vector
+//    24576 pairs of 64 Q1_0 experts of 2816 x 2048: 470 to 530 us, 536 to 605 TOPS (places without a pair not counted), the vector
 //    unit some three quarters busy, two thirds of it the rescale.
 //  * Planar weights have no block scales: the MFMA accumulates int32 over the whole row and the two
 //    per-row / per-tensor scales are applied once at the end.
@@ -115,6 +115,11 @@ struct LaneOffs {
     uint32_t x[2];  // its two activation-tile slots: row offset + 16 x chunk (x_slot)
 };
 
+// Whether a row may end in half a step: K of Q2_0_g64 and planar weights is a multiple of 64, the others' of 128.  (What a
+// half step does otherwise is done without branches around loads: where paths with and without a load meet, the compiler
+// waits for what is in flight, as soon as it is issued.  24576 pairs of 64 Q1_0 experts of 2816 x 2048 480 -> 465 us, 512 x
+// 12288 x 4096 Q4_0 84.5 -> 80.6.)
+constexpr bool halves(int fmt) { return fmt == LB_Q2_0_G64 || fmt == LB_TERNARY_PLANAR; }
 // Whether every 32 weights have a scale of their own: Q4_0, Q8_0
 constexpr bool scale32(int fmt) { return fmt == LB_Q8_0 || fmt == LB_Q4_0; }
 
@@ -178,7 +183,7 @@ __device__ __forceinline__ LaneOffs lane_offsets(int N, int K, int M, int n0, in
 
 // One step's weight codes / scales and activation scales into registers.  A full step (128 columns) reads
 // exactly the step's blocks.  The half step that ends a Q2_0 / planar row of an odd number of 64-column
-// blocks (only one step of the walk) takes a branch whose lanes of the missing second block re-read the
+// blocks (only one step of the walk) has lanes of the missing second block, which re-read the
 // first.  Every thread loads the activation scales of activation row tid mod TM (the first TM threads
 // store them).
 template <int FMT, bool GROUPED>
@@ -187,7 +192,7 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
                                           bool half_step, int tid, int m0, int M, int K)
 {
     uint32_t ow = o.w + step_wbytes<FMT>(kk), os = o.ws + step_sbytes<FMT>(kk);
-    if (half_step) { // uniform
+    if (halves(FMT) && half_step) { // uniform
         const uint32_t second = (uint32_t)((tid >> 2) & 1); // the lane's record / beat index within the step
         ow -= 16u * second;
         os -= 2u * second;
@@ -203,10 +208,11 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
             odx = (uint32_t)min(m0 + t, M - 1) * (uint32_t)(K / QK8) * 2u;
         }
         odx += (uint32_t)(kk / QK8) * 2u;
-        // one 8-byte load per activation row (4-byte aligned: K / 32 and kk / 32 are even); the half step has
-        // two blocks only
-        if (half_step) { // (blocks 2 and 3 are stored as zero)
+        // one 8-byte load per activation row (4-byte aligned: K / 32 and kk / 32 are even); with half steps, which have
+        // two blocks only, two of 4 bytes
+        if (halves(FMT)) { // (blocks 2 and 3 of a half step are stored as zero)
             r.c.x = *(const gu32 *)((const gu8 *)xsc + odx);
+            r.c.y = *(const gu32 *)((const gu8 *)xsc + (odx + (half_step ? 0u : 4u)));
         } else {
             const v2u_a4 t = *(const gv2u *)((const gu8 *)xsc + odx);
             r.c.x = t.x, r.c.y = t.y;
@@ -237,18 +243,20 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
 // instruction fills 64 consecutive 16-byte slots and each thread issues two.  Chunk c (16 bytes) of tile
 // row r sits in slot r * XCH + (c ^ ((r >> 1) & 7)), so the operand reads (16 lanes, one chunk of 16
 // consecutive rows each) meet 16 different bank groups; the lane that fills a slot loads the chunk that
-// belongs there.  On the half step the lanes of the chunks past K load nothing (each wave holds whole
-// rows, so every wave still issues both instructions).
+// belongs there.  On the half step the lanes of the chunks past K load the first half's again (their weights are zeros).
 __device__ __forceinline__ int x_slot(int r, int c) { return r * XCH + (c ^ ((r >> 1) & 7)); }
 
+template <int FMT>
 __device__ __forceinline__ void issue_x(uint32_t *lds_tile, const int8_t *__restrict__ X, const LaneOffs &o, int kk,
                                        bool half_step, int wave, int lane)
 {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         uint32_t *dst = lds_tile + 4 * (128 * wave + 64 * u); // the wave's 64 slots
-        if (!half_step || ((64 * u + lane) % XCH ^ (((128 * wave + 64 * u + lane) / XCH >> 1) & 7)) < 4)
-            __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + (o.x[u] + (uint32_t)kk)), (lvoid *)dst, 16, 0, 0);
+        uint32_t at = o.x[u] + (uint32_t)kk;
+        if (halves(FMT)) // chunks 4 to 7 are those of the lanes whose bit 2 differs from u
+            at -= half_step ? (uint32_t)((lane << 4) & 64) ^ (64u * u) : 0u;
+        __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + at), (lvoid *)dst, 16, 0, 0);
     }
 }
 
@@ -519,7 +527,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     StepRegs ring;
     int kk = kfirst;
     load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kk, K - kk < KS, tid, m0, M, K);
-    issue_x(xt0[half], X, lo, kk, K - kk < KS, wave, lane);
+    issue_x<FMT>(xt0[half], X, lo, kk, K - kk < KS, wave, lane);
 
     for (int j0 = 0; j0 < nsh; j0 += 2)
 #pragma unroll
@@ -540,7 +548,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         kn = kn >= kend ? kn - kend : kn;
         kn = kn >= kend ? kn - kend : kn;
         load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
-        issue_x(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
+        issue_x<FMT>(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
         if (active && some)
             step_compute<FMT, EMIT, 4, KSPLIT>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
                                        kk, acc, iacc, cbias, sums);
