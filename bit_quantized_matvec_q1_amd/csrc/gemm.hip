@@ -124,8 +124,8 @@ constexpr bool halves(int fmt) { return fmt == LB_Q2_0_G64 || fmt == LB_TERNARY_
 constexpr bool scale32(int fmt) { return fmt == LB_Q8_0 || fmt == LB_Q4_0; }
 
 // Q4_0's weight scales stay binary16 in LDS where a workgroup has all 16 waves of a CU (KSPLIT = 2): there their reads, half
-// of the step's bytes from LDS as fp32, are what a step takes (512 x 4096 x 12288: 102 us as fp32, 93 as binary16, converted by
-// the multiply-add).  Two workgroups a CU hide more of them, and the conversions show (2048 x 4096 x 4096: 111 us, 116).
+// of the step's bytes from LDS as fp32, are what a step takes (512 x 4096 x 12288: 95 us as fp32, 91 as binary16, converted by
+// the multiply-add).  Two workgroups a CU hide more of them, and the conversions show (2048 x 4096 x 4096: 104 us, 110).
 constexpr bool half_scales(int fmt, int ksplit) { return fmt == LB_Q4_0 && ksplit == 2; }
 
 // Bytes a step advances each base by: weight records (16 bytes per 64 Q2_0 / planar, 128 Q1_0 or 32 Q4_0 weights, 32
