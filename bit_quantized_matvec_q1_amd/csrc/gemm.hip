@@ -468,7 +468,17 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     const int h = lane >> 5, l32 = lane & 31;
     // this wave's 32 x 32 output tile inside the 64 x 128 workgroup tile
     const int wn = wave & 1, wm = wave >> 1;
-    const int bn = blockIdx.x % ntn, bm = blockIdx.x / ntn; // weight tiles vary fastest
+    // Weight tiles vary fastest, in the order of the workgroups, which go round the eight XCDs.  Activations that an XCD's L2 (4
+    // MiB) does not hold come from behind it for nearly every workgroup then (512 x 4096 x 12288: 374 MB fetched, for 35 MB),
+    // so there each XCD has a run of tiles instead, of few activation rows.  Measured, Q1_0, Q2_0 and Q4_0: 512 x 4096 x 12288
+    // 86.6 -> 78.6 us, 92.0 -> 84.7, 91 -> 88, 8192 x 4096 x 4096 373 -> 357 and 399 -> 384; below that size 512 x 12288 x 4096
+    // (2 MB) 76.1 -> 77.7 and 79.5 -> 82.4.  Grouped tiles stay in order: those without rows are the last ones.
+    int id = blockIdx.x;
+    if (!GROUPED && (int64_t)M * K > 4 << 20) { // uniform
+        const int each = gridDim.x / 8, more = gridDim.x % 8, xcd = id % 8;
+        id = xcd * each + min(xcd, more) + id / 8;
+    }
+    const int bn = id % ntn, bm = id / ntn;
     const int n0 = bn * TN, m0 = GROUPED ? 0 : bm * TM;
     Gather g = {};
     if constexpr (GROUPED) {
