@@ -203,10 +203,10 @@ template <int DT> hipError_t combine_d(const CombineArgs &a, hipStream_t s)
 
 } // namespace
 
-// Rows a tile: 16, and 128 from 96 pairs an expert on.  Measured with 64 experts of 1536 x 2048 and 128 of 2048 x 768, of
-// every format: with 64 pairs an expert the tiles of 16 are 10 to 30 % faster, with 128 those of 128 up to 20 %, with
-// 512 up to 40 %.
-int64_t experts_tile_rows(int64_t pairs, int64_t E) { return pairs >= 96 * E ? 128 : 16; }
+// Rows a tile: 16, and 128 from 64 pairs an expert on.  Measured with 64 experts of 1536 x 2048 and 128 of 2048 x 768 (us with
+// tiles of 16 and of 128): 48 pairs an expert Q1_0 56 and 66, 63 and 73, Q2_0 60 and 67, 76 and 79, Q4_0 75 and 76, 93 and 84;
+// 64 pairs 69 and 72, 82 and 82, 75 and 72, 97 and 91, 92 and 83, 116 and 94; 80 pairs 85 and 81 to 139 and 103.
+int64_t experts_tile_rows(int64_t pairs, int64_t E) { return pairs >= 64 * E ? 128 : 16; }
 int64_t experts_max_tiles(int64_t pairs, int64_t E) { return pairs / experts_tile_rows(pairs, E) + (pairs < E ? pairs : E); }
 
 hipError_t launch_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, int32_t *plan, hipStream_t s)

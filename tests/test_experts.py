@@ -94,7 +94,7 @@ def test_plan(pairs, E):
         ok = (which >= 0) & (which < E)
         want = np.argsort(np.where(ok, which, E), kind="stable")[:ok.sum()]
         assert p[1] == ok.sum()
-        size = 128 if pairs >= 96 * E else 16
+        size = 128 if pairs >= 64 * E else 16  # rows a tile
         n = pairs // size + min(pairs, E)
         tiles, places = p[4:4 + 2 * n].reshape(-1, 2), p[4 + (2 * n + 3) // 4 * 4:][:n * size].reshape(n, size)
         assert (tiles[p[0]:, 1] == 0).all() and (tiles[:, 1] >= 0).all()
@@ -173,7 +173,7 @@ def test_few_rows(fmt, E, N, K, n, per):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
-@pytest.mark.parametrize("E,N,K,n,per", [(1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4), (40, 1000, 1152, 500, 1), (20, 1000, 1408, 150, 2)])
+@pytest.mark.parametrize("E,N,K,n,per", [(1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (8, 130, 384, 400, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4), (40, 1000, 1152, 500, 1), (20, 1000, 1408, 150, 2)])
 def test_many_rows(fmt, E, N, K, n, per):
     say(f"case many rows {W.NAMES[fmt]} E={E} N={N} K={K} pairs={n} per={per}")
     layer = Layer(fmt, E, N, K)
@@ -207,7 +207,7 @@ def test_a_plan_of_other_pairs_stays_inside():
     layer = Layer(L.Q2_0_G64, 4, 40, 256)
     n = 30
     q, s = W.random_rows(np.random.default_rng(0), n, 256)
-    for pairs in (n, 70):  # few and many rows an expert
+    for pairs in (n, 70, 300):  # few and many rows an expert
         q, s = W.random_rows(np.random.default_rng(0), pairs, 256)
         for fill in (0x7F, 0xFF, 0x01, 0x00):
             plan = torch.full((L.lowbit_experts_plan_bytes(pairs, 4),), fill, dtype=torch.uint8, device="cuda")
