@@ -335,7 +335,7 @@ lb_status lowbit_kv_read(int dtype, const void *cache, int64_t pages, int64_t pa
  *   a = positions[t] * inv_freq[i],  (x, y) -> factor * (x cos a - y sin a,  y cos a + x sin a)
  * inv_freq: device fp32 [rotary_dim / 2]; whatever scaling of long contexts a model has is in them and in factor.
  * Angles, sines and products are in 64 bits; a turned element is rounded to fp32 and then to dtype.  The cache's bytes are
- * those of turning first and lowbit_kv_append.  q_out may be q, with the same stride, but not overlap it otherwise;
+ * those of turning first and lowbit_kv_append.  q_out may be q, with the same stride, but not overlap it otherwise, nor k, v;
  * q_heads may be 0 (q and q_out are not used then).  A row whose slot is negative or past the cache is left out: neither
  * cache nor q_out change.  T * (q_heads + kv_heads) * head_dim below about 2^35, and at most 65535 heads in all.
  */

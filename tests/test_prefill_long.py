@@ -1,5 +1,6 @@
-"""Prefill products whose activations exceed an XCD's L2 (M * K over 4 MiB), where workgroups take their tiles in another
-order: sampled rows against 64 bits, and every row against the product of fewer rows."""
+"""Prefill products: those whose activations exceed an XCD's L2 (M * K over 4 MiB), where workgroups take their tiles in
+another order (sampled rows against 64 bits, and every row against the product of fewer rows), and outputs that are aligned
+to 4 bytes only."""
 import numpy as np
 import pytest
 import torch
@@ -53,3 +54,46 @@ def test_rows_as_with_fewer(fmt, M, N, K):
         L.lowbit_gemm(fmt, w, N, K, 1.0, act, q[a:a + n].contiguous(), s[a:a + n].contiguous(), n, parts[a:a + n])
     assert (whole[M] == 5).all() and torch.isfinite(parts).all()
     assert torch.equal(whole[:M], parts)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [L.Q1_0, L.Q2_0_G64, L.Q8_0, L.Q4_0, L.TERNARY_PLANAR])
+def test_outputs_that_lie_on_4_bytes(fmt):
+    """Outputs one to three elements off 16 bytes, rows of every remainder: the values of aligned ones, and nothing beside."""
+    planar = fmt == L.TERNARY_PLANAR
+    for M, N, K in ((300, 16001, 128), (129, 130, 384), (40, 67, 256), (600, 2600, 128)):
+        say(f"case outputs on 4 bytes fmt={fmt} M={M} N={N} K={K}")
+        g = torch.Generator(device="cuda").manual_seed(N)
+        w = torch.randint(0, 60, (L.lowbit_weight_bytes(fmt, N, K),), dtype=torch.uint8, generator=g, device="cuda")
+        q = torch.randint(-127, 128, (M, K), dtype=torch.int8, generator=g, device="cuda")
+        s = torch.rand(M, device="cuda") if planar else torch.rand(M, K // 32, device="cuda").half()
+        act = L.ACT_I8_ROW if planar else L.ACT_Q8_0
+        want = torch.zeros(M, N, device="cuda")
+        L.lowbit_gemm(fmt, w, N, K, 1.0, act, q, s, M, want)
+        for off in (1, 2, 3):
+            buf = torch.full((off + M * N + 5,), 5.0, device="cuda")
+            L.lowbit_gemm(fmt, w, N, K, 1.0, act, q, s, M, buf[off:off + M * N])
+            assert torch.equal(buf[off:off + M * N].view(M, N), want)
+            assert (buf[:off] == 5).all() and (buf[off + M * N:] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [L.Q1_0, L.Q2_0_G64, L.Q4_0])
+@pytest.mark.parametrize("pairs", [30, 250])
+def test_experts_outputs_that_lie_on_4_bytes(fmt, pairs):
+    E, N, K = 3, 333, 384
+    say(f"case experts' outputs on 4 bytes fmt={fmt} pairs={pairs}")
+    g = torch.Generator(device="cuda").manual_seed(pairs)
+    w = torch.randint(0, 60, (L.lowbit_experts_weight_bytes(fmt, E, N, K),), dtype=torch.uint8, generator=g, device="cuda")
+    e = torch.randint(-1, E, (pairs,), dtype=torch.int32, generator=g, device="cuda")
+    q = torch.randint(-127, 128, (pairs, K), dtype=torch.int8, generator=g, device="cuda")
+    s = torch.rand(pairs, K // 32, generator=g, device="cuda").half()
+    plan = torch.zeros(L.lowbit_experts_plan_bytes(pairs, E), dtype=torch.uint8, device="cuda")
+    L.lowbit_experts_plan(e, pairs, E, plan)
+    want = torch.full((pairs, N), 5.0, device="cuda")
+    L.lowbit_experts_matmul(fmt, w, E, N, K, q, s, e, pairs, 1, want, plan=plan)
+    for off in (1, 2, 3):
+        buf = torch.full((off + pairs * N + 5,), 5.0, device="cuda")
+        L.lowbit_experts_matmul(fmt, w, E, N, K, q, s, e, pairs, 1, buf[off:off + pairs * N], plan=plan)
+        assert torch.equal(buf[off:off + pairs * N].view(pairs, N), want)
+        assert (buf[:off] == 5).all() and (buf[off + pairs * N:] == 5).all() and (want[e < 0] == 5).all()
