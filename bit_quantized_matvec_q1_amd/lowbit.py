@@ -322,6 +322,9 @@ def _row_arg(t, name, dtype, T, heads, D, stride):
     """Rows [T][heads][D]: (address, token stride).  A tensor may be a part of wider rows (any token stride, the
     row itself dense); an address takes `stride`, dense rows by default."""
     width = heads * D if heads > 0 and D > 0 else 0
+    if (stride is None and isinstance(t, _Tensor) and t.shape == (T, heads, D) and t.is_contiguous() and t.dtype is _DTYPES.get(dtype)
+            and T and width):  # as nearly always
+        return t.data_ptr(), width
     if t is None or isinstance(t, int):
         return t, width if stride is None else int(stride)
     if not isinstance(t, _Tensor):
