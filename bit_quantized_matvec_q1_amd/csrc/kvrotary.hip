@@ -10,10 +10,10 @@
 // The rows are what has to move, but 64 bits cost more than their bytes if done carelessly: sines computed again for every
 // head, elements converted twice.  Hence the split: a workgroup takes 2048 / D tokens and a run of heads (queries, or keys
 // and values), and computes the tokens' sines and cosines once, spread over its threads, through LDS.  A lane of a query has
-// four whole pairs, four elements of either half of the turned part, and keeps their sines over the heads; the next head's
+// four whole pairs, four elements of either half of the turned part, and keeps their sines over the heads; the next heads'
 // elements are loaded ahead.  (Keys are written by lanes of eight consecutive elements, which read the other half's again.)
 //
-// Measured: 16384 bf16 rows of 32 query and 2 x 8 key and value heads of 128: 84 to 93 us, 355 MB, 3.8 to 4.2 TB/s of the 5.1
+// Measured: 16384 bf16 rows of 32 query and 2 x 8 key and value heads of 128: 78 to 86 us, 355 MB, 4.1 to 4.5 TB/s of the 5.1
 // that a large copy reaches (120 us with sines by head and the library's functions); 32 fp32 rows 6 us.
 #include "kvcache_device.h"
 
@@ -59,7 +59,7 @@ template <int DT> __device__ __forceinline__ void put2(typename RowType<DT>::T *
     }
 }
 
-template <int DT, int D> __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int shift, int q_runs, int q_per, int kv_per)
+template <int DT, int D, int H> __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int shift, int q_runs, int q_per, int kv_per)
 {
     using R = RowType<DT>;
     using T = typename R::T;
@@ -90,9 +90,16 @@ template <int DT, int D> __global__ __launch_bounds__(256) void rotary_kernel(Ro
         const T *from = static_cast<const T *>(a.q) + t * a.q_stride;
         T *to = static_cast<T *>(a.q_out) + t * a.q_out_stride;
         using V = RowVec<DT, 4>;
-        V v0 = {}, v1 = {};
+        V v0[H] = {}, v1[H] = {};
+        auto load = [&](int h) {
+#pragma unroll
+            for (int i = 0; i < H; i++) {
+                const int hn = min(h + i, h1 - 1);
+                v0[i] = *reinterpret_cast<const V *>(from + hn * D + e0), v1[i] = *reinterpret_cast<const V *>(from + hn * D + e1);
+            }
+        };
         if (row)
-            v0 = *reinterpret_cast<const V *>(from + h0 * D + e0), v1 = *reinterpret_cast<const V *>(from + h0 * D + e1);
+            load(h0);
         sines();
         if (!row)
             return;
@@ -102,32 +109,41 @@ template <int DT, int D> __global__ __launch_bounds__(256) void rotary_kernel(Ro
             const double2 v = mine[turned ? 4 * at + j : 0];
             c[j] = v.x, s[j] = v.y;
         }
-        for (int h = h0; h < h1; h++) {
-            const V x0 = v0, x1 = v1;
-            const int hn = min(h + 1, h1 - 1);
-            v0 = *reinterpret_cast<const V *>(from + hn * D + e0), v1 = *reinterpret_cast<const V *>(from + hn * D + e1);
-            V o0 = x0, o1 = x1;
-            if (turned) {
-                float u[8];
-                if (a.pairs) { // uniform
+        for (int g = h0; g < h1; g += H) {
+            V w0[H], w1[H];
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const double x = (double)R::get((j < 2 ? x0 : x1).v[2 * j % 4]), y = (double)R::get((j < 2 ? x0 : x1).v[2 * j % 4 + 1]);
-                        u[2 * j] = (float)(x * c[j] - y * s[j]), u[2 * j + 1] = (float)(y * c[j] + x * s[j]);
-                    }
-                } else {
+            for (int i = 0; i < H; i++)
+                w0[i] = v0[i], w1[i] = v1[i];
+            load(g + H);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const double x = (double)R::get(x0.v[j]), y = (double)R::get(x1.v[j]);
-                        u[j] = (float)(x * c[j] - y * s[j]), u[4 + j] = (float)(y * c[j] + x * s[j]);
+            for (int i = 0; i < H; i++) {
+                const int h = g + i;
+                if (h >= h1)
+                    break;
+                const V x0 = w0[i], x1 = w1[i];
+                V o0 = x0, o1 = x1;
+                if (turned) {
+                    float u[8];
+                    if (a.pairs) { // uniform
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const double x = (double)R::get((j < 2 ? x0 : x1).v[2 * j % 4]), y = (double)R::get((j < 2 ? x0 : x1).v[2 * j % 4 + 1]);
+                            u[2 * j] = (float)(x * c[j] - y * s[j]), u[2 * j + 1] = (float)(y * c[j] + x * s[j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const double x = (double)R::get(x0.v[j]), y = (double)R::get(x1.v[j]);
+                            u[j] = (float)(x * c[j] - y * s[j]), u[4 + j] = (float)(y * c[j] + x * s[j]);
+                        }
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2)
+                        put2<DT>(o0.v + j, u[j], u[j + 1]), put2<DT>(o1.v + j, u[4 + j], u[5 + j]);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; j += 2)
-                    put2<DT>(o0.v + j, u[j], u[j + 1]), put2<DT>(o1.v + j, u[4 + j], u[5 + j]);
+                // (in place: a lane reads and writes its own elements only)
+                *reinterpret_cast<V *>(to + h * D + e0) = o0, *reinterpret_cast<V *>(to + h * D + e1) = o1;
             }
-            // (in place: a lane reads and writes its own elements only)
-            *reinterpret_cast<V *>(to + h * D + e0) = o0, *reinterpret_cast<V *>(to + h * D + e1) = o1;
         }
         return;
     }
@@ -185,9 +201,14 @@ template <int DT> static hipError_t rotary_d(const RotaryArgs &a, hipStream_t s)
     const int64_t per = (heads + runs - 1) / runs, q_per = per < a.q_heads ? per : a.q_heads, kv_per = per < a.kv_heads ? per : a.kv_heads;
     const int64_t q_runs = a.q_heads ? (a.q_heads + q_per - 1) / q_per : 0, kv_runs = (a.kv_heads + kv_per - 1) / kv_per;
     const dim3 grid((unsigned)groups, (unsigned)(q_runs + kv_runs));
+    // Long runs of heads load four heads ahead (16384 rows of 32 + 2 x 8 heads of 128: bf16 86 -> 78 us, fp32 163 -> 157), short
+    // ones one, which are done sooner (4096 fp16 rows of 40 heads: 23.6 us, 25.0 with four).
 #define LB_ROTARY(d)                                                                                          \
     case d:                                                                                                   \
-        hipLaunchKernelGGL((rotary_kernel<DT, d>), grid, dim3(256), 0, s, a, shift, (int)q_runs, (int)q_per, (int)kv_per);  \
+        if (per >= 8)                                                                                         \
+            hipLaunchKernelGGL((rotary_kernel<DT, d, 4>), grid, dim3(256), 0, s, a, shift, (int)q_runs, (int)q_per, (int)kv_per);  \
+        else                                                                                                  \
+            hipLaunchKernelGGL((rotary_kernel<DT, d, 1>), grid, dim3(256), 0, s, a, shift, (int)q_runs, (int)q_per, (int)kv_per);  \
         return hipGetLastError();
     switch (a.head_dim) {
         LB_ROTARY(64) LB_ROTARY(128) LB_ROTARY(256)
