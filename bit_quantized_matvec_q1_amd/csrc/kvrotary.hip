@@ -13,7 +13,7 @@
 // four whole pairs, four elements of either half of the turned part, and keeps their sines over the heads; the next heads'
 // elements are loaded ahead.  (Keys are written by lanes of eight consecutive elements, which read the other half's again.)
 //
-// Measured: 16384 bf16 rows of 32 query and 2 x 8 key and value heads of 128: 78 to 86 us, 355 MB, 4.1 to 4.5 TB/s of the 5.1
+// Measured: 16384 bf16 rows of 32 query and 2 x 8 key and value heads of 128: 76 to 84 us, 355 MB, 4.2 to 4.7 TB/s of the 5.1
 // that a large copy reaches (120 us with sines by head and the library's functions); 32 fp32 rows 6 us.
 #include "kvcache_device.h"
 
@@ -162,6 +162,12 @@ template <int DT, int D, int H> __global__ __launch_bounds__(256) void rotary_ke
     };
     ahead(h0);
     sines();
+    double c[8], s[8]; // of elements e + j, the sine with the sign that its product has (pairs: four, each twice)
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const double2 v = mine[!turned ? 0 : a.pairs ? 4 * at + j / 2 : first ? e + j : e - half + j];
+        c[j] = v.x, s[j] = (a.pairs ? (j & 1) == 0 : first) ? -v.y : v.y;
+    }
     for (int h = h0; h < h1; h++) { // uniform
         const V kx = k0, ko = k1, vx = v0;
         ahead(min(h + 1, h1 - 1));
@@ -173,10 +179,8 @@ template <int DT, int D, int H> __global__ __launch_bounds__(256) void rotary_ke
             float u[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const bool low = a.pairs ? (j & 1) == 0 : first;
-                const double2 v = mine[a.pairs ? 4 * at + j / 2 : first ? e + j : e - half + j];
-                const double x = (double)xk[j] * v.x, y = (double)R::get(a.pairs ? kx.v[j ^ 1] : ko.v[j]) * v.y;
-                u[j] = (float)(low ? x - y : x + y);
+                const double x = (double)xk[j] * c[j], y = (double)R::get(a.pairs ? kx.v[j ^ 1] : ko.v[j]) * s[j];
+                u[j] = (float)(x + y);
             }
             T w[8];
 #pragma unroll
@@ -201,7 +205,7 @@ template <int DT> static hipError_t rotary_d(const RotaryArgs &a, hipStream_t s)
     const int64_t per = (heads + runs - 1) / runs, q_per = per < a.q_heads ? per : a.q_heads, kv_per = per < a.kv_heads ? per : a.kv_heads;
     const int64_t q_runs = a.q_heads ? (a.q_heads + q_per - 1) / q_per : 0, kv_runs = (a.kv_heads + kv_per - 1) / kv_per;
     const dim3 grid((unsigned)groups, (unsigned)(q_runs + kv_runs));
-    // Long runs of heads load four heads ahead (16384 rows of 32 + 2 x 8 heads of 128: bf16 86 -> 78 us, fp32 163 -> 157), short
+    // Long runs of heads load four heads ahead (16384 rows of 32 + 2 x 8 heads of 128: 8 to 4 % faster), short
     // ones one, which are done sooner (4096 fp16 rows of 40 heads: 23.6 us, 25.0 with four).
 #define LB_ROTARY(d)                                                                                          \
     case d:                                                                                                   \
