@@ -1,26 +1,32 @@
 // The experts' products with up to 16 rows of activations a tile, on the int8 matrix cores.
 //
 // Between a decode step's one or two rows an expert, where nibble dot products on the vector unit keep up with HBM
-// (experts.hip), and a prompt's hundreds (gemm.hip) a product of 16 x 16 tiles reads the weights once for 16 rows: the rows
-// are the A operand (from LDS), 16 weight rows the B operand, unpacked in registers as they come from HBM.
-//  * Lane (n, q) = (lane mod 16, lane / 16) loads whole 16-byte records, record 4 s + q of weight row n.  The matrix product
-//    wants a q8_0 block's weights spread over the four q, so four records are transposed between the lanes' quarters, dword
-//    by dword (v_permlane32_swap, v_permlane16_swap: four instructions for four records).
+// (experts.hip), and a prompt's hundreds (gemm.hip) products of 16 x 16 read the weights once for 16 rows: the activations
+// are the A operand (from LDS), 16 weight rows the B operand, unpacked in registers as they come from HBM.  Lane (n, q) =
+// (lane mod 16, lane / 16) loads whole 16-byte records, record 4 s + q of weight row n.
 //  * The order of weights within a block is free, as long as the activations have the same: they are staged in the order in
 //    which shifts and masks isolate the weights' bytes, which needs no further arrangement.  Q4_0: nibbles in the upper
 //    halves of bytes, 16 w (the factor is in the activation scale); Q2_0_g64: codes w + 1; Q1_0: 2 bit = w + 1.  The sum of
 //    the activations that codes carry too much is subtracted by the accumulator's start.
-//  * A Q2_0_g64 dword belongs to one of its record's two q8_0 blocks: the 64-deep product is taken twice, with the other
-//    block's activations read as zeros.
 //  * Results are read as fp32 through the bias 1.5 * 2^23 as in gemm.hip: round(d_x * isum), then one multiply-add with the
-//    weight scale (one value a lane).
+//    weight scale (one value a lane).  That takes as long as anything else, and 16 x 16 results of which few are wanted
+//    would cost it in full.  Hence two ways:
+//  * Up to four rows (eight, of Q4_0 and Q2_0_g64, in two turns): the A operand's 16 rows are four rows times four records.
+//    Its row (j, r) has row r's activations where quarter j's record is, and zeros elsewhere, so that one product has the
+//    sums of four records, each lane those of its own record, as it was loaded; the quarters are added at the end.
+//  * More: the A operand's rows are 16 rows of activations.  A q8_0 block's weights have to be spread over the four q then, so
+//    four records are transposed between the lanes' quarters, dword by dword (v_permlane32_swap, v_permlane16_swap: four
+//    instructions for four records).  A Q2_0_g64 dword belongs to one of its record's two blocks: the 64-deep product is
+//    taken twice, with the other block's activations read as zeros.
 // A wave has G groups of 16 weight rows, so that what it reads from LDS (activations, scales, accumulator starts) is read
 // once for all of them.  lowbit_gemm takes the same kernel for Q4_0 products of few rows, whose tiles need no plan.
 //
-// What bounds it: loads while experts have few rows (360 pairs of 128 Q4_0 experts of 2048 x 768, 107 MB: 22 to 24 us, 4.5 to
-// 4.9 TB/s; a workgroup's start, plan to rows to LDS, beside its three steps of K), the vector unit with many (12 to 14 instructions for eight weights of a lane and 16 rows, eight of them the
-// rescale).  Two things made it: each row's scales staged through LDS by whole lines (read four at a time from memory, their
-// lines came through the caches again for every step, Q4_0 875 -> 577 us for 32768 pairs), and results in vector registers.
+// Measured (us, the first way against the second alone): 64 experts of 1536 x 2048 with half a pair each Q1_0 7.7 and 12.0,
+// Q2_0 8.5 and 14.4, Q4_0 12.1 and 15.4; 360 pairs of 128 experts of 2048 x 768 14.6 and 16.4, 14.6 and 18.4, 22.7 and 24.9 (107
+// MB of Q4_0: 4.7 TB/s; a workgroup's start, plan to rows to LDS, beside its three steps of K).  With many rows the vector
+// unit bounds it (12 to 14 instructions for eight weights of a lane and 16 rows, eight of them the rescale).  Two things made
+// that: each row's scales staged through LDS by whole lines (read four at a time from memory, their lines came through the
+// caches again for every step, Q4_0 875 -> 577 us for 32768 pairs), and results in vector registers.
 #include "matvec_tile.h"
 #include "serve_internal.h"
 
@@ -41,11 +47,13 @@ template <int FMT, int G, bool KS> struct __attribute__((aligned(16))) TileLds {
     static constexpr int BLOCKS = KC / QK8, RECORDS = KC / F<FMT>::SW, WROWS = (KS ? 16 : 64) * G;
     // a weight row's scales of the chunk, 8 bytes apart from the next row's (16 rows' reads of 8 bytes meet 16 pairs of banks)
     static constexpr int SCALES = RECORDS + 4;
-    uint32_t x[KC * TR / 4]; // Q4_0, Q1_0: [block][q][row] 8 bytes; Q2_0_g64: [record][q][row] 16 bytes
+    // Few rows: [four records][block][half][row / 4][record][row mod 4] 16 bytes.  Otherwise Q4_0, Q1_0: [block][q][row] 8
+    // bytes; Q2_0_g64: [record][q][row] 16 bytes.
+    uint32_t x[KC * TR / 4];
+    uint32_t zeros[F<FMT>::SW * TR]; // as many bytes as four records have there, so that both are read at the same offsets
     float dx[BLOCKS * TR];   // [block][row]
     int start[FMT == LB_Q4_0 ? 4 : BLOCKS * TR]; // accumulator starts, [block][row]
     uint16_t dw[WROWS * SCALES];
-    uint4 zero;
 };
 
 __device__ __forceinline__ uint32_t bperm(uint32_t s0, uint32_t s1, uint32_t sel) { return __builtin_amdgcn_perm(s0, s1, sel); }
@@ -73,11 +81,41 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&d)[4])
     d[2] = p[0], d[3] = p[1];
 }
 
-// Block b (32 columns from column 32 b of the chunk) of activation row r: 32 bytes and their scale.
-template <int FMT, typename Lds> __device__ __forceinline__ void stage_block(Lds &lds, int b, int r, uint4 lo, uint4 hi, float dx)
+// Four values a lane, summed over the lanes' quarters: value row_of(q) in quarter q
+__device__ __forceinline__ int row_of(int q) { return (q & 1) << 1 | q >> 1; }
+__device__ __forceinline__ float sum_quarters(const float (&v)[4])
 {
+    auto both = [](float a, float b, bool row) {
+        const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+        const auto p = row ? __builtin_amdgcn_permlane16_swap(x, y, false, false) : __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        return __uint_as_float((uint32_t)p[0]) + __uint_as_float((uint32_t)p[1]);
+    };
+    return both(both(v[0], v[1], false), both(v[2], v[3], false), true);
+}
+
+// Block b (32 columns from column 32 b of the chunk) of activation row r: 32 bytes, in the order in which the weights' bytes
+// are isolated, and their scale.
+template <int FMT, bool FEW, typename Lds> __device__ __forceinline__ void stage_block(Lds &lds, int b, int r, uint4 lo, uint4 hi, float dx)
+{
+    constexpr int BPR = F<FMT>::SW / QK8;
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (FMT == LB_Q2_0_G64) { // weights 16 q + 4 t + s at byte t of dword s
+    if (FEW) {
+        const int rec = b / BPR;
+        uint32_t *to = lds.x + (((rec >> 2) * BPR + b % BPR) * 2 * TR + (r >> 2 << 2)) * 16 + ((rec & 3) * 4 + (r & 3)) * 4;
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+            const uint32_t *e = w + 4 * m;
+            uint4 o;
+            if (FMT == LB_Q2_0_G64) { // weights 16 m + 4 t + i at byte t of dword i
+                const uint32_t lo01 = bperm(e[1], e[0], 0x05010400u), hi01 = bperm(e[1], e[0], 0x07030602u);
+                const uint32_t lo23 = bperm(e[3], e[2], 0x05010400u), hi23 = bperm(e[3], e[2], 0x07030602u);
+                o = make_uint4(bperm(lo23, lo01, 0x05040100u), bperm(lo23, lo01, 0x07060302u), bperm(hi23, hi01, 0x05040100u), bperm(hi23, hi01, 0x07060302u));
+            } else { // weights 16 m + 0, 2, 4, 6, then 1, 3, 5, 7, then eight further on
+                o = make_uint4(bperm(e[1], e[0], 0x06040200u), bperm(e[1], e[0], 0x07050301u), bperm(e[3], e[2], 0x06040200u), bperm(e[3], e[2], 0x07050301u));
+            }
+            *reinterpret_cast<uint4 *>(to + m * TR * 16) = o;
+        }
+    } else if (FMT == LB_Q2_0_G64) { // weights 16 q + 4 t + s at byte t of dword s
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const uint32_t *e = w + 4 * h;
@@ -103,34 +141,30 @@ template <int FMT, typename Lds> __device__ __forceinline__ void stage_block(Lds
         lds.start[b * TR + r] = (int)BIAS - sq;
 }
 
-// (Two waves a SIMD at the least: with 256 registers the matrix products' results are in vector registers; with more the
-// compiler has them in accumulator registers, which costs a move each.)
-template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 2) void experts_tile_kernel(ExpertsArgs a, int chunks)
+// Place r's pair
+__device__ __forceinline__ uint32_t pair_at(const ExpertsArgs &a, const int32_t *pairs, int tile, int r)
+{
+    return min(pairs ? (uint32_t)pairs[r] : (uint32_t)(TR * tile + r), (uint32_t)(a.pairs - 1));
+}
+
+// The main loop, for tiles of up to 4 NG rows.
+template <int FMT, int G, bool WHOLE, bool KS, int NG>
+__device__ __forceinline__ void tile_rows(const ExpertsArgs &a, TileLds<FMT, G, KS> &lds, const uint8_t *W, int chunk, int rows, uint32_t row16,
+                                          const int32_t *pairs, int tile)
 {
     using Lds = TileLds<FMT, G, KS>;
-    __shared__ Lds lds;
     constexpr int BPR = F<FMT>::SW / QK8; // q8_0 blocks a record
-    const int chunk = blockIdx.x % chunks, tile = blockIdx.x / chunks;
-    // without a plan the rows are those of one matrix product, one after another
-    const int2 t = a.plan ? *reinterpret_cast<const int2 *>(a.plan + experts_tile_at(tile)) : make_int2(0, a.pairs - TR * tile);
-    const int32_t *pairs = a.plan ? a.plan + experts_pairs_at(a.max_tiles, tile, TR) : nullptr;
-    auto pair_at = [&](int r) { return min(pairs ? (uint32_t)pairs[r] : (uint32_t)(TR * tile + r), (uint32_t)(a.pairs - 1)); };
-    // staging: a thread has blocks tid / TR, and so on by 256 / TR, of activation row tid mod TR (a place without a pair reads
-    // some row, and is not stored)
-    constexpr int BSTEP = WG / TR, U = Lds::BLOCKS / BSTEP;
-    const int sr = threadIdx.x % TR, sb = threadIdx.x / TR;
-    const int64_t row = pair_at(sr) / (uint32_t)a.per_row;
-    const int rows = min(t.y, TR);
-    if ((unsigned)t.x >= (unsigned)a.E || rows < 1)
-        return; // no tile, or no plan of these pairs
-    const uint8_t *W = a.W + t.x * a.expert_bytes;
+    constexpr bool FEW = NG < 4;
+    constexpr int ROWS = 4 * NG, STEP4 = F<FMT>::SW * TR; // dwords of four records' activations
     const int ns = a.K / F<FMT>::SW;
     const uint8_t *scales = W + (int64_t)a.N * ns * CODE_BYTES;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
     const int wrow = (KS ? 0 : wave * G * 16) + (lane & 15); // this lane's weight row of the workgroup's, in group 0
     const int n0 = chunk * Lds::WROWS + wrow;
-    if (threadIdx.x == 0)
-        lds.zero = make_uint4(0, 0, 0, 0);
+    // staging: a thread has blocks tid / ROWS, and so on by 256 / ROWS, of activation row tid mod ROWS
+    constexpr int BSTEP = WG / ROWS, U = (Lds::BLOCKS + BSTEP - 1) / BSTEP;
+    const int sr = threadIdx.x % ROWS, sb = threadIdx.x / ROWS;
+    const int64_t row = (uint32_t)__shfl((int)row16, sr);
 
     uint32_t rec0[G]; // first record of the lane's rows
 #pragma unroll
@@ -151,8 +185,69 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
                 r.code[h][g] = make_uint4(c.x, c.y, c.z, c.w);
             }
     };
-    float acc[G][4] = {};
-    auto compute = [&](const uint4 (&code)[G], int s, int first) { // records 4 s .. 4 s + 3; first: the chunk's first
+    // The activations that this lane gives a product: row lane mod 4 of its quarter's record, or zeros.
+    const bool live = ((lane & 15) >> 2) == q;
+    const uint32_t xat = live ? (uint32_t)(4 * (lane & 15)) : (uint32_t)(lds.zeros - lds.x);
+    float acc[FEW ? NG : 1][G][4] = {};
+    auto compute_few = [&](const uint4 (&code)[G], int s, int first) { // records 4 s .. 4 s + 3; first: the chunk's first
+        const int own = min(4 * s + q, ns - 1) - first; // this quarter's record, of the chunk's
+        float dw[G];
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            dw[g] = half_bits_to_float(lds.dw[(wrow + g * 16) * Lds::SCALES + own]);
+            if (!WHOLE)
+                dw[g] = 4 * s + q < ns ? dw[g] : 0.0f; // no record: its sums count nothing
+        }
+        const uint32_t *x = lds.x + (xat + (live ? (uint32_t)((4 * s - first) / 4 * STEP4) : 0u));
+#pragma unroll
+        for (int b = 0; b < BPR; b++) {
+            v4i w[G][2];
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const uint32_t v[4] = {code[g].x, code[g].y, code[g].z, code[g].w};
+#pragma unroll
+                for (int m = 0; m < 2; m++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        uint32_t o;
+                        if (FMT == LB_Q2_0_G64) { // codes i, 4 + i, 8 + i, 12 + i
+                            o = (v[2 * b + m] >> (2 * i)) & 0x03030303u;
+                        } else {
+                            const uint32_t d = v[2 * m + (i >> 1)];
+                            if (FMT == LB_Q4_0) // even nibbles, odd nibbles
+                                o = (i & 1 ? d : d << 4) & 0xF0F0F0F0u;
+                            else // the sign of block b, at bit b of each nibble, moved to bit 1
+                                o = (i & 1 ? d >> (b + 3) : b ? d >> (b - 1) : d << 1) & 0x02020202u;
+                        }
+                        w[g][m][i] = (int)o;
+                    }
+            }
+#pragma unroll
+            for (int r = 0; r < NG; r++) {
+                const v4i x0 = *reinterpret_cast<const v4i *>(x + b * 512 + r * 64), x1 = *reinterpret_cast<const v4i *>(x + b * 512 + 256 + r * 64);
+                const int at = (own * BPR + b) * TR + 4 * r;
+                const float4 dx = *reinterpret_cast<const float4 *>(lds.dx + at);
+                v4i start = {(int)BIAS, (int)BIAS, (int)BIAS, (int)BIAS};
+                if (FMT != LB_Q4_0)
+                    start = *reinterpret_cast<const v4i *>(lds.start + at);
+                const float dxv[4] = {dx.x, dx.y, dx.z, dx.w};
+                float c[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    c[i] = -dxv[i] * BIASF; // exact: an 11-bit significand times 3 * 2^22
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    v4i D = __builtin_amdgcn_mfma_i32_16x16x64_i8(x0, w[g][0], start, 0, 0, 0);
+                    D = __builtin_amdgcn_mfma_i32_16x16x64_i8(x1, w[g][1], D, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        acc[r][g][i] = fmaf(dw[g], fmaf(dxv[i], __int_as_float(D[i]), c[i]), acc[r][g][i]); // round(d_x * isum)
+                }
+            }
+        }
+    };
+
+    auto compute_16 = [&](const uint4 (&code)[G], int s, int first) { // the same
         uint32_t d[G][4];
         uint2 sc[G];
 #pragma unroll
@@ -200,7 +295,7 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
                 v4i xw = {};
                 long xb = 0;
                 if (FMT == LB_Q2_0_G64) {
-                    const uint32_t *p = (q >> 1) == b ? lds.x + r0 * 256 + lane * 4 : reinterpret_cast<const uint32_t *>(&lds.zero);
+                    const uint32_t *p = (q >> 1) == b ? lds.x + r0 * 256 + lane * 4 : lds.zeros;
                     xw = *reinterpret_cast<const v4i *>(p);
                 } else {
                     xb = *reinterpret_cast<const long *>(lds.x + (r0 * BPR + b) * 128 + lane * 2);
@@ -226,7 +321,7 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
             for (int g = 0; g < G; g++)
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    acc[g][i] = fmaf(dw[g], tg[g][i], acc[g][i]);
+                    acc[0][g][i] = fmaf(dw[g], tg[g][i], acc[0][g][i]);
         };
         if (4 * s + 4 <= ns) { // uniform: in one piece, so that one record's loads from LDS go out in another's arithmetic
 #pragma unroll
@@ -283,7 +378,7 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
 #pragma unroll
         for (int v = 0; v < U; v++)
             if (sb + BSTEP * v < nblk)
-                stage_block<FMT>(lds, sb + BSTEP * v, sr, lo[v], hi[v], half_bits_to_float((uint16_t)sc[v]));
+                stage_block<FMT, FEW>(lds, sb + BSTEP * v, sr, lo[v], hi[v], half_bits_to_float((uint16_t)sc[v]));
 #pragma unroll
         for (int v = 0; v < P; v++) {
             const int p = threadIdx.x + v * WG;
@@ -299,11 +394,17 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
     auto step = [&](const Regs &r, int s, int first) {
 #pragma unroll
         for (int h = 0; h < H; h++)
-            if (h == 0 || 4 * (H * s + h) < ns) // uniform
-                compute(r.code[h], H * s + h, first);
+            if (h == 0 || 4 * (H * s + h) < ns) { // uniform
+                if constexpr (FEW)
+                    compute_few(r.code[h], H * s + h, first);
+                else
+                    compute_16(r.code[h], H * s + h, first);
+            }
     };
     Regs buf[2];
     load_chunk(0);
+    for (int i = threadIdx.x; i < STEP4; i += WG) // (a barrier follows)
+        lds.zeros[i] = 0;
     if constexpr (KS) {
         // the waves have the same weight rows and a step of every chunk each, and add up what they have at the end
         const int mine = min(wave, SPC - 1), chunks_k = (steps + SPC - 1) / SPC;
@@ -321,22 +422,6 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
             }
         }
         chunk_barrier();
-        float *sums = reinterpret_cast<float *>(lds.x); // [wave][group][4][lane]
-        static_assert(sizeof(lds.x) >= 4 * (WG / 64) * G * 4 * 64, "the waves' sums");
-#pragma unroll
-        for (int g = 0; g < G; g++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                sums[((wave * G + g) * 4 + i) * 64 + lane] = acc[g][i];
-        __syncthreads();
-        if (wave)
-            return;
-#pragma unroll
-        for (int g = 0; g < G; g++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                for (int w = 1; w < WG / 64; w++)
-                    acc[g][i] += sums[((w * G + g) * 4 + i) * 64 + lane];
     } else {
         issue(buf[0], 0);
         for (int s = 0; s < steps; s += 2) {
@@ -352,15 +437,63 @@ template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 
             }
         }
     }
+    // FEW: the four quarters' sums, row row_of(q) of each four in quarter q; otherwise quarter q has rows 4 q to 4 q + 3
+    float sum[NG][G];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = 4 * q + i;
-        const int64_t pair = pair_at(r);
+    for (int r = 0; r < NG; r++)
 #pragma unroll
         for (int g = 0; g < G; g++)
-            if (r < rows && n0 + 16 * g < a.N)
-                a.y[pair * a.N + n0 + 16 * g] = acc[g][i];
+            sum[r][g] = FEW ? sum_quarters(acc[FEW ? r : 0][g]) : acc[0][g][r];
+    if constexpr (KS) { // and the waves'
+        float *sums = reinterpret_cast<float *>(lds.x); // [wave][four rows][group][lane]
+        static_assert(sizeof(lds.x) >= 4 * (WG / 64) * NG * G * 64, "the waves' sums");
+#pragma unroll
+        for (int r = 0; r < NG; r++)
+#pragma unroll
+            for (int g = 0; g < G; g++)
+                sums[((wave * NG + r) * G + g) * 64 + lane] = sum[r][g];
+        __syncthreads();
+        if (wave)
+            return;
+#pragma unroll
+        for (int r = 0; r < NG; r++)
+#pragma unroll
+            for (int g = 0; g < G; g++)
+                for (int w = 1; w < WG / 64; w++)
+                    sum[r][g] += sums[((w * NG + r) * G + g) * 64 + lane];
     }
+#pragma unroll
+    for (int r = 0; r < NG; r++) {
+        const int at = FEW ? 4 * r + row_of(q) : 4 * q + r;
+        const int64_t pair = pair_at(a, pairs, tile, at);
+#pragma unroll
+        for (int g = 0; g < G; g++)
+            if (at < rows && n0 + 16 * g < a.N)
+                a.y[pair * a.N + n0 + 16 * g] = sum[r][g];
+    }
+}
+
+// (Two waves a SIMD at the least: with 256 registers the matrix products' results are in vector registers; with more the
+// compiler has them in accumulator registers, which costs a move each.)
+template <int FMT, int G, bool WHOLE, bool KS> __global__ __launch_bounds__(WG, 2) void experts_tile_kernel(ExpertsArgs a, int chunks)
+{
+    __shared__ TileLds<FMT, G, KS> lds;
+    const int chunk = blockIdx.x % chunks, tile = blockIdx.x / chunks;
+    // without a plan the rows are those of one matrix product, one after another
+    const int2 t = a.plan ? *reinterpret_cast<const int2 *>(a.plan + experts_tile_at(tile)) : make_int2(0, a.pairs - TR * tile);
+    const int32_t *pairs = a.plan ? a.plan + experts_pairs_at(a.max_tiles, tile, TR) : nullptr;
+    // place lane mod 16's activation row (a place without a pair reads some row, and is not stored)
+    const uint32_t row16 = pair_at(a, pairs, tile, threadIdx.x % TR) / (uint32_t)a.per_row;
+    const int rows = min(t.y, TR);
+    if ((unsigned)t.x >= (unsigned)a.E || rows < 1)
+        return; // no tile, or no plan of these pairs
+    const uint8_t *W = a.W + t.x * a.expert_bytes;
+    if (rows <= 4)
+        tile_rows<FMT, G, WHOLE, KS, 1>(a, lds, W, chunk, rows, row16, pairs, tile);
+    else if (FMT != LB_Q1_0 && rows <= 8) // (Q1_0, whose unpacking is most of a second turn: 64 experts of 1536 x 2048 18.7 and 20.3)
+        tile_rows<FMT, G, WHOLE, KS, 2>(a, lds, W, chunk, rows, row16, pairs, tile);
+    else
+        tile_rows<FMT, G, WHOLE, KS, 4>(a, lds, W, chunk, rows, row16, pairs, tile);
 }
 
 template <int FMT, int G, bool KS> hipError_t tile_g(const ExpertsArgs &a, hipStream_t s)

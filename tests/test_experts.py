@@ -184,6 +184,21 @@ def test_many_rows(fmt, E, N, K, n, per):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
+@pytest.mark.parametrize("N,K", [(20, 1152), (600, 384), (1500, 2304), (1700, 1152), (50, 6912), (1700, 128)])
+def test_every_number_of_rows(fmt, N, K):
+    """Experts with one pair to 19: tiles of every number of rows, in each of the product's forms."""
+    E = 19
+    if fmt == L.Q2_0_G64 and K > 1000:
+        K += 64 * (1 + N % 3)  # rows of every remainder of blocks
+    say(f"case every number of rows {W.NAMES[fmt]} N={N} K={K}")
+    layer = Layer(fmt, E, N, K)
+    e = np.repeat(np.arange(E, dtype=np.int32), np.arange(1, E + 1))
+    np.random.default_rng(N).shuffle(e)
+    layer.check(e, 1, planned(e, E))
+
+
+@pytest.mark.gpu
 def test_odd_numbers_of_blocks():
     """Q2_0_g64 rows of an odd number of 64-weight blocks, few and many."""
     for n in (5, 90):
