@@ -701,7 +701,7 @@ hipError_t launch_gemm(int fmt, const uint8_t *W, int64_t N, int64_t K, float w_
 {
     const bool emit = sums != nullptr;
     // Few rows, or few weight rows: tiles of 16 rows (experts_tile.hip), as one expert's.  Measured: 2 rows of 4096 x 4096
-    // 9 us so and 29 here, 128 22 and 31; 64 of 12288 x 4096 28 and 30, 96 41 and 31; 192 of 4096 x 12288 75 and 84.
+    // 5.6 us so and 29 here, 128 22 and 30; 64 of 12288 x 4096 29 and 31, 96 42 and 32; 192 of 4096 x 12288 76 and 82.
     if (fmt == LB_Q4_0 && !emit && (M + 15) / 16 * ((N + 63) / 64) <= 768) {
         ExpertsArgs a = {};
         a.W = W, a.E = 1, a.N = (int32_t)N, a.K = (int32_t)K, a.pairs = (int32_t)M, a.per_row = 1, a.max_tiles = (M + 15) / 16;

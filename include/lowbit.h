@@ -419,8 +419,8 @@ lb_status lowbit_experts_plan(const int32_t *experts, int64_t pairs, int64_t E, 
  * pair has its own (its last).  fmt LB_Q1_0, LB_Q2_0_G64 or LB_Q4_0 (others LB_EUNSUPPORTED); xq int8
  * [ceil(pairs / pairs_per_row)][K] and xscale binary16 [..][K/32] are q8_0 rows (lowbit_quantize_act); y fp32 [pairs][N].
  * With a plan, weights are read once for up to 16 or 128 rows, and `experts` is not read; without (NULL), each pair is
- * computed by itself, with lowbit_matvec's results, which is best for a single token and up to about one pair an expert
- * (two of Q1_0 or Q2_0_g64).  Integer block sums are exact and scaled as lowbit_matvec does, in an order that depends on
+ * computed by itself, with lowbit_matvec's results, which is best for a single token and up to about half a pair an
+ * expert.  Integer block sums are exact and scaled as lowbit_matvec does, in an order that depends on
  * the sizes and on how many pairs an expert has.
  * Limits: K a multiple of 128 (64 for LB_Q2_0_G64), at most 32768 (16384 for LB_Q4_0); xq below 4 GiB.
  */
