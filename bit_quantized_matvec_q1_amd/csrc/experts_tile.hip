@@ -40,8 +40,6 @@ constexpr uint32_t BIAS = 0x4B400000u; // 1.5 * 2^23 as fp32 bits
 constexpr float BIASF = 12582912.0f;
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef unsigned v2u_a2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef __attribute__((address_space(1))) const v2u_a2 gv2u_a2;
 
 template <int FMT, int G, bool KS> struct __attribute__((aligned(16))) TileLds {
     static constexpr int BLOCKS = KC / QK8, RECORDS = KC / F<FMT>::SW, WROWS = (KS ? 16 : 64) * G;
