@@ -12,8 +12,9 @@
 //    double-buffered LDS -- the weights unpacked to int8 in natural column order (shift and mask, a 4x4
 //    byte transpose with v_perm_b32, and a v_perm_b32 lookup from code to weight byte: Q2_0 c -> c - 1,
 //    Q1_0 bit -> +/-1, planar (pos, neg) -> pos - neg; Q8_0 weights are int8 already and copied as they
-//    are; a Q4_0 nibble w, moved to its byte's upper half, is the int8 16 w, whose factor the activation scale takes back) -- and one barrier per step separates the writes from the reads.  Every thread loads and
-//    unpacks an equal share of the weight tile and issues an equal share of the activation tile.
+//    are; a Q4_0 nibble w, moved to its byte's upper half, is the int8 16 w, whose factor the activation
+//    scale takes back) -- and one barrier per step separates the writes from the reads.  Every thread loads
+//    and unpacks an equal share of the weight tile and issues an equal share of the activation tile.
 //  * A workgroup is 8 waves (512 threads), two per SIMD, and two workgroups fit a CU.  Wave w computes
 //    the 32 x 32 output tile (weight rows 32 (w mod 2), activation rows 32 (w / 2)) over every step's
 //    four q8_0 blocks (32 columns each, the MFMA's K depth): per block one A operand (weights) and one B

@@ -173,7 +173,9 @@ def test_few_rows(fmt, E, N, K, n, per):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
-@pytest.mark.parametrize("E,N,K,n,per", [(1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (8, 130, 384, 400, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4), (40, 1000, 1152, 500, 1), (20, 1000, 1408, 150, 2)])
+@pytest.mark.parametrize("E,N,K,n,per", [
+    (1, 1, 128, 17, 1), (2, 65, 256, 200, 2), (8, 130, 384, 700, 7), (8, 130, 384, 400, 7), (3, 300, 2048, 600, 1), (60, 64, 128, 1000, 4),
+    (40, 1000, 1152, 500, 1), (20, 1000, 1408, 150, 2)])
 def test_many_rows(fmt, E, N, K, n, per):
     say(f"case many rows {W.NAMES[fmt]} E={E} N={N} K={K} pairs={n} per={per}")
     layer = Layer(fmt, E, N, K)
