@@ -303,6 +303,8 @@ lb_status lowbit_route(int dtype, const void *logits, int64_t stride, int64_t T,
         return lb::abi_fail(LB_ESHAPE, fn, "groups must be a divisor of E up to 64, groups_kept from 1 to groups, group_best 1 or 2");
     if (top_k < 1 || top_k > 64 || top_k > E / groups * groups_kept)
         return lb::abi_fail(LB_ESHAPE, fn, "top_k must be from 1 to 64, and at most the experts of the groups kept");
+    if (lb::route_blocks(T, E, groups) >= (1 << 24)) // a launch's threads are numbered in 32 bits
+        return lb::abi_fail(LB_ESHAPE, fn, "over 2^26 - 4 tokens with more than 256 experts or 32 groups");
     if (stride < E)
         return lb::abi_fail(LB_ESHAPE, fn, "a row stride is shorter than the row");
     if (T == 0)

@@ -268,10 +268,12 @@ template <int DT, int LT, int NE> hipError_t route_n(const RouteArgs &a, hipStre
     return hipGetLastError();
 }
 
+// two tokens a wave from 1024 tokens on, where their experts are at most eight a lane
+bool two_a_wave(int64_t T, int64_t E, int64_t groups) { return T >= 1024 && E <= 256 && groups <= 32; }
+
 template <int DT> hipError_t route_d(const RouteArgs &a, hipStream_t s)
 {
-    // two tokens a wave from 1024 tokens on, where their experts are at most eight a lane
-    if (a.T >= 1024 && a.E <= 256 && a.groups <= 32)
+    if (two_a_wave(a.T, a.E, a.groups))
         return a.E <= 32 ? route_n<DT, 32, 1>(a, s) : a.E <= 64 ? route_n<DT, 32, 2>(a, s) : a.E <= 128 ? route_n<DT, 32, 4>(a, s) : route_n<DT, 32, 8>(a, s);
     return a.E <= 64    ? route_n<DT, 64, 1>(a, s)
            : a.E <= 128 ? route_n<DT, 64, 2>(a, s)
@@ -281,6 +283,12 @@ template <int DT> hipError_t route_d(const RouteArgs &a, hipStream_t s)
 }
 
 } // namespace
+
+int64_t route_blocks(int64_t T, int64_t E, int64_t groups)
+{
+    const int64_t tokens = two_a_wave(T, E, groups) ? 2 * WAVES : WAVES;
+    return (T + tokens - 1) / tokens;
+}
 
 hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s)
 {

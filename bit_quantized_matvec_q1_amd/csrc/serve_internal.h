@@ -120,6 +120,7 @@ struct RouteArgs {
     int32_t *experts;
     float *weights;
 };
+int64_t route_blocks(int64_t T, int64_t E, int64_t groups); // workgroups (of 256) of launch_route
 hipError_t launch_route(int dtype, const RouteArgs &a, hipStream_t s);
 
 // The routed pairs by expert (include/lowbit.h, lowbit_experts_plan), in tiles of R = experts_tile_rows() places, of one

@@ -392,7 +392,7 @@ lb_status lowbit_kv_attention(int dtype, const void *q, int64_t q_stride, int64_
  * Scores, sums and comparisons are in 64 bits, weights rounded to fp32 once.  A NaN logit counts as -inf, and a softmax of
  * logits of -inf alone is that of equal ones; of infinite ones, those share it; a p + bias that is NaN or -inf comes last.
  * count: device int32, NULL for T; tokens from count[0] on (a padded step's; the last of lowbit_kv_plan's cu_q is that
- * number) get experts -1 and weights 0.  T below 2^26.
+ * number) get experts -1 and weights 0.  T below 2^26, and at most 2^26 - 4 with more than 256 experts or 32 groups.
  */
 typedef enum { LB_SCORE_SOFTMAX = 0, LB_SCORE_SIGMOID = 1 } lb_score;
 lb_status lowbit_route(int dtype, const void *logits, int64_t stride, int64_t T, int64_t E, int score, const float *bias, int64_t groups,

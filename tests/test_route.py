@@ -192,3 +192,37 @@ def test_captured():
         assert torch.equal(out[0], mine[0]) and torch.equal(out[1], mine[1])
         n = T - 9 * i
         assert np.array_equal(host(out[0])[:n], reference(x[:n].double().cpu().numpy(), k, True, host(b), 8, 4, 2)[0])
+
+
+def test_sizes_of_a_launch():
+    """A launch's threads are numbered in 32 bits: four tokens a workgroup of 256 allow 2^26 - 4 tokens, eight all below 2^26.
+    (A size that is taken goes on to the next refusal, of an address.)"""
+    def call(T, E, groups):
+        return L.lib.lowbit_route(0, A, E, T, E, 0, None, groups, groups, 1, 1, 1, 1.0, None, A + 2, A, None)
+
+    for E, groups in ((257, 1), (512, 1), (1024, 64), (64, 64), (256, 64)):
+        for T in (2**26 - 1, 2**26 - 2, 2**26 - 3):
+            assert call(T, E, groups) == L.LB_ESHAPE, (T, E, groups)
+        assert call(2**26 - 4, E, groups) == L.LB_EALIGN
+    for E, groups in ((1, 1), (256, 1), (256, 32)):
+        assert call(2**26 - 1, E, groups) == L.LB_EALIGN and call(2**26, E, groups) == L.LB_ESHAPE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,groups", [(2**26 - 4, 64, 64), (2**26 - 1, 4, 2)])
+def test_the_longest_batches(T, E, groups):
+    """Both numbers of tokens a wave at the largest T, at sampled tokens."""
+    say(f"case route longest T={T} E={E} groups={groups}")
+    rng = np.random.default_rng(E)
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 4, 1023, T // 3, T - 9, T - 2, T - 1]
+    rows = torch.from_numpy(rng.standard_normal((len(at), E))).to(torch.bfloat16)
+    x[at] = rows.cuda()
+    experts, weights = torch.full((T + 1, 2), -7, dtype=torch.int32, device="cuda"), torch.full((T + 1, 2), -7.0, device="cuda")
+    L.lowbit_route(L.BF16, x, T, E, 2, experts, weights, groups=groups, groups_kept=groups)
+    we, ww = reference(rows.double().numpy(), 2)
+    assert np.array_equal(host(experts[at]), we) and (np.abs(host(weights[at]) - ww) <= ww * 2.0**-24 * (1 + 1e-6)).all()
+    assert (experts[T] == -7).all() and (weights[T] == -7).all()
+    # all other tokens' logits are equal: the first two experts, half of the weight each
+    assert int((experts[:T] != torch.tensor([0, 1], dtype=torch.int32, device="cuda")).any(1).sum()) <= len(at)
+    assert int((weights[:T] != 0.5).any(1).sum()) <= len(at)
