@@ -436,3 +436,21 @@ def test_on_another_stream_and_two_at_once():
         go(n, e, q, s, plan, z, None)
         torch.cuda.synchronize()
         assert torch.equal(y, z)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
+@pytest.mark.parametrize("E,N,K,n,per,rows", [(128, 70, 256, 5000, 4, 16), (20, 130, 384, 9000, 1, 128)])
+def test_products_on_a_plan_with_gaps(fmt, E, N, K, n, per, rows):
+    """Past 4096 pairs an expert's tiles begin at a number that the pairs before it give, with tiles without rows between:
+    both sizes of tile on such a table, with experts that have no pair, and all pairs of one expert."""
+    say(f"case a plan with gaps {W.NAMES[fmt]} E={E} N={N} K={K} pairs={n} per={per}")
+    layer = Layer(fmt, E, N, K)
+    e = some_pairs(np.random.default_rng(n), n, E)
+    e[np.isin(e, [1, E // 2, E - 1])] = 0
+    for which in (e, np.full(n, E - 1, np.int32)):
+        plan = planned(which, E)
+        p, tiles = host(plan).view(np.int32), n // rows + E
+        assert len(p) == -(-(4 + (2 * tiles + 3) // 4 * 4 + tiles * rows) // 4) * 4  # the size for tiles of so many rows
+        assert (p[4:4 + 2 * p[0]].reshape(-1, 2)[:, 1] == 0).any()
+        layer.check(which, per, plan)
