@@ -454,3 +454,29 @@ def test_products_on_a_plan_with_gaps(fmt, E, N, K, n, per, rows):
         assert len(p) == -(-(4 + (2 * tiles + 3) // 4 * 4 + tiles * rows) // 4) * 4  # the size for tiles of so many rows
         assert (p[4:4 + 2 * p[0]].reshape(-1, 2)[:, 1] == 0).any()
         layer.check(which, per, plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS, ids=W.NAMES.get)
+@pytest.mark.parametrize("pairs,rows", [(30, 16), (300, 128)])
+@pytest.mark.parametrize("place", [-1, None, 2**31 - 1, -2**31])
+def test_pairs_past_the_end_count_as_the_last(fmt, pairs, rows, place):
+    """Tiles of an expert that is there, whose pairs are not (`place`; None: the number of pairs, the first past the end):
+    rows of x and y are those of the last pair, and nothing else is read or written."""
+    say(f"case pairs past the end {W.NAMES[fmt]} {pairs} pairs, {rows} rows a tile, place {place}")
+    E, N, K = 4, 40, 256
+    layer, tiles = Layer(fmt, E, N, K), pairs // rows + E
+    plan = np.zeros(L.lowbit_experts_plan_bytes(pairs, E) // 4, np.int32)
+    at = 4 + (2 * tiles + 3) // 4 * 4
+    assert len(plan) == -(-(at + tiles * rows) // 4) * 4  # the size for tiles of so many rows
+    q, s = W.random_rows(np.random.default_rng(0), pairs, K)
+    want, mags = W.product(fmt, layer.w[2], layer.d[2], q[-1:], s[-1:])
+    for used in (1, 5, rows - 1, rows):  # in the forms for few and for many rows
+        plan[0], plan[1], plan[4:at] = tiles, tiles * used, np.resize(np.int32([2, used]), at - 4)
+        plan[at:] = pairs if place is None else place
+        y = torch.full((pairs + 2, N), 7.0, device="cuda")
+        L.lowbit_experts_matmul(fmt, layer.packed, E, N, K, dev(q), dev(s), None, pairs, 1, y[1:-1], plan=dev(plan))
+        got = host(y)
+        assert (np.abs(got[pairs] - want[0]) <= W.allowance(mags[0], K)).all()
+        got[pairs] = 7
+        assert (got == 7).all()
