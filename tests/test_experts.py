@@ -480,3 +480,32 @@ def test_pairs_past_the_end_count_as_the_last(fmt, pairs, rows, place):
         assert (np.abs(got[pairs] - want[0]) <= W.allowance(mags[0], K)).all()
         got[pairs] = 7
         assert (got == 7).all()
+
+
+@pytest.mark.gpu
+def test_outputs_of_16_row_tiles_past_32_bits():
+    """Rows past 2^32 outputs, from a full tile and from one of few rows, at sampled places."""
+    fmt, E, K, pairs, N = L.Q1_0, 3, 128, 150, 31_000_000
+    say(f"case outputs of 16-row tiles past 32 bits {pairs} x {N}")
+    tiles = pairs // 16 + E
+    assert L.lowbit_experts_plan_bytes(pairs, E) == -(-4 * (4 + (2 * tiles + 3) // 4 * 4 + 16 * tiles) // 16) * 16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randint(0, 256, (E, L.lowbit_experts_weight_bytes(fmt, 1, N, K)), dtype=torch.uint8, generator=g, device="cuda")
+    w[:, 16 * N:18 * N] = (torch.rand(E, N, generator=g, device="cuda") * 0.02 + 0.005).half().view(torch.uint8)
+    q, s = W.random_rows(np.random.default_rng(0), pairs, K)
+    e = (np.arange(pairs) % E).astype(np.int32)  # 50 pairs each: three tiles of 16, the last two in one of their own
+    y = torch.full((pairs * N + 64,), 7.0, device="cuda")
+    L.lowbit_experts_matmul(fmt, w.view(-1), E, N, K, dev(q), dev(s), dev(e), pairs, 1, y, plan=planned(e, E))
+    assert (y[pairs * N:] == 7).all()
+    at_n = [0, 63, 64, N // 3, N - 1]
+    assert 143 * N > 2**32
+    for p in (0, 2, 75, 143, 144, 149):
+        got = y[p * N:(p + 1) * N][at_n].cpu().numpy()
+        x = w[e[p]]
+        rec = np.stack([x[16 * n:16 * n + 16].cpu().numpy() for n in at_n])
+        d = np.stack([x[16 * N + 2 * n:16 * N + 2 * n + 2].cpu().numpy().view(np.float16) for n in at_n])
+        i = np.arange(128)
+        bit = 32 * (i % 32 // 8) + 4 * (i % 8) + i // 32
+        signs = 2 * (rec[:, bit // 8] >> (bit % 8) & 1).astype(np.int64) - 1
+        want, mags = W.product(fmt, signs, d, q[p:p + 1], s[p:p + 1])
+        assert (np.abs(got - want[0]) <= W.allowance(mags[0], K)).all(), p
