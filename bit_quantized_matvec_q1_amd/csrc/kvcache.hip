@@ -25,18 +25,13 @@ template <int DT, int D> __global__ __launch_bounds__(256) void append_kernel(Ro
     Slot s = {nullptr, 0};
     if (t < a.T)
         s = slot_of(a, t, head, shift);
-    float xk[8] = {}, xv[8] = {};
-    if (s.rec) {
-        auto load = [&](const void *p, int64_t stride, float (&x)[8]) {
-            const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(static_cast<const typename R::T *>(p) + t * stride + (int64_t)head * D + 8 * at);
+    auto load = [&](const void *p, int64_t stride, float (&x)[8]) {
+        const RowVec<DT, 8> v = *reinterpret_cast<const RowVec<DT, 8> *>(static_cast<const typename R::T *>(p) + t * stride + (int64_t)head * D + 8 * at);
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                x[i] = R::get(v.v[i]);
-        };
-        load(a.k, a.k_stride, xk);
-        load(a.v, a.v_stride, xv);
-    }
-    write_row<DT, D>(s, shift, xk, xv, lds);
+        for (int i = 0; i < 8; i++)
+            x[i] = R::get(v.v[i]);
+    };
+    write_row<DT, D>(s, shift, [&](float (&xk)[8], float (&xv)[8]) { load(a.k, a.k_stride, xk), load(a.v, a.v_stride, xv); }, lds);
 }
 
 // A lane gives 8 consecutive elements of a row's key and of its value; a row without a slot is zeros.

@@ -190,7 +190,12 @@ template <int DT, int D, int H> __global__ __launch_bounds__(256) void rotary_ke
             for (int j = 0; j < 8; j++)
                 xk[j] = R::get(w[j]);
         }
-        write_row<DT, D>(slot_of(a.cache, a.pages, a.kv_heads, D, slot, h, shift), shift, xk, xv, lds);
+        auto values = [&](float (&wk)[8], float (&wv)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                wk[j] = xk[j], wv[j] = xv[j];
+        };
+        write_row<DT, D>(slot_of(a.cache, a.pages, a.kv_heads, D, slot, h, shift), shift, values, lds);
     }
 }
 
