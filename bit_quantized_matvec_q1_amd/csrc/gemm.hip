@@ -254,10 +254,13 @@ __device__ __forceinline__ void issue_x(uint32_t *lds_tile, const int8_t *__rest
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         uint32_t *dst = lds_tile + 4 * (128 * wave + 64 * u); // the wave's 64 slots
-        uint32_t at = o.x[u] + (uint32_t)kk;
-        if (halves(FMT)) // chunks 4 to 7 are those of the lanes whose bit 2 differs from u
-            at -= half_step ? (uint32_t)((lane << 4) & 64) ^ (64u * u) : 0u;
-        __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + at), (lvoid *)dst, 16, 0, 0);
+        uint32_t at = o.x[u];
+        // Chunks 4 to 7 are those of the lanes whose bit 2 differs from u.  (The step stays in the scalar base: added to the lanes'
+        // offsets, with a select of the whole term, 8 x 12288 x 4096 planar took 15.7 us instead of 15.0, its block sums of 64 rows
+        // of 4096 x 4096 18.6 instead of 17.5.)
+        if (halves(FMT))
+            at -= ((uint32_t)(lane << 4) ^ (64u * u)) & (half_step ? 64u : 0u);
+        __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + (uint32_t)kk + at), (lvoid *)dst, 16, 0, 0);
     }
 }
 
