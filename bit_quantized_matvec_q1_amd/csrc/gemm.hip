@@ -247,20 +247,23 @@ __device__ __forceinline__ void load_step(StepRegs &r, const LaneOffs &o, const 
 // belongs there.  On the half step the lanes of the chunks past K load the first half's again (their weights are zeros).
 __device__ __forceinline__ int x_slot(int r, int c) { return r * XCH + (c ^ ((r >> 1) & 7)); }
 
-template <int FMT>
+template <int FMT, bool EMIT>
 __device__ __forceinline__ void issue_x(uint32_t *lds_tile, const int8_t *__restrict__ X, const LaneOffs &o, int kk,
                                        bool half_step, int wave, int lane)
 {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         uint32_t *dst = lds_tile + 4 * (128 * wave + 64 * u); // the wave's 64 slots
-        uint32_t at = o.x[u];
-        // Chunks 4 to 7 are those of the lanes whose bit 2 differs from u.  (The step stays in the scalar base: added to the lanes'
-        // offsets, with a select of the whole term, 8 x 12288 x 4096 planar took 15.7 us instead of 15.0, its block sums of 64 rows
-        // of 4096 x 4096 18.6 instead of 17.5.)
-        if (halves(FMT))
-            at -= ((uint32_t)(lane << 4) ^ (64u * u)) & (half_step ? 64u : 0u);
-        __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + (uint32_t)kk + at), (lvoid *)dst, 16, 0, 0);
+        // (chunks 4 to 7 are those of the lanes whose bit 2 differs from u)
+        if constexpr (EMIT && FMT == LB_TERNARY_PLANAR) { // with the step in a scalar base: 64 rows of 4096 x 4096 18.6 -> 17.5 us
+            const uint32_t at = o.x[u] - (((uint32_t)(lane << 4) ^ (64u * u)) & (half_step ? 64u : 0u));
+            __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + (uint32_t)kk + at), (lvoid *)dst, 16, 0, 0);
+        } else { // (a base costs most others a register too many: 24576 pairs of 64 Q1_0 experts of 2816 x 2048 463 -> 473 us)
+            uint32_t at = o.x[u] + (uint32_t)kk;
+            if (halves(FMT))
+                at -= half_step ? (uint32_t)((lane << 4) & 64) ^ (64u * u) : 0u;
+            __builtin_amdgcn_global_load_lds((gvoid *)((const gu8 *)X + at), (lvoid *)dst, 16, 0, 0);
+        }
     }
 }
 
@@ -541,7 +544,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     StepRegs ring;
     int kk = kfirst;
     load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kk, K - kk < KS, tid, m0, M, K);
-    issue_x<FMT>(xt0[half], X, lo, kk, K - kk < KS, wave, lane);
+    issue_x<FMT, EMIT>(xt0[half], X, lo, kk, K - kk < KS, wave, lane);
 
     for (int j0 = 0; j0 < nsh; j0 += 2)
 #pragma unroll
@@ -562,7 +565,7 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
         kn = kn >= kend ? kn - kend : kn;
         kn = kn >= kend ? kn - kend : kn;
         load_step<FMT, GROUPED>(ring, lo, W, wsc, xsc, kn, K - kn < KS, tid, m0, M, K);
-        issue_x<FMT>(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
+        issue_x<FMT, EMIT>(q ? xt0[half] : xt1[half], X, lo, kn, K - kn < KS, wave, lane);
         if (active && some)
             step_compute<FMT, EMIT, 4, KSPLIT>(lds[half], q, q ? xt1[half] : xt0[half], xb, h, l32, wn, wm, m0, n0, M, N, nab,
                                        kk, acc, iacc, cbias, sums);
