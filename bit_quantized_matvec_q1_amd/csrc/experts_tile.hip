@@ -24,10 +24,12 @@
 // Measured (us, the first way against the second alone): 64 experts of 1536 x 2048 with half a pair each Q1_0 7.7 and 12.0,
 // Q2_0 8.5 and 14.4, Q4_0 12.1 and 15.4; 360 pairs of 128 experts of 2048 x 768 14.6 and 16.4, 14.6 and 18.4, 22.7 and 24.9 (107
 // MB of Q4_0: 4.7 TB/s, bound by loads; two runs of weight rows a workgroup, which starts half as often, take 5 to 50 %
-// longer, one group a wave up to 30).  With many rows the vector unit bounds it (12 to 14 instructions for eight weights of a
-// lane and 16 rows, eight of them the rescale).  Two things made that: each row's scales staged through LDS by whole lines
-// (read four at a time from memory, their lines came through the caches again for every step, Q4_0 875 -> 577 us for 32768
-// pairs), and results in vector registers.
+// longer, one group a wave up to 30).  Of Q1_0 and Q2_0, 27 and 54 MB there, it is not the bytes: the vector unit is 58 and 49 %
+// busy, and the time grows with the columns (768 to 4608 of them: 15 to 66 us, 14 to 76), so it is their unpacking and their
+// activations' way through LDS, and not a workgroup's start.  With many rows the vector unit bounds it (12 to 14 instructions
+// for eight weights of a lane and 16 rows, eight of them the rescale).  Two things made that: each row's scales staged through
+// LDS by whole lines (read four at a time from memory, their lines came through the caches again for every step, Q4_0 875 ->
+// 577 us for 32768 pairs), and results in vector registers.
 #include "matvec_tile.h"
 #include "serve_internal.h"
 

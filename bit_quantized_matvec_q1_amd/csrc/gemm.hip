@@ -29,7 +29,8 @@
 //  * The experts' products (GROUPED) are the same tiles with other rows: a tile is up to TM pairs of one expert, from the
 //    plan of experts.hip, whose activation rows are gathered and whose output rows are scattered by the pairs' numbers.
 //    24576 pairs of 64 Q1_0 experts of 2816 x 2048: 470 to 530 us, 536 to 605 TOPS (places without a pair not counted), the vector
-//    unit some three quarters busy, two thirds of it the rescale.
+//    unit 91 % busy, two thirds of it the rescale.  Tiles that are partly filled keep a whole one's loads, unpacking and barriers,
+//    while the waves of rows that are not there idle: 4000 pairs of 32 Q2_0 experts of 2560 x 1408 70 us, 79 % busy.
 //  * Planar weights have no block scales: the MFMA accumulates int32 over the whole row and the two
 //    per-row / per-tensor scales are applied once at the end.
 #include "serve_internal.h"
@@ -476,8 +477,8 @@ __global__ __launch_bounds__(GT * KSPLIT, EMIT ? 2 * KSPLIT : 4) void gemm_kerne
     // this wave's 32 x 32 output tile inside the 64 x 128 workgroup tile
     const int wn = wave & 1, wm = wave >> 1;
     // Weight tiles vary fastest, in the order of the workgroups, which go round the eight XCDs.  Activations that an XCD's L2 (4
-    // MiB) does not hold come from behind it for nearly every workgroup then (512 x 4096 x 12288: 374 MB fetched, for 35 MB),
-    // so there each XCD has a run of tiles instead, of few activation rows.  Measured, Q1_0, Q2_0 and Q4_0: 512 x 4096 x 12288
+    // MiB) does not hold come from behind it for nearly every workgroup then (512 x 4096 x 12288, Q4_0: 374 MB fetched, for
+    // 35 MB), so there each XCD has a run of tiles instead, of few activation rows (137 MB).  Measured, Q1_0, Q2_0 and Q4_0: 512 x 4096 x 12288
     // 86.6 -> 78.6 us, 92.0 -> 84.7, 91 -> 88, 8192 x 4096 x 4096 373 -> 357 and 399 -> 384; below that size 512 x 12288 x 4096
     // (2 MB) 76.1 -> 77.7 and 79.5 -> 82.4.  Grouped tiles stay in order: those without rows are the last ones.
     int id = blockIdx.x;
@@ -708,7 +709,8 @@ hipError_t launch_gemm(int fmt, const uint8_t *W, int64_t N, int64_t K, float w_
 {
     const bool emit = sums != nullptr;
     // Few rows, or few weight rows: tiles of 16 rows (experts_tile.hip), as one expert's.  Measured: 2 rows of 4096 x 4096
-    // 5.6 us so and 29 here, 128 22 and 30; 64 of 12288 x 4096 29 and 31, 96 42 and 32; 192 of 4096 x 12288 76 and 82.
+    // 5.6 us so and 29 here, 128 22 and 30; 64 of 12288 x 4096 29 and 31, 96 42 and 32; 192 of 4096 x 12288 76 and 82.  (The formats
+    // that were here before keep these tiles for every M, and with them their sums' order and their results' bits.)
     if (fmt == LB_Q4_0 && !emit && (M + 15) / 16 * ((N + 63) / 64) <= 768) {
         ExpertsArgs a = {};
         a.W = W, a.E = 1, a.N = (int32_t)N, a.K = (int32_t)K, a.pairs = (int32_t)M, a.per_row = 1, a.max_tiles = (M + 15) / 16;

@@ -11,9 +11,10 @@
 // those that have it.  What it takes is instructions, and nearly as many for 32 lanes as for 64: so long batches put two
 // tokens in a wave, and short ones, where a single token's time counts, one.
 //
-// Measured: 8191 bf16 tokens of 256 experts in 8 groups, 8 chosen: 14 to 15 us (4.2 MB in: the vector unit's instructions
-// bound it); one fp32 token of 64 experts 3 us, a launch.  With the library's exponential and a token a wave the
-// first took 18 us.
+// Measured: 8191 bf16 tokens of 256 experts in 8 groups, 8 chosen: 13 to 15 us (4.2 MB in).  That is one round of four waves a
+// SIMD with 1572 vector instructions each, which keep the vector unit busy for 75 % of the kernel; the rest is its start, the
+// logits' way in, and where the four waves wait in their chains of reductions at once.  One fp32 token of 64 experts 3 us, a
+// launch.  With the library's exponential and a token a wave the first took 18 us.
 #include "serve_internal.h"
 
 namespace lb {
